@@ -12,20 +12,28 @@
 #include <new>
 
 #include "fd.h"
+#include "fd_api.h"
 #include "fd_internal.h"
 #include "fd_launch.h"
 
-struct fd_workspace {
-    void *base;
-    size_t bytes;
-    int64_t max_segments;
-    int32_t max_rows, head_dim, max_ctas;
-    int32_t *counters;
-    int32_t *status;
-    float *partials;
-    size_t partial_floats;
-    int device;
-};
+namespace fd {
+
+int sm_count_current() {
+    static std::mutex mu;
+    static int cached[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lk(mu);
+    if (cached[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return 0;
+        cached[dev] = n;
+    }
+    return cached[dev];
+}
+
+}  // namespace fd
 
 namespace {
 
@@ -51,40 +59,10 @@ WsLayout ws_layout(int64_t max_segments, int32_t max_rows, int32_t head_dim,
     return L;
 }
 
-int sm_count_current() {
-    static std::mutex mu;
-    static int cached[64] = {0};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    std::lock_guard<std::mutex> lk(mu);
-    if (cached[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return 0;
-        cached[dev] = n;
-    }
-    return cached[dev];
-}
-
-int esize(int32_t dt) {
-    switch (dt) {
-        case FD_BF16: return 2;
-        case FD_F32: return 4;
-        case FD_I8: return 1;
-        case FD_I32: return 4;
-        default: return 0;
-    }
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Basic structural check of a tensor descriptor.
-int check_tensor(const fd_tensor *t, int ndim) {
-    if (!t || !t->data || t->ndim != ndim || esize(t->dtype) == 0) return FD_ERR_ARG;
-    for (int i = 0; i < ndim; ++i)
-        if (t->shape[i] < 0 || t->stride[i] < 0) return FD_ERR_ARG;
-    return FD_OK;
-}
+using fd::aligned16;
+using fd::check_tensor;
+using fd::esize;
+using fd::sm_count_current;
 
 int kernel_tile(int32_t kernel) {
     return kernel == FD_KERNEL_TC ? fd::tc_tile_tokens() : fd::simt_tile_tokens();

@@ -1,0 +1,62 @@
+// fd_fp4_launch.h -- launch parameters of the 4-bit cache kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "fd_internal.h"
+
+namespace fd {
+
+// Decode over a 4-bit cache (fd_fp4_decode.cu).  `p` describes the launch to
+// the split partitioner: p.k / p.v are the code caches (strides in bytes), a
+// segment is (sequence, kv head, part of the kv head's query rows), p.Hkv
+// counts (kv head, part) pairs and p.rows the rows of a part.
+struct Fp4Params {
+    Params p;
+    const uint8_t *ks; int64_t kss[3];   // e4m3 scales, strides in bytes
+    const uint8_t *vs; int64_t vss[3];
+    float v_global;
+    int32_t parts;       // parts of each kv head's query rows
+    int32_t all_rows;    // g * n_q
+};
+// Rows that one part holds at most for this head_dim.
+int fp4_max_rows(int d);
+// Cache positions per tile of the partitioner.
+int fp4_tile_tokens(int d);
+// Blocks per SM of the kernel for this part size.
+int fp4_blocks_per_sm(int d, int rows);
+int launch_fp4_decode(const Fp4Params &p, int num_ctas, cudaStream_t stream);
+
+// The rows of a 4-bit cache between bf16 (or fp32) and its own format
+// (fd_fp4_rows.cu).  Cache strides in bytes: [sequence or page, kv head, row].
+struct Fp4Rows {
+    int32_t B, n, Hkv, d;
+    int64_t cap;
+    uint8_t *k, *v, *ks, *vs;
+    int64_t kst[3], vst[3], kss[3], vss[3];
+    float k_global, v_global;
+    const int32_t *block_table;   // null: flat
+    int32_t page_size, page_shift, max_pages;
+    int64_t num_pages;
+    const int32_t *lengths;       // append: filled positions; read: positions that exist
+    int32_t *status;
+    // append: new rows [B, n, Hkv, d] bf16 (strides in elements), how many of
+    // them each sequence really has (null: n), and where the new lengths go
+    // (null: nowhere)
+    const uint16_t *k_new, *v_new;
+    int64_t kns[3], vns[3];
+    const int32_t *new_lengths;
+    int32_t *lengths_out;
+    int32_t *grid;                // non-null: lengths_out overlaps lengths, so the
+                                  // last block to finish writes it
+    // read: first position of each sequence (null: 0) and [B, n, Hkv, d]
+    // outputs, bf16 or fp32 (strides in elements)
+    const int32_t *start;
+    void *k_out, *v_out;
+    int64_t kos[3], vos[3];
+    int32_t out_f32;
+};
+int launch_fp4_append(const Fp4Rows &p, cudaStream_t stream);
+int launch_fp4_read(const Fp4Rows &p, cudaStream_t stream);
+
+}  // namespace fd

@@ -8,10 +8,13 @@ every call raises.
 Low-level names mirror the C ABI (``fd_decode``, ``fd_decode_int8``,
 ``fd_decode_append``, ``fd_decode_paged``, ``fd_decode_masked``,
 ``fd_decode_gather``, ``fd_decode_gather_int8``, ``fd_decode_gather_bias``,
-``fd_topk_blocks``,
+``fd_topk_blocks``, ``fd_decode_fp4``, ``fd_append_fp4``, ``fd_read_fp4``,
+``fd_pages_reserve`` / ``_fork`` / ``_free`` / ``_compact`` / ``_copy``,
 ``fd_workspace_create`` ...) and take ``FdTensor`` / ``FdOpts`` structures;
 ``decode``, ``decode_int8``, ``decode_append``, ``decode_paged``,
-``decode_masked``, ``decode_gather`` and ``topk_blocks`` take
+``decode_masked``, ``decode_gather``, ``topk_blocks``, ``decode_fp4``,
+``append_fp4``, ``read_fp4``, ``pages_reserve``, ``pages_fork``,
+``pages_free``, ``pages_compact`` and ``pages_copy`` take
 torch tensors, allocate ``out`` with torch when it is not given, and keep one
 workspace per (device, stream).
 """
@@ -20,6 +23,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -31,13 +35,13 @@ LIB_PATH = os.path.join(_HERE, "libfd.so")
 # constants from include/fd.h
 FD_OK, FD_ERR_ARG, FD_ERR_UNSUPPORTED, FD_ERR_ALIGN, FD_ERR_WORKSPACE, FD_ERR_CUDA = 0, -1, -2, -3, -4, -5
 FD_ERR_SCRATCH = -6
-FD_BF16, FD_F32, FD_I8, FD_I32 = 0, 1, 2, 3
-FD_DEV_BAD_LENGTH, FD_DEV_BAD_INDEX, FD_DEV_INTERNAL = 1, 2, 4
+FD_BF16, FD_F32, FD_I8, FD_I32, FD_U8, FD_E4M3 = 0, 1, 2, 3, 4, 5
+FD_DEV_BAD_LENGTH, FD_DEV_BAD_INDEX, FD_DEV_INTERNAL, FD_DEV_NO_PAGES = 1, 2, 4, 8
 FD_KERNEL_AUTO, FD_KERNEL_SIMT, FD_KERNEL_TC = 0, 1, 2
 FD_MAX_ROWS = 64
 
 _DTYPES = {torch.bfloat16: FD_BF16, torch.float32: FD_F32, torch.int8: FD_I8,
-           torch.int32: FD_I32}
+           torch.int32: FD_I32, torch.uint8: FD_U8, torch.float8_e4m3fn: FD_E4M3}
 
 
 class FdTensor(ctypes.Structure):
@@ -98,6 +102,37 @@ _SIGNATURES = [
     ("fd_decode_noalloc", ctypes.c_int,
      [_P(FdTensor), _P(FdTensor), _P(FdTensor), ctypes.c_void_p, ctypes.c_int32,
       ctypes.c_int32, ctypes.c_float, _P(FdTensor), ctypes.c_void_p, ctypes.c_int32]),
+    # the 4-bit cache and the page calls take their descriptors as packed
+    # bytes (or any pointer): see _pack
+    ("fd_decode_fp4", ctypes.c_int,
+     [ctypes.c_void_p] * 5 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_int32,
+                              ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                              ctypes.c_void_p, ctypes.c_void_p]),
+    ("fd_append_fp4", ctypes.c_int,
+     [ctypes.c_void_p] * 7 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_int32,
+                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    ("fd_read_fp4", ctypes.c_int,
+     [ctypes.c_void_p] * 4 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_int32]
+     + [ctypes.c_void_p] * 5),
+    ("fd_pages_scratch_bytes", ctypes.c_size_t, [ctypes.c_int64]),
+    ("fd_pages_reserve", ctypes.c_int,
+     [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+      ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+      ctypes.c_void_p, ctypes.c_void_p]),
+    ("fd_pages_fork", ctypes.c_int,
+     [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+      ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+      ctypes.c_int32, ctypes.c_void_p]),
+    ("fd_pages_free", ctypes.c_int,
+     [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+      ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+      ctypes.c_void_p]),
+    ("fd_pages_compact", ctypes.c_int,
+     [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    ("fd_pages_copy", ctypes.c_int,
+     [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+      ctypes.c_void_p]),
     ("fd_workspace_bytes", ctypes.c_size_t,
      [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]),
     ("fd_workspace_create", ctypes.c_int,
@@ -560,3 +595,289 @@ def decode_gather(q, k_cache, v_cache, idx, scale=None, out=None,
                                     ctypes.byref(o))
     _check(rc, "fd_decode_gather")
     return out
+
+
+# ------------------------------------------- 4-bit caches and their pages
+_TENSOR = struct.Struct("Pii4q4q")     # fd_tensor
+_OPTS = struct.Struct("PPiifi2i")      # fd_opts
+_PAD = ((), (0, 0, 0), (0, 0), (0,), ())
+
+
+def _pack(t: torch.Tensor) -> bytes:
+    """fd_tensor of a CUDA tensor, as bytes (a fraction of the time that a
+    ctypes structure takes to fill)."""
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError("unsupported dtype %s" % t.dtype)
+    shape = t.shape
+    n = len(shape)
+    if not 1 <= n <= 4:
+        raise ValueError("1 to 4 dimensions")
+    pad = _PAD[n]
+    return _TENSOR.pack(t.data_ptr(), dt, n, *shape, *pad, *t.stride(), *pad)
+
+
+def _pack_opts(sh, ws, num_ctas=0) -> bytes:
+    return _OPTS.pack(sh, ws.handle.value, num_ctas, FD_KERNEL_AUTO, 0.0, 0, 0, 0)
+
+
+def _on(device, **tensors):
+    """Every tensor given lies on `device`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s must be on %s" % (name, device))
+
+
+def _ints(t, shape, device, name) -> int:
+    """Address of a contiguous int32 tensor of this shape (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous int32 %s tensor on %s" % (name, list(shape), device))
+    return t.data_ptr()
+
+
+def _table(block_table, B, device):
+    if block_table is None:
+        return 0, 0
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be a contiguous int32 [B, max_pages] tensor")
+    max_pages = block_table.shape[1]
+    return _ints(block_table, (B, max_pages), device, "block_table"), max_pages
+
+
+def _workspace(workspace, device, sh, segments=1, rows=1, ctas=1):
+    """The call's workspace: the given one, or the stream's, which has room
+    for 1024 blocks and grows with the segments."""
+    return workspace if workspace is not None else workspace_for(device, sh, segments, rows, 256, ctas)
+
+
+def decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q=None, causal=False,
+               scale=None, k_global=1.0, v_global=1.0, block_table=None, out=None,
+               out_dtype=torch.bfloat16, num_ctas=0, stream=None,
+               workspace: Optional[Workspace] = None):
+    """As ``decode`` over a cache held in 4 bits: k_cache / v_cache
+    [B, Hkv, cap, d/2] (uint8, two e2m1 codes a byte, the even value in the low
+    nibble), k_scale / v_scale [B, Hkv, cap, d/16] (float8_e4m3fn, one per 16
+    values); a value is code * scale * k_global (v_global).  With block_table
+    [B, max_pages] (int32, contiguous) the four are pools
+    [num_pages, Hkv, page_size, ...], as in ``decode_paged``."""
+    B, nq, Hq, d = q.shape
+    device = q.device
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    _on(device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out=out)
+    lens = _ints(kv_lengths, (B,), device, "kv_lengths")
+    table, max_pages = _table(block_table, B, device)
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=device)
+    Hkv = max(k_cache.shape[1], 1)
+    rows = Hq // Hkv * nq
+    sh = _stream_handle(stream, device)
+    # at most a part for every 16 rows
+    ws = _workspace(workspace, device, sh, B * Hkv * ((rows + 15) // 16), min(rows, 32), max(num_ctas, 1))
+    with _on_device(device):
+        rc = lib().fd_decode_fp4(_pack(q), _pack(k_cache), _pack(v_cache), _pack(k_scale),
+                                 _pack(v_scale), k_global, v_global, table, max_pages, lens,
+                                 nq if n_q is None else n_q, bool(causal),
+                                 1.0 / math.sqrt(d) if scale is None else scale, _pack(out),
+                                 _pack_opts(sh, ws, num_ctas))
+    _check(rc, "fd_decode_fp4")
+    return out
+
+
+def append_fp4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, kv_lengths, new_lengths=None,
+               lengths_out=None, k_global=1.0, v_global=1.0, block_table=None, stream=None,
+               workspace: Optional[Workspace] = None):
+    """Quantises new rows k_new / v_new [B, n, Hkv, d] (bf16) into a 4-bit
+    cache (see ``decode_fp4``) at positions kv_lengths[b] .. kv_lengths[b] +
+    new_lengths[b] - 1 (int32 [B]; None: n for every sequence; rows past it
+    are padding).  lengths_out (int32 [B], may be kv_lengths) receives the
+    lengths with the new rows."""
+    B = k_new.shape[0]
+    device = k_new.device
+    if not k_new.is_cuda:
+        raise ValueError("k_new must be a CUDA tensor")
+    _on(device, v_new=v_new, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    lens = _ints(kv_lengths, (B,), device, "kv_lengths")
+    new = _ints(new_lengths, (B,), device, "new_lengths")
+    after = _ints(lengths_out, (B,), device, "lengths_out")
+    table, max_pages = _table(block_table, B, device)
+    sh = _stream_handle(stream, device)
+    ws = _workspace(workspace, device, sh)
+    with _on_device(device):
+        rc = lib().fd_append_fp4(_pack(k_new), _pack(v_new), new, _pack(k_cache), _pack(v_cache),
+                                 _pack(k_scale), _pack(v_scale), k_global, v_global, table,
+                                 max_pages, lens, after, _pack_opts(sh, ws))
+    _check(rc, "fd_append_fp4")
+
+
+def read_fp4(k_cache, v_cache, k_scale, v_scale, kv_lengths, n, start=None, k_global=1.0,
+             v_global=1.0, block_table=None, out=None, out_dtype=torch.bfloat16, stream=None,
+             workspace: Optional[Workspace] = None):
+    """Positions start[b] .. start[b] + n - 1 (int32 [B]; None: from 0) of a
+    4-bit cache (see ``decode_fp4``) as numbers: returns (k, v)
+    [B, n, Hkv, d], zeros at or past kv_lengths[b].  out: such a pair to fill."""
+    B = kv_lengths.shape[0]
+    device = k_cache.device
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache must be a CUDA tensor")
+    if out is None:
+        shape = (B, int(n), k_cache.shape[1], 2 * k_cache.shape[3])
+        out = (torch.empty(shape, dtype=out_dtype, device=device),
+               torch.empty(shape, dtype=out_dtype, device=device))
+    k, v = out
+    _on(device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out=k, out_v=v)
+    if k.dim() != 4 or k.shape[0] != B or k.shape[1] != n:
+        raise ValueError("out must be two [B, n, Hkv, d] tensors")
+    lens = _ints(kv_lengths, (B,), device, "kv_lengths")
+    first = _ints(start, (B,), device, "start")
+    table, max_pages = _table(block_table, B, device)
+    sh = _stream_handle(stream, device)
+    ws = _workspace(workspace, device, sh)
+    with _on_device(device):
+        rc = lib().fd_read_fp4(_pack(k_cache), _pack(v_cache), _pack(k_scale), _pack(v_scale),
+                               k_global, v_global, table, max_pages, first, lens, _pack(k),
+                               _pack(v), _pack_opts(sh, ws))
+    _check(rc, "fd_read_fp4")
+    return k, v
+
+
+def _books(block_table, kv_lengths, refs):
+    """Checked addresses of a paged cache's books: (device, table, B,
+    max_pages, lengths, refs, num_pages)."""
+    device = block_table.device
+    if not block_table.is_cuda or block_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("block_table must be a CUDA [B, max_pages] tensor and refs [num_pages]")
+    B, max_pages = block_table.shape
+    num_pages = refs.shape[0]
+    return (device, _ints(block_table, (B, max_pages), device, "block_table"), B, max_pages,
+            _ints(kv_lengths, (B,), device, "kv_lengths"),
+            _ints(refs, (num_pages,), device, "refs"), num_pages)
+
+
+def _pages_workspace(workspace, device, sh, num_pages):
+    if workspace is not None:
+        return workspace
+    # room for the scratch in slots of the default 16 rows at head_dim 256,
+    # beyond those of its 1024 blocks
+    extra = 3 * num_pages // slot_floats(16, 256) - 1000
+    return workspace_for(device, sh, max(extra, 1), 1, 256, 1)
+
+
+def pages_reserve(block_table, kv_lengths, refs, page_size, n_new, pairs=None, count=None,
+                  stream=None, workspace: Optional[Workspace] = None):
+    """Pages of its own for each sequence's next n_new positions (an int for
+    all of them, or int32 [B]): free pages where block_table [B, max_pages]
+    has none, and pages to copy shared ones into.  Returns (pairs, count):
+    pairs int32 [B, 2] (old, new) pages for ``pages_copy``, count int32 [1] of
+    them, or minus the pages that are missing (nothing is then reserved).
+    refs int32 [num_pages] counts the entries that name each page."""
+    device, table, B, max_pages, lens, counts, num_pages = _books(block_table, kv_lengths, refs)
+    each = 0
+    new = 0
+    if isinstance(n_new, torch.Tensor):
+        new = _ints(n_new, (B,), device, "n_new")
+    else:
+        each = int(n_new)
+    if pairs is None:
+        pairs = torch.empty((B, 2), dtype=torch.int32, device=device)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=device)
+    sh = _stream_handle(stream, device)
+    ws = _pages_workspace(workspace, device, sh, num_pages)
+    with _on_device(device):
+        rc = lib().fd_pages_reserve(table, B, max_pages, lens, new, each, page_size, counts,
+                                    num_pages, _ints(pairs, (B, 2), device, "pairs"),
+                                    _ints(count, (1,), device, "count"), _pack_opts(sh, ws))
+    _check(rc, "fd_pages_reserve")
+    return pairs, count
+
+
+def pages_fork(block_table, kv_lengths, refs, page_size, src, dst, lengths=None, stream=None,
+               workspace: Optional[Workspace] = None):
+    """Row dst[i] of the block table lets go of its pages and shares those of
+    row src[i] (int32 [n]), the first lengths[i] positions of them where
+    lengths is given; kv_lengths[dst[i]] follows."""
+    device, table, B, max_pages, lens, counts, num_pages = _books(block_table, kv_lengths, refs)
+    n = src.shape[0]
+    sh = _stream_handle(stream, device)
+    ws = _workspace(workspace, device, sh)
+    with _on_device(device):
+        rc = lib().fd_pages_fork(table, B, max_pages, lens, page_size, counts, num_pages,
+                                 _ints(src, (n,), device, "src"), _ints(dst, (n,), device, "dst"),
+                                 _ints(lengths, (n,), device, "lengths"), n, _pack_opts(sh, ws))
+    _check(rc, "fd_pages_fork")
+
+
+def pages_free(block_table, kv_lengths, refs, page_size, seqs=None, lengths=None, stream=None,
+               workspace: Optional[Workspace] = None):
+    """Sequences seqs (int32 [n]; None: every one) shrink to lengths (int32
+    [n]; None: 0) where that is less, and let go of the pages past it."""
+    device, table, B, max_pages, lens, counts, num_pages = _books(block_table, kv_lengths, refs)
+    n = B if seqs is None else seqs.shape[0]
+    sh = _stream_handle(stream, device)
+    ws = _workspace(workspace, device, sh)
+    with _on_device(device):
+        rc = lib().fd_pages_free(table, B, max_pages, lens, page_size, counts, num_pages,
+                                 _ints(seqs, (n,), device, "seqs"),
+                                 _ints(lengths, (n,), device, "lengths"), n, _pack_opts(sh, ws))
+    _check(rc, "fd_pages_free")
+
+
+def pages_compact(block_table, refs, pairs=None, count=None, stream=None,
+                  workspace: Optional[Workspace] = None):
+    """Renumbers the pages in use to 0 .. used - 1 in block_table and refs.
+    Returns (pairs, count): int32 [num_pages // 2, 2] (from, to) pages for
+    ``pages_copy`` and int32 [1], how many."""
+    device = block_table.device
+    if not block_table.is_cuda or block_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("block_table must be a CUDA [B, max_pages] tensor and refs [num_pages]")
+    B, max_pages = block_table.shape
+    num_pages = refs.shape[0]
+    half = max(num_pages // 2, 1)
+    if pairs is None:
+        pairs = torch.empty((half, 2), dtype=torch.int32, device=device)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=device)
+    sh = _stream_handle(stream, device)
+    ws = _pages_workspace(workspace, device, sh, num_pages)
+    with _on_device(device):
+        rc = lib().fd_pages_compact(_ints(block_table, (B, max_pages), device, "block_table"), B,
+                                    max_pages, _ints(refs, (num_pages,), device, "refs"),
+                                    num_pages, _ints(pairs, (half, 2), device, "pairs"),
+                                    _ints(count, (1,), device, "count"), _pack_opts(sh, ws))
+    _check(rc, "fd_pages_compact")
+    return pairs, count
+
+
+class PagePools:
+    """The pools of a paged cache ([num_pages, ...] CUDA tensors of any dtype:
+    codes, scales, of K and V, of every layer) as ``pages_copy`` wants them;
+    made once, kept with the pools, whose memory it holds on to."""
+
+    def __init__(self, pools):
+        self.pools = list(pools)
+        if not self.pools:
+            raise ValueError("no pools")
+        self.device = self.pools[0].device
+        for t in self.pools:
+            if not t.is_cuda or t.device != self.device:
+                raise ValueError("pools must be CUDA tensors on one device")
+        self.packed = b"".join(_pack(t) for t in self.pools)
+
+
+def pages_copy(pools, pairs, count, stream=None, workspace: Optional[Workspace] = None):
+    """Copies pages pairs[i] = (from, to) in every pool (a ``PagePools``, or
+    up to 256 tensors) for i < count, both as ``pages_reserve`` and
+    ``pages_compact`` return them."""
+    if not isinstance(pools, PagePools):
+        pools = PagePools(pools)
+    device = pools.device
+    n = pairs.shape[0]
+    sh = _stream_handle(stream, device)
+    ws = _workspace(workspace, device, sh)
+    with _on_device(device):
+        rc = lib().fd_pages_copy(pools.packed, len(pools.pools), _ints(pairs, (n, 2), device, "pairs"),
+                                 _ints(count, (1,), device, "count"), n, _pack_opts(sh, ws))
+    _check(rc, "fd_pages_copy")

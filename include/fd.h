@@ -26,6 +26,10 @@
  *     QSA decode", llama.cpp #28213: per-token lists for multi-row verify);
  *     fd_decode_gather_bias adds a bias per list entry, and fd_topk_blocks
  *     builds the lists from block scores.
+ *   - fd_decode_fp4: the dense prefix over a cache held in 4 bits, flat or
+ *     paged; fd_append_fp4 writes such a cache and fd_read_fp4 reads rows of
+ *     it back.
+ *   - fd_pages_*: who holds which page of a paged cache, and copies of pages.
  * The prefix is split across thread blocks and the last block to finish a
  * (sequence, kv head) combines the splits inside the same launch
  * (comfy-kitchen #239, "GQA decode"); the query heads of one GQA group share
@@ -82,12 +86,16 @@ extern "C" {
 #define FD_F32 1
 #define FD_I8 2
 #define FD_I32 3
+#define FD_U8 4                  /* bytes; two e2m1 codes each in a 4-bit cache */
+#define FD_E4M3 5                /* 8-bit floats, the scales of a 4-bit cache  */
 
 /* sticky device status bits (fd_get_device_status) */
 #define FD_DEV_BAD_LENGTH 1      /* some kv_lengths[b] outside [0, cap]    */
 #define FD_DEV_BAD_INDEX 2       /* some idx entry >= cap (skipped)        */
 #define FD_DEV_INTERNAL 4        /* a bounded internal wait gave up; the
                                     call's output is not valid              */
+#define FD_DEV_NO_PAGES 8        /* fd_pages_reserve: fewer free pages than
+                                    wanted; nothing was reserved            */
 
 /* kernel selection (fd_opts.kernel); AUTO takes the tensor-core kernel for
  * the calls it serves when q's base pointer and strides are 16-byte aligned
@@ -372,6 +380,154 @@ int fd_decode_noalloc(const fd_tensor *q, const fd_tensor *k_cache,
                       const fd_tensor *v_cache, const int32_t *kv_lengths,
                       int32_t n_q, int32_t causal, float scale,
                       const fd_tensor *out, void *stream, int32_t num_ctas);
+
+/*
+ * A cache held in 4 bits.  A row of d values (one position of one kv head) is
+ * d/2 bytes of e2m1 codes (sign, two exponent bits, one mantissa bit: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives), value 2j in the low nibble of byte
+ * j and value 2j+1 in its high nibble, and d/16 e4m3 scales, one for each 16
+ * consecutive values.  Value x stands for code * scale * global, with one
+ * fp32 factor per call for K and one for V (1 where the scales' own range,
+ * 2^-9 .. 448, is enough).  These arguments are the same in the three calls
+ * below:
+ *   k_cache, v_cache: FD_U8 [B, Hkv, cap, d/2], or with a block_table pools
+ *     [num_pages, Hkv, page_size, d/2]; both of one shape; 16-byte aligned
+ *     base, strides that are multiples of 16 bytes, innermost stride 1.
+ *   k_scale, v_scale: FD_E4M3 [.., .., .., d/16], as the caches; base and
+ *     strides multiples of d/16 bytes.
+ *   k_global, v_global: finite, 2^-64 .. 2^64.
+ *   block_table: NULL for flat caches, else device int32 [B, max_pages],
+ *     contiguous, as in fd_decode_paged; max_pages is 0 for flat caches.
+ *   d is 128 or 256.
+ */
+
+/*
+ * Dense prefix decode over a 4-bit cache: the visible set, causal window and
+ * output of fd_decode (flat) or fd_decode_paged.  Up to 64 rows
+ * ((Hq / Hkv) * n_q) share a kv head; above 32 (d = 128) or 16 (d = 256) the
+ * rows are served in the fewest equal parts, each of which reads the prefix
+ * and needs a segment of the workspace: B * Hkv * parts of them.
+ * The scores and all sums are fp32 over exact products of the codes, the
+ * scales and q (an entry of q below 2^-14 of its row's largest is rounded to
+ * 2^-24 of that); each softmax weight is rounded to fp16, i.e. by up to
+ * 2^-12 of itself or 2^-29 of the row's largest weight.  Positions below the
+ * length must hold numbers: a NaN scale (fd_append_fp4 writes one for a row
+ * that is not finite) reaches every query row of its kv head, those that the
+ * causal window hides it from too.  Positions at or past the length and pages
+ * past it are never read.  opts->kernel must be FD_KERNEL_AUTO.
+ */
+int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_cache,
+                  const fd_tensor *k_scale, const fd_tensor *v_scale, float k_global,
+                  float v_global, const int32_t *block_table, int32_t max_pages,
+                  const int32_t *kv_lengths, int32_t n_q, int32_t causal, float scale,
+                  const fd_tensor *out, const fd_opts *opts);
+/*
+ * Writes new rows into a 4-bit cache.  For sequence b with base_b =
+ * kv_lengths[b] (clamped to [0, cap]), row i of k_new / v_new
+ * [B, n, Hkv, d] (bf16; 16-byte aligned base and strides, innermost stride
+ * 1) goes to position base_b + i, for i below new_lengths[b] (device int32[B],
+ * clamped to [0, n]; NULL: n).  Rows past that are padding and are not read;
+ * positions at or past cap are not written.
+ *   16 values x share s = e4m3(max|x| / (6 * global)), rounded to nearest even
+ *   and at most 448; their codes are e2m1(x / (s * global)), to nearest, ties
+ *   to the even code, at most 6 (with the quotient's sign; s = 0 gives zero
+ *   codes).  Where one of them is a NaN or an infinity the scale is NaN and
+ *   the codes are 0.
+ *   lengths_out: device int32[B], gets min(base_b + new_b, cap); may be
+ *   kv_lengths itself (but overlap it in no other way), or NULL.
+ * FD_DEV_BAD_LENGTH is set where a length, a new length or base_b + new_b is
+ * out of range, FD_DEV_BAD_INDEX where a page's table entry names no page
+ * (its rows are not written).  A page must not be reached through two
+ * sequences' write ranges (fd_pages_reserve sees to that).  opts supplies the
+ * stream and the workspace's status word; opts->kernel must be
+ * FD_KERNEL_AUTO, and opts->num_ctas is not used.
+ */
+int fd_append_fp4(const fd_tensor *k_new, const fd_tensor *v_new, const int32_t *new_lengths,
+                  const fd_tensor *k_cache, const fd_tensor *v_cache, const fd_tensor *k_scale,
+                  const fd_tensor *v_scale, float k_global, float v_global,
+                  const int32_t *block_table, int32_t max_pages, const int32_t *kv_lengths,
+                  int32_t *lengths_out, const fd_opts *opts);
+/*
+ * Reads rows of a 4-bit cache: k_out / v_out [B, n, Hkv, d] (both bf16 or both
+ * fp32; 16-byte aligned base and strides, innermost stride 1) get positions
+ * start_b .. start_b + n - 1 of every sequence (start: device int32[B], or
+ * NULL for 0), and zeros for positions below 0, at or past kv_lengths[b]
+ * (clamped to [0, cap]) or on a page whose table entry names none
+ * (FD_DEV_BAD_INDEX).  A value is code * scale, exactly, times global in
+ * fp32, rounded to the output's type.  opts as in fd_append_fp4.
+ */
+int fd_read_fp4(const fd_tensor *k_cache, const fd_tensor *v_cache, const fd_tensor *k_scale,
+                const fd_tensor *v_scale, float k_global, float v_global,
+                const int32_t *block_table, int32_t max_pages, const int32_t *start,
+                const int32_t *kv_lengths, const fd_tensor *k_out, const fd_tensor *v_out,
+                const fd_opts *opts);
+
+/*
+ * Pages of a paged cache, shared between sequences by reference counts.  The
+ * books are caller-owned device memory:
+ *   block_table int32 [B, max_pages], contiguous; -1 where a row holds no
+ *     page; kv_lengths int32 [B]; refs int32 [num_pages]: how many table
+ *     entries name the page, 0 for a free one.
+ * B * max_pages below 2^31; num_pages 1 .. 2^30; page_size >= 1.
+ * Choices go by number: the lowest free pages are taken, sequences and their
+ * pages in increasing order, so equal books give equal books.  A listed
+ * sequence or page that does not exist is skipped and FD_DEV_BAD_INDEX set; a
+ * length outside [0, max_pages * page_size] is clamped and FD_DEV_BAD_LENGTH
+ * set.  The calls only queue work on opts->stream, so they can be captured.
+ * opts supplies the stream and the workspace; opts->kernel must be
+ * FD_KERNEL_AUTO, and opts->num_ctas is not used.
+ *
+ * fd_pages_reserve makes sure that every page in which positions
+ *   kv_lengths[b] .. kv_lengths[b] + n_b - 1 lie (n_b: n_new[b], or n_each
+ *   where n_new is NULL; a negative one counts as 0) is sequence b's alone.  An
+ *   entry that names no page gets a free one; an entry whose page others name
+ *   too is moved to a free one, except that the first of them (in order of
+ *   sequences, then pages) keeps it when all of them write.  Where such a
+ *   page holds positions below kv_lengths[b], (old, new) is put into pairs
+ *   (int32 [B, 2]; the rest stays as it was) for fd_pages_copy.  count
+ *   (int32[1]) gets the number of pairs.  With too few free pages nothing is
+ *   reserved, count gets minus the missing pages and FD_DEV_NO_PAGES is set.
+ *   kv_lengths is not changed.
+ * fd_pages_fork: for each i < n, row dst[i] releases its pages and takes those
+ *   that hold the first L positions of row src[i], L = kv_lengths[src[i]], or
+ *   lengths[i] where that is given and smaller; kv_lengths[dst[i]] = L.  An
+ *   entry whose dst is an earlier entry's dst, or another entry's src, is
+ *   skipped and flagged as above; src[i] = dst[i] changes nothing.
+ * fd_pages_free: for each i < n, the length of sequence seqs[i] (seqs NULL:
+ *   sequence i, n = B) becomes 0, or lengths[i] where lengths is given and
+ *   smaller than the length, and the row's pages past it are released.
+ *   A sequence listed twice ends at the smaller length.
+ * fd_pages_compact moves the pages in use to the numbers 0 .. used - 1: the
+ *   i-th page in use at or past `used` goes to the i-th free page below it.
+ *   block_table and refs are renumbered, pairs (int32 [num_pages / 2, 2])
+ *   lists (from, to) and count their number; the contents follow by
+ *   fd_pages_copy.
+ * fd_pages_copy copies, in each of n_pools pools (1 .. 256) [num_pages, ...]
+ *   of any dtype and 1 to 4 dimensions, page pairs[2i] to page pairs[2i+1] for
+ *   i < count[0] (at most max_pairs; nothing for a negative count).  A page's
+ *   elements must fill one block of memory, in any order of dimensions.  No
+ *   page may be both copied from and copied to, nor be copied to twice.
+ *
+ * reserve and compact use pages_scratch(num_pages) bytes of the workspace's
+ * room for split partials (fd_pages_scratch_bytes; the room is
+ * fd_workspace_bytes(segments, rows, head_dim, ctas) less about 4 * segments
+ * bytes).
+ */
+size_t fd_pages_scratch_bytes(int64_t num_pages);
+int fd_pages_reserve(int32_t *block_table, int32_t B, int32_t max_pages,
+                     const int32_t *kv_lengths, const int32_t *n_new, int32_t n_each,
+                     int32_t page_size, int32_t *refs, int32_t num_pages, int32_t *pairs,
+                     int32_t *count, const fd_opts *opts);
+int fd_pages_fork(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *kv_lengths,
+                  int32_t page_size, int32_t *refs, int32_t num_pages, const int32_t *src,
+                  const int32_t *dst, const int32_t *lengths, int32_t n, const fd_opts *opts);
+int fd_pages_free(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *kv_lengths,
+                  int32_t page_size, int32_t *refs, int32_t num_pages, const int32_t *seqs,
+                  const int32_t *lengths, int32_t n, const fd_opts *opts);
+int fd_pages_compact(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *refs,
+                     int32_t num_pages, int32_t *pairs, int32_t *count, const fd_opts *opts);
+int fd_pages_copy(const fd_tensor *pools, int32_t n_pools, const int32_t *pairs,
+                  const int32_t *count, int32_t max_pairs, const fd_opts *opts);
 
 /*
  * Workspace.  A launch unit ("segment") is one (sequence, kv head) in the
