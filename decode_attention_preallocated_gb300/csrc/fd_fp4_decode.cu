@@ -24,7 +24,7 @@
 // of two so that its largest entry lies in [1, 2): a bf16 entry is then exact
 // in fp16 down to 2^-14 of the largest, and below that off by at most 2^-25
 // of it.  The weights are kept as w * 2^4 (up to 2^14, see kGrow) and
-// rounded to fp16: off by 2^-12 of the weight, or by 2^-29 of the row's
+// rounded to fp16: off by up to 2^-11 of the weight, or by 2^-29 of the row's
 // largest weight where that is more; the sums, the reference and both
 // accumulators are fp32.
 #include <cuda_runtime.h>

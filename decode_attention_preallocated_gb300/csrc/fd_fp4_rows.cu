@@ -60,12 +60,12 @@ __device__ __forceinline__ uint2 quantise(const uint32_t *w, float g, uint32_t &
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(want));
         scale = finite ? (uint32_t)two & 0xffu : 0x7fu;
         const __half s = __ushort_as_half((unsigned short)(scales_to_f16x2(two) & 0xffffu));
-        sg = __half2float(s) * g;
-        r = sg > 0.f && finite ? __frcp_rn(sg) : 0.f;
+        sg = finite ? __half2float(s) * g : 0.f;
+        r = sg > 0.f ? __frcp_rn(sg) : 0.f;
     }
     // a scale at its largest (448) leaves values past 6 s g: they saturate
     const float most = 8.f * sg;
-    const bool past = amax > most && finite && sg > 0.f;
+    const bool past = amax > most && sg > 0.f;
     uint32_t out[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -80,7 +80,8 @@ __device__ __forceinline__ uint2 quantise(const uint32_t *w, float g, uint32_t &
             // the IBM RISC System/6000 processor", 1990), so that a value
             // halfway between two codes is seen as such
             const float q = x * r;
-            y[i] = __fmaf_rn(__fmaf_rn(-q, sg, x), r, q);
+            // (and with x's sign, which the sum of a zero loses)
+            y[i] = copysignf(__fmaf_rn(__fmaf_rn(-q, sg, x), r, q), x);
         }
         asm("{\n\t.reg .b8 c;\n\t"
             "cvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\t"

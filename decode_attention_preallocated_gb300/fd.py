@@ -646,6 +646,14 @@ def _table(block_table, B, device):
     return _ints(block_table, (B, max_pages), device, "block_table"), max_pages
 
 
+def _empty(shape, dtype, device, stream):
+    """New memory that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _workspace(workspace, device, sh, segments=1, rows=1, ctas=1):
     """The call's workspace: the given one, or the stream's, which has room
     for 1024 blocks and grows with the segments."""
@@ -670,7 +678,7 @@ def decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q=None, caus
     lens = _ints(kv_lengths, (B,), device, "kv_lengths")
     table, max_pages = _table(block_table, B, device)
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=device)
+        out = _empty(q.shape, out_dtype, device, stream)
     Hkv = max(k_cache.shape[1], 1)
     rows = Hq // Hkv * nq
     sh = _stream_handle(stream, device)
@@ -724,8 +732,7 @@ def read_fp4(k_cache, v_cache, k_scale, v_scale, kv_lengths, n, start=None, k_gl
         raise ValueError("k_cache must be a CUDA tensor")
     if out is None:
         shape = (B, int(n), k_cache.shape[1], 2 * k_cache.shape[3])
-        out = (torch.empty(shape, dtype=out_dtype, device=device),
-               torch.empty(shape, dtype=out_dtype, device=device))
+        out = (_empty(shape, out_dtype, device, stream), _empty(shape, out_dtype, device, stream))
     k, v = out
     _on(device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out=k, out_v=v)
     if k.dim() != 4 or k.shape[0] != B or k.shape[1] != n:
@@ -781,9 +788,9 @@ def pages_reserve(block_table, kv_lengths, refs, page_size, n_new, pairs=None, c
     else:
         each = int(n_new)
     if pairs is None:
-        pairs = torch.empty((B, 2), dtype=torch.int32, device=device)
+        pairs = _empty((B, 2), torch.int32, device, stream)
     if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=device)
+        count = _empty((1,), torch.int32, device, stream)
     sh = _stream_handle(stream, device)
     ws = _pages_workspace(workspace, device, sh, num_pages)
     with _on_device(device):
@@ -837,9 +844,9 @@ def pages_compact(block_table, refs, pairs=None, count=None, stream=None,
     num_pages = refs.shape[0]
     half = max(num_pages // 2, 1)
     if pairs is None:
-        pairs = torch.empty((half, 2), dtype=torch.int32, device=device)
+        pairs = _empty((half, 2), torch.int32, device, stream)
     if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=device)
+        count = _empty((1,), torch.int32, device, stream)
     sh = _stream_handle(stream, device)
     ws = _pages_workspace(workspace, device, sh, num_pages)
     with _on_device(device):

@@ -408,9 +408,9 @@ int fd_decode_noalloc(const fd_tensor *q, const fd_tensor *k_cache,
  * rows are served in the fewest equal parts, each of which reads the prefix
  * and needs a segment of the workspace: B * Hkv * parts of them.
  * The scores and all sums are fp32 over exact products of the codes, the
- * scales and q (an entry of q below 2^-14 of its row's largest is rounded to
- * 2^-24 of that); each softmax weight is rounded to fp16, i.e. by up to
- * 2^-12 of itself or 2^-29 of the row's largest weight.  Positions below the
+ * scales and q (an entry of q below 2^-14 of its row's largest is off by up
+ * to 2^-25 of that); each softmax weight is rounded to fp16, i.e. by up to
+ * 2^-11 of itself or 2^-29 of the row's largest weight.  Positions below the
  * length must hold numbers: a NaN scale (fd_append_fp4 writes one for a row
  * that is not finite) reaches every query row of its kv head, those that the
  * causal window hides it from too.  Positions at or past the length and pages
