@@ -170,7 +170,7 @@ int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor 
     p.g = (int32_t)g; p.d = (int32_t)c.d; p.cap = c.cap; p.rows = part_rows;
     p.mode = block_table ? fd::kPaged : fd::kDense;
     p.causal = causal; p.out_f32 = out->dtype == FD_F32;
-    p.tile = fd::fp4_tile_tokens((int)c.d);
+    p.tile = fd::fp4_tile_tokens((int)c.d, part_rows);
     p.scale_log2 = (float)((double)scale * k_global * 1.4426950408889634);
     p.nseg = B * p.Hkv;
     p.q = static_cast<const uint16_t *>(q->data);
@@ -195,7 +195,7 @@ int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor 
         const int sms = fd::sm_count_current();
         if (sms <= 0) return FD_ERR_CUDA;
         const int64_t most = p.nseg * fd::ceil_div(c.cap, p.tile);
-        const int64_t want = (int64_t)sms * fd::fp4_blocks_per_sm((int)c.d, part_rows);
+        const int64_t want = (int64_t)sms * fd::fp4_blocks_per_sm(part_rows);
         G = (int32_t)(want < most ? want : most);
     }
     if (p.nseg > ws->max_segments || part_rows > ws->max_rows || c.d > ws->head_dim ||

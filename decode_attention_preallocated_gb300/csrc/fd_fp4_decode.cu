@@ -6,13 +6,16 @@
 // pass with a running reference m.  A position costs d/2 + d/16 bytes of K and
 // as many of V, a quarter of a bf16 cache.
 //
-// Layout.  Every warp is on its own: it walks 32 (d = 128) or 16 (d = 256)
-// positions at a time through a private cp.async ring, turns the codes into
-// fp16 operands in registers and feeds mma.sync m16n8k16, so nothing is
-// written back to shared memory and no warp waits for another until its piece
-// of the prefix ends.  Positions are the M side of S^T = K Q^T and head
-// dimensions the M side of O^T = V^T P^T; the query rows are N, in eights, so
-// a group of up to 8 rows wastes nothing.
+// Layout.  A warp walks 32 positions at a time through a private cp.async ring,
+// turns the codes into fp16 operands in registers and feeds mma.sync m16n8k16,
+// so nothing is written back to shared memory.  Positions are the M side of
+// S^T = K Q^T and head dimensions the M side of O^T = V^T P^T; the query rows
+// are N, in eights, so a group of up to 8 rows wastes nothing.
+//   A warp takes 128 values of each row: at d = 128 it is on its own until its
+//   piece of the prefix ends; at d = 256 two warps share the positions, each
+//   with one half of the row, and add their partial scores through shared
+//   memory, so that no code is converted twice and a warp's accumulators hold
+//   128 dimensions in either case.
 //   K: lane 4*gid + t holds 32 consecutive values (two scale groups) of
 //   position gid; the contraction runs over values in the order the lanes hold
 //   them, and Q's fragments are laid out in that order.
@@ -41,43 +44,55 @@ namespace {
 
 using namespace fp4;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 // The reference of a row is its running maximum less 4 when it was last set;
 // it is set again only when a weight would pass 2^14, which keeps every weight
-// within fp16 and spares most tiles the shuffles and the rescaling.
+// within fp16 and spares most steps the shuffles and the rescaling.
 constexpr float kBelow = 4.f, kGrow = 14.f;
+// The reference of a row that has seen nothing yet.
+constexpr float kNone = -3.402823466e38f;
+
+constexpr int kSub = 32;               // positions per warp step
+constexpr int kCode = kSub * 64;       // a step's K (or V) codes of 128 dimensions
+constexpr int kScale = kSub * 8;
+constexpr int kStage = 2 * kCode + 2 * kScale;
 
 template <int NH, int NT>
 struct Cfg {
     static constexpr int D = NH * 128;
-    static constexpr int MT = 2 / NH;            // 16-position blocks per step
-    static constexpr int SUB = 16 * MT;          // positions per warp step
-    static constexpr int TILE = SUB * kWarps;    // positions per partition tile
     static constexpr int ROWS = 8 * NT;
-    static constexpr int CODE = SUB * D / 2;     // bytes of K (or V) codes per step
-    static constexpr int SCALE = SUB * D / 16;
-    static constexpr int STAGE = 2 * CODE + 2 * SCALE;
-    // accumulators of NH * NT * 32 registers: up to 32 of them leave room for
-    // two blocks per SM
-    static constexpr int OCC = NH * NT == 1 ? 2 : (NH * NT == 2 ? 2 : 1);
-    static constexpr int NST = OCC == 2 ? 3 : 4;
-    static constexpr int RING = kWarps * NST * STAGE;
-    static constexpr int MERGE = kWarps * ROWS * (D + 4) * 4;
-    static constexpr int QFRAG = NH * NT * 8 * 32 * 8;
-    static constexpr int BODY = RING > MERGE ? RING : MERGE;
-    static constexpr int SMEM = BODY + QFRAG + ROWS * 4 + kWarps * NST * 4;
-    static_assert((SMEM + 64 + 1024) * OCC <= 228 * 1024, "shared memory");
-    static_assert(QFRAG >= 2 * kWarps * ROWS * 4, "the warps' statistics reuse the Q fragments");
+    // Accumulators take 32 * NT registers: 16 warps an SM fit with one eight
+    // of rows, 12 with two (as two blocks, so that one's start and end overlap
+    // the other's middle), 8 beyond.
+    static constexpr int OCC = NT <= 2 ? 2 : 1;
+    static constexpr int WARPS = NT == 2 ? 6 : 8;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int STREAMS = WARPS / NH;         // warps (pairs) side by side
+    static constexpr int TILE = kSub * STREAMS;        // positions per partition tile
+    static constexpr int MERGE = STREAMS * ROWS * (D + 4) * 4;
+    static constexpr int SWAP = NH == 2 ? 2 * WARPS * NT * 1024 : 0;   // partial scores, two steps
+    static constexpr int QFRAG = NH * NT * 2048;
+    static constexpr int NST = WARPS * 3 * kStage + SWAP + QFRAG <= 108 * 1024 * (3 - OCC) ? 3 : 2;
+    static constexpr int RING = WARPS * NST * kStage;
+    static constexpr int BODY = RING + SWAP > MERGE ? RING + SWAP : MERGE;
+    static constexpr int SMEM = BODY + QFRAG + ROWS * 4 + WARPS * NST * 4;
+    static_assert((SMEM + 128 + 1024) * OCC <= 228 * 1024, "shared memory");
+    static_assert(QFRAG >= 2 * STREAMS * ROWS * 4, "the streams' statistics reuse the Q fragments");
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-// 16 (or 8) bytes into shared memory; zeros when !ok (src is then not read).
+// 16 (or 8) bytes into shared memory; with `ok`, zeros where that is false
+// (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy8(uint32_t dst, const uint8_t *src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
@@ -111,47 +126,110 @@ __device__ __forceinline__ uint32_t chunk_at(int p, int c) {
     return (uint32_t)((p >> 1) * 128 + ((((p & 1) * 4 + c) ^ (2 * ((p >> 1) & 3))) * 16));
 }
 
+// A segment: one part of the query rows of one (sequence, kv head).
 struct Seg {
-    int b, hk, row0, rows;   // sequence, kv head, first row of the part, its rows
-    int64_t len;
+    int b, hp;               // sequence; kv head and part, hp = hk * parts + part
+    int hk, row0, rows;      // kv head; first row of the part and its rows
+    int len;
+    int64_t first, tiles;    // first partition tile and number of tiles
+};
+
+// Walks the launch's tiles in order.  Every warp keeps its own copy (lane l
+// holds the tile count of sequence 32 * chunk + l), so that no barrier is
+// needed to find the next segment.
+struct Finder {
+    const Fp4Params &fp;
+    int lane, chunk;
+    int64_t n;               // tiles per segment of this lane's sequence
+    __device__ __forceinline__ Finder(const Fp4Params &f) : fp(f), lane(threadIdx.x & 31), chunk(0) { load(0); }
+    __device__ __forceinline__ void load(int c) {
+        chunk = c;
+        const int b = c * 32 + lane;
+        n = b < fp.p.B ? ceil_div(seq_len(fp.p, b), fp.p.tile) : 0;
+    }
+    __device__ __forceinline__ int64_t total() {
+        int64_t sum = 0;
+        for (int c = 0; c * 32 < fp.p.B; ++c) {
+            if (c != chunk) load(c);
+            sum += n;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        return sum * fp.p.Hkv;
+    }
+    __device__ __forceinline__ void fill(Seg &g) const {
+        g.hk = g.hp / fp.parts;
+        g.row0 = (g.hp - g.hk * fp.parts) * fp.p.rows;
+        g.rows = min(fp.p.rows, fp.all_rows - g.row0);
+    }
+    // The segment that holds tile t (below the total).
+    __device__ __forceinline__ void find(int64_t t, Seg &g) {
+        int64_t base = 0;
+        for (int c = 0; c * 32 < fp.p.B; ++c) {
+            if (c != chunk) load(c);
+            const int64_t mine = n * fp.p.Hkv;
+            int64_t upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, t < base + upto);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                const int64_t before = base + __shfl_sync(0xffffffffu, upto - mine, src);
+                g.tiles = __shfl_sync(0xffffffffu, n, src);
+                g.b = c * 32 + src;
+                g.hp = (int)((t - before) / g.tiles);
+                g.first = before + g.hp * g.tiles;
+                g.len = (int)seq_len(fp.p, g.b);
+                fill(g);
+                return;
+            }
+            base += __shfl_sync(0xffffffffu, upto, 31);
+        }
+    }
+    // The segment after g (one exists: the caller has tiles left).
+    __device__ __forceinline__ void next(Seg &g) {
+        g.first += g.tiles;
+        if (++g.hp == fp.p.Hkv) {
+            g.hp = 0;
+            for (int c = (g.b + 1) / 32; c * 32 < fp.p.B; ++c) {
+                if (c != chunk) load(c);
+                const unsigned live = __ballot_sync(0xffffffffu, n > 0 && c * 32 + lane > g.b);
+                if (live) {
+                    const int src = __ffs(live) - 1;
+                    g.b = c * 32 + src;
+                    g.tiles = __shfl_sync(0xffffffffu, n, src);
+                    break;
+                }
+            }
+            g.len = (int)seq_len(fp.p, g.b);
+        }
+        fill(g);
+    }
 };
 
 template <int NH, int NT, bool PAGED>
-__global__ void __launch_bounds__(kThreads, (Cfg<NH, NT>::OCC))
+__global__ void __launch_bounds__((Cfg<NH, NT>::THREADS), (Cfg<NH, NT>::OCC))
 fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
     using C = Cfg<NH, NT>;
-    constexpr int D = C::D, MT = C::MT, SUB = C::SUB, NST = C::NST, ROWS = C::ROWS;
+    constexpr int D = C::D, NST = C::NST, ROWS = C::ROWS, STREAMS = C::STREAMS, kThreads = C::THREADS;
     const Params &p = fp.p;
     extern __shared__ __align__(128) unsigned char smem[];
-    uint2 *qfrag = reinterpret_cast<uint2 *>(smem + C::BODY);          // [NH][NT][8][32]
+    float4 *swap = reinterpret_cast<float4 *>(smem + C::RING);       // [2][WARPS][2 * NT][32]
+    uint4 *qfrag = reinterpret_cast<uint4 *>(smem + C::BODY);        // [NH][NT][4][32]
     float *qmul = reinterpret_cast<float *>(smem + C::BODY + C::QFRAG);   // [ROWS]
-    uint32_t *seen = reinterpret_cast<uint32_t *>(qmul + ROWS);        // [kWarps][NST]: valid positions
-    // reference and sum of each warp's rows, once the Q fragments are done with
-    float *wm = reinterpret_cast<float *>(qfrag), *wl = wm + kWarps * ROWS;   // [kWarps][ROWS]
-    __shared__ int64_t sh_total, sh_seg, sh_first, sh_n;
+    uint32_t *seen = reinterpret_cast<uint32_t *>(qmul + ROWS);   // [WARPS][NST]: valid positions (paged)
+    // reference and sum of each stream's rows, once the Q fragments are done with
+    float *wm = reinterpret_cast<float *>(qfrag), *wl = wm + STREAMS * ROWS;   // [STREAMS][ROWS]
     __shared__ int sh_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gid = lane >> 2, t4 = lane & 3;
+    const int half = NH == 2 ? warp & 1 : 0, stream = warp / NH;
     const int G = gridDim.x, cta = blockIdx.x;
 
-    if (warp == 0) {
-        const int64_t tot = total_tiles_warp(p);
-        if (lane == 0) sh_total = tot;
-    }
-    __syncthreads();
-    const int64_t total = sh_total;
-
-    const auto seg_of = [&](int64_t s) {
-        Seg g;
-        const int hp = (int)(s % p.Hkv);
-        g.b = (int)(s / p.Hkv);
-        g.hk = hp / fp.parts;
-        g.row0 = (hp % fp.parts) * p.rows;
-        g.rows = min(p.rows, fp.all_rows - g.row0);
-        g.len = seq_len(p, g.b);
-        return g;
-    };
     // Output pointer offset of row r of a segment.
     const auto out_off = [&](const Seg &g, int r) {
         const int rr = g.row0 + r;
@@ -180,13 +258,24 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
         }
     };
 
-    // Segments with nothing to attend still need their output rows zeroed.
-    for (int64_t s = cta; s < p.nseg; s += G) {
-        if (seg_tiles(p, s) != 0) continue;
-        const Seg g = seg_of(s);
-        const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int e = tid; e < g.rows * (D / 8); e += kThreads)
-            store8(out_off(g, e / (D / 8)) + (e % (D / 8)) * 8, z);
+    Finder finder(fp);
+    const int64_t total = finder.total();
+    // Sequences with nothing to attend still need their output rows zeroed.
+    for (int c = 0; c * 32 < p.B; ++c) {
+        if (c != finder.chunk) finder.load(c);
+        unsigned empty = __ballot_sync(0xffffffffu, finder.n == 0 && c * 32 + lane < p.B);
+        for (; empty; empty &= empty - 1) {
+            const int64_t s0 = (int64_t)(c * 32 + __ffs(empty) - 1) * p.Hkv;
+            for (int hp = (int)(((int64_t)cta - s0 % G + G) % G); hp < p.Hkv; hp += G) {
+                Seg g;
+                g.b = (int)(s0 / p.Hkv);
+                g.hp = hp;
+                finder.fill(g);
+                const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                for (int e = tid; e < g.rows * (D / 8); e += kThreads)
+                    store8(out_off(g, e / (D / 8)) + (e % (D / 8)) * 8, z);
+            }
+        }
     }
     if (total == 0) return;
     const int32_t Gw = working_blocks(total, G);
@@ -194,100 +283,103 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
     const Split sp{total, Gw};
     const int64_t t_begin = sp.start(cta), t_end = sp.start(cta + 1);
 
-    unsigned char *ring = smem + warp * (NST * C::STAGE);
+    unsigned char *ring = smem + warp * (NST * kStage);
     const uint32_t ring_a = smem_addr(ring);
 
-    int64_t t = t_begin;
-    while (t < t_end) {
-        __syncthreads();
-        if (warp == 0) {
-            SegPos pos;
-            const int64_t s = seg_of_tile_warp(p, t, &pos);
-            if (lane == 0) { sh_seg = s; sh_first = pos.first; sh_n = pos.ntiles; }
-        }
-        __syncthreads();
-        const int64_t s = sh_seg, first = sh_first, nt = sh_n;
-        if (s < 0 || nt <= 0) break;   // cannot happen for t < total
+    Seg g;
+    finder.find(t_begin, g);
+    for (int64_t t = t_begin; t < t_end;) {
+        const int64_t s = (int64_t)g.b * p.Hkv + g.hp, first = g.first, nt = g.tiles;
         const int64_t piece_end = min(t_end, first + nt);
-        const Seg g = seg_of(s);
-        const int len = (int)g.len;
+        const int len = g.len;
 
         // ---- the warp's steps: step n covers positions start + n * TILE ..
-        const int start = (int)((t - first) * C::TILE) + warp * SUB;
+        const int start = (int)((t - first) * C::TILE) + stream * kSub;
         const int ntile = (int)(piece_end - t);
         // steps whose first position lies in the prefix
         const int steps = start >= len ? 0 : min(ntile, (int)(((unsigned)(len - start) + (C::TILE - 1u)) / C::TILE));
 
-        const uint8_t *kb = static_cast<const uint8_t *>(p.k) + (int64_t)g.hk * p.ks[1];
-        const uint8_t *vb = static_cast<const uint8_t *>(p.v) + (int64_t)g.hk * p.vs[1];
-        const uint8_t *ksb = fp.ks + (int64_t)g.hk * fp.kss[1];
-        const uint8_t *vsb = fp.vs + (int64_t)g.hk * fp.vss[1];
+        // This lane's part of a step: 16-byte chunk lane & 3 of rows lane >> 2,
+        // + 8, .. (codes) and the scales of row `lane`.
+        const uint8_t *kb = static_cast<const uint8_t *>(p.k) + (int64_t)g.hk * p.ks[1] + half * 64 + t4 * 16;
+        const uint8_t *vb = static_cast<const uint8_t *>(p.v) + (int64_t)g.hk * p.vs[1] + half * 64 + t4 * 16;
+        const uint8_t *ksb = fp.ks + (int64_t)g.hk * fp.kss[1] + half * 8;
+        const uint8_t *vsb = fp.vs + (int64_t)g.hk * fp.vss[1] + half * 8;
         if (!PAGED) {
-            kb += (int64_t)g.b * p.ks[0];
-            vb += (int64_t)g.b * p.vs[0];
-            ksb += (int64_t)g.b * fp.kss[0];
-            vsb += (int64_t)g.b * fp.vss[0];
+            kb += (int64_t)g.b * p.ks[0] + (int64_t)(start + gid) * p.ks[2];
+            vb += (int64_t)g.b * p.vs[0] + (int64_t)(start + gid) * p.vs[2];
+            ksb += (int64_t)g.b * fp.kss[0] + (int64_t)(start + lane) * fp.kss[2];
+            vsb += (int64_t)g.b * fp.vss[0] + (int64_t)(start + lane) * fp.vss[2];
         }
-        // Copies step n into ring slot n % NST.  Lane = position while the
-        // rows are located (page lookup), then lane = 16-byte chunk.
+        const uint32_t to = ring_a + chunk_at(gid, t4);    // rows 8 further lie 512 bytes on
+        // Page of each of the step's four runs of 8 rows (in lanes 0 .. 3),
+        // looked up a step ahead; -1 past the steps and where there is none.
+        const bool runs = PAGED && (p.page_size & 7) == 0;
+        const auto lookup = [&](int n) {
+            int e = -1;
+            const int at = start + n * C::TILE + 8 * lane;
+            if (n < steps && lane < 4 && 8 * lane < len - (start + n * C::TILE)) e = page_of(p, g.b, at);
+            return e;
+        };
+        int ahead = runs ? lookup(0) : 0;
+        // Copies step n into ring slot n % NST.
         const auto fetch = [&](int n) {
             if (n < steps) {
-                const int pos0 = start + n * C::TILE;
+                const int pos0 = start + n * C::TILE, left = len - pos0;   // positions that exist from here on
                 const int slot = n % NST;
-                const uint32_t dst = ring_a + slot * C::STAGE;
-                const int mine = pos0 + lane;
-                bool ok = lane < min(SUB, len - pos0);
-                int page = 0, row = mine;
-                if (PAGED) {
-                    if (ok) {
-                        page = page_of(p, g.b, mine);
-                        row = page_row(p, mine);
-                        ok = page >= 0;
-                    }
-                    if (!ok) { page = 0; row = 0; }
-                }
-                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
-                constexpr int CPR = D / 32;          // 16-byte chunks per row
-                constexpr int RPI = 32 / CPR;        // rows per copy instruction
+                const uint32_t dst = to + slot * kStage;
+                const uint32_t sd = ring_a + slot * kStage + 2 * kCode + lane * 8;
+                if (!PAGED) {
+                    const int64_t far = (int64_t)n * C::TILE;
+                    const uint8_t *k0 = kb + far * p.ks[2], *v0 = vb + far * p.vs[2];
+                    const uint8_t *k1 = ksb + far * fp.kss[2], *v1 = vsb + far * fp.vss[2];
+                    const int64_t k8 = 8 * p.ks[2], v8 = 8 * p.vs[2];
+                    if (left >= kSub) {
 #pragma unroll
-                for (int i = 0; i < SUB / RPI; ++i) {
-                    const int r = i * RPI + lane / CPR, c = lane % CPR;
-                    const bool in = (valid >> r) & 1u;
-                    int64_t ko, vo;
-                    if (PAGED) {
-                        const int pg = __shfl_sync(0xffffffffu, page, r);
-                        const int rw = __shfl_sync(0xffffffffu, row, r);
-                        ko = (int64_t)pg * p.ks[0] + (int64_t)rw * p.ks[2];
-                        vo = (int64_t)pg * p.vs[0] + (int64_t)rw * p.vs[2];
-                    } else {
-                        const int64_t rw = in ? pos0 + r : 0;
-                        ko = rw * p.ks[2];
-                        vo = rw * p.vs[2];
+                        for (int i = 0; i < 4; ++i) {
+                            copy16(dst + i * 512, k0 + i * k8);
+                            copy16(dst + i * 512 + kCode, v0 + i * v8);
+                        }
+                        copy8(sd, k1);
+                        copy8(sd + kScale, v1);
+                    } else {   // rows past the length: zeros, from an address that exists
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const bool in = 8 * i + gid < left;
+                            copy16(dst + i * 512, in ? k0 + i * k8 : static_cast<const uint8_t *>(p.k), in);
+                            copy16(dst + i * 512 + kCode, in ? v0 + i * v8 : static_cast<const uint8_t *>(p.v), in);
+                        }
+                        const bool in = lane < left;
+                        copy8(sd, in ? k1 : fp.ks, in);
+                        copy8(sd + kScale, in ? v1 : fp.vs, in);
                     }
-                    const uint32_t a = dst + (NH == 2 ? (c >> 2) * (SUB * 64) : 0) + chunk_at(r, c & 3);
-                    copy16(a, kb + ko + c * 16, in);
-                    copy16(a + C::CODE, vb + vo + c * 16, in);
-                }
-                const uint32_t sd = dst + 2 * C::CODE;
-                if (NH == 1) {
-                    const int64_t rw = PAGED || ok ? row : 0;
-                    copy8(sd + lane * 8, ksb + (PAGED ? (int64_t)page * fp.kss[0] : 0) + rw * fp.kss[2], ok);
-                    copy8(sd + C::SCALE + lane * 8,
-                          vsb + (PAGED ? (int64_t)page * fp.vss[0] : 0) + rw * fp.vss[2], ok);
                 } else {
-                    // lanes 0-15 the K scales, lanes 16-31 the V scales
-                    const int r = lane & 15;
-                    const bool in = (valid >> r) & 1u;
-                    int64_t pg = 0, rw = in ? pos0 + r : 0;
-                    if (PAGED) {
-                        pg = __shfl_sync(0xffffffffu, page, r);
-                        rw = __shfl_sync(0xffffffffu, row, r);
+                    // row `lane`: its page and row in it
+                    int page, row;
+                    if (runs) {
+                        page = __shfl_sync(0xffffffffu, ahead, lane >> 3);
+                        row = page_row(p, pos0 + (lane & ~7)) + (lane & 7);
+                    } else {
+                        page = lane < left ? page_of(p, g.b, pos0 + lane) : -1;
+                        row = lane < left ? page_row(p, pos0 + lane) : 0;
                     }
-                    const uint8_t *src = lane < 16 ? ksb + pg * fp.kss[0] * (PAGED ? 1 : 0) + rw * fp.kss[2]
-                                                   : vsb + pg * fp.vss[0] * (PAGED ? 1 : 0) + rw * fp.vss[2];
-                    copy16(sd + lane * 16, src, in);
+                    const bool ok = lane < left && page >= 0;
+                    if (page < 0) page = 0;
+                    if (!ok) row = 0;
+                    const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+                    if (lane == 0) seen[warp * NST + slot] = valid;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int pg = __shfl_sync(0xffffffffu, page, 8 * i + gid);
+                        const int rw = __shfl_sync(0xffffffffu, row, 8 * i + gid);
+                        const bool in = (valid >> (8 * i + gid)) & 1u;
+                        copy16(dst + i * 512, kb + (int64_t)pg * p.ks[0] + (int64_t)rw * p.ks[2], in);
+                        copy16(dst + i * 512 + kCode, vb + (int64_t)pg * p.vs[0] + (int64_t)rw * p.vs[2], in);
+                    }
+                    copy8(sd, ksb + (int64_t)page * fp.kss[0] + (int64_t)row * fp.kss[2], ok);
+                    copy8(sd + kScale, vsb + (int64_t)page * fp.vss[0] + (int64_t)row * fp.vss[2], ok);
+                    if (runs) ahead = lookup(n + 1);
                 }
-                if (lane == 0) seen[warp * NST + slot] = valid;
             }
             copy_commit();
         };
@@ -295,7 +387,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
         for (int n = 0; n < NST - 1; ++n) fetch(n);
 
         // ---- Q: fp16 fragments and each row's factor, while K and V arrive
-        for (int r = warp; r < ROWS; r += kWarps) {
+        for (int r = warp; r < ROWS; r += C::WARPS) {
             float x[NH][4];
             float amax = 0.f;
             const int rr = g.row0 + r;
@@ -313,79 +405,76 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             // 2^e <= amax < 2^(e+1); e within what 2^-e and 2^e can hold
             int e = (int)((__float_as_uint(amax) >> 23) & 255u) - 127;
             e = amax > 0.f ? max(-126, min(126, e)) : 0;
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            if (lane == 0) qmul[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+            // a negative scale turns the query instead: the factors stay >= 0
+            const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), p.scale_log2);
+            // (and above 0, so that -inf stays -inf when multiplied)
+            if (lane == 0)
+                qmul[r] = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1.1754944e-38f);
 #pragma unroll
             for (int h = 0; h < NH; ++h) {
                 const uint2 f = make_uint2(pack_f16x2(x[h][0] * down, x[h][1] * down),
                                            pack_f16x2(x[h][2] * down, x[h][3] * down));
                 // values 4*lane .. +3 of the half: owner lane t = lane / 8, k step lane % 8
-                qfrag[((h * NT + (r >> 3)) * 8 + (lane & 7)) * 32 + (r & 7) * 4 + (lane >> 3)] = f;
+                reinterpret_cast<uint2 *>(qfrag)[((((h * NT + (r >> 3)) * 4 + ((lane & 7) >> 1)) * 32 +
+                                                   (r & 7) * 4 + (lane >> 3)) * 2) + (lane & 1)] = f;
             }
         }
         __syncthreads();
 
-        float mul[NT][2];    // rows 8*n + 2*t4 and the next: factor on q.k
-        int lim[NT][2];      // last position each row sees
         float mr[NT][2], l[NT][2];
-        float O[NH][8][NT][4];
+        float O[8][NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int r = n * 8 + 2 * t4 + c;
-                mul[n][c] = qmul[r];
-                lim[n][c] = p.causal ? len - p.n_q + (g.row0 + r) % p.n_q : len - 1;
-                mr[n][c] = neg_inf();
+                mr[n][c] = kNone;
                 l[n][c] = 0.f;
             }
 #pragma unroll
-        for (int h = 0; h < NH; ++h)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int e = 0; e < 4; ++e) O[j][n][e] = 0.f;
+        const uint4 *qf = qfrag + half * NT * 128 + lane;
+        uint4 qr[4];         // one eight of rows keeps its fragments in registers
+        if (NT == 1)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) O[h][j][n][e] = 0.f;
+            for (int w = 0; w < 4; ++w) qr[w] = qf[w * 32];
+        const float2 mul1 = *reinterpret_cast<const float2 *>(qmul + 2 * t4);
 
         for (int n0 = 0; n0 < steps; ++n0) {
             copy_wait<NST - 2>();
             __syncwarp();
             fetch(n0 + NST - 1);
-            const unsigned char *st = ring + (n0 % NST) * C::STAGE;
+            const unsigned char *st = ring + (n0 % NST) * kStage;
             const int pos0 = start + n0 * C::TILE;
 
-            // ---- S^T = K Q^T
-            float S[MT][NT][4];
+            // ---- S^T = K Q^T over this warp's 128 values
+            float S[2][NT][4];
+            {
+                const unsigned char *kh = st + chunk_at(gid, t4);
+                const unsigned char *sc = st + 2 * kCode + gid * 8 + 2 * t4;
+                uint4 ka[2], kc[2];
+                uint32_t sa[2], sb[2];
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < 2; ++m) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) S[m][n][e] = 0.f;
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const unsigned char *kh = st + h * (SUB * 64);
-                const unsigned char *sc = st + 2 * C::CODE + h * 8 + 2 * t4;
-                uint4 ka[MT], kc[MT];
-                uint32_t sa[MT], sb[MT];
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    ka[m] = *reinterpret_cast<const uint4 *>(kh + chunk_at(m * 16 + gid, t4));
-                    kc[m] = *reinterpret_cast<const uint4 *>(kh + chunk_at(m * 16 + gid + 8, t4));
-                    sa[m] = scales_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + (m * 16 + gid) * (NH * 8)));
-                    sb[m] = scales_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + (m * 16 + gid + 8) * (NH * 8)));
+                        for (int e = 0; e < 4; ++e) S[m][n][e] = 0.f;
+                    ka[m] = *reinterpret_cast<const uint4 *>(kh + m * 1024);
+                    kc[m] = *reinterpret_cast<const uint4 *>(kh + m * 1024 + 512);
+                    sa[m] = scales_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + m * 128));
+                    sb[m] = scales_to_f16x2(*reinterpret_cast<const uint16_t *>(sc + m * 128 + 64));
                 }
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {   // word w: k steps 2w and 2w + 1
-                    uint2 qf[2][NT];
+                    uint4 q4[NT];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int n = 0; n < NT; ++n) q4[n] = NT == 1 ? qr[w] : qf[(n * 4 + w) * 32];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            qf[i][n] = qfrag[((h * NT + n) * 8 + 2 * w + i) * 32 + lane];
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
+                    for (int m = 0; m < 2; ++m) {
                         const uint32_t wa = w == 0 ? ka[m].x : w == 1 ? ka[m].y : w == 2 ? ka[m].z : ka[m].w;
                         const uint32_t wb = w == 0 ? kc[m].x : w == 1 ? kc[m].y : w == 2 ? kc[m].z : kc[m].w;
                         const uint32_t ga = __byte_perm(sa[m], 0, w < 2 ? 0x1010 : 0x3232);
@@ -399,38 +488,71 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                             b[e] = mul_f16x2(b[e], gb);
                         }
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                        for (int n = 0; n < NT; ++n) mma(S[m][n], a[0], b[0], a[1], b[1], q4[n].x, q4[n].y);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma(S[m][n], a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], qf[i][n].x, qf[i][n].y);
+                        for (int n = 0; n < NT; ++n) mma(S[m][n], a[2], b[2], a[3], b[3], q4[n].z, q4[n].w);
                     }
                 }
             }
-
-            // ---- mask, reference, weights
-            const uint32_t valid = seen[warp * NST + n0 % NST];
-            const bool whole = valid == (SUB == 32 ? 0xffffffffu : 0xffffu) &&
-                               (!p.causal || pos0 + SUB - 1 <= len - p.n_q);
-            float top[NT][2];
+            // d = 256: both halves' parts of the scores meet in shared memory;
+            // both warps add the same two numbers, so they agree on everything
+            // that follows.  Two buffers: one is written again only after the
+            // next step's barrier, when the partner has read it.
+            if (NH == 2) {
+                float4 *mine = swap + (((n0 & 1) * C::WARPS + warp) * (2 * NT)) * 32 + lane;
+                const float4 *theirs = swap + (((n0 & 1) * C::WARPS + (warp ^ 1)) * (2 * NT)) * 32 + lane;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                top[n][0] = top[n][1] = neg_inf();
+                for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                    for (int n = 0; n < NT; ++n)
+                        mine[(m * NT + n) * 32] = make_float4(S[m][n][0], S[m][n][1], S[m][n][2], S[m][n][3]);
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + stream) : "memory");
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = e & 1, at = m * 16 + gid + (e >> 1) * 8;
-                        float x = S[m][n][e] * mul[n][c];
-                        if (!whole && (!((valid >> at) & 1u) || pos0 + at > lim[n][c])) x = neg_inf();
-                        S[m][n][e] = x;
-                        top[n][c] = fmaxf(top[n][c], x);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float4 o = theirs[(m * NT + n) * 32];
+                        S[m][n][0] += o.x; S[m][n][1] += o.y; S[m][n][2] += o.z; S[m][n][3] += o.w;
                     }
             }
+            uint32_t valid;
+            if (PAGED) valid = seen[warp * NST + n0 % NST];
+            else valid = len - pos0 >= kSub ? 0xffffffffu : (1u << (len - pos0)) - 1u;
+            const bool masked = valid != 0xffffffffu || (p.causal && pos0 + (kSub - 1) > len - p.n_q);
+
+            // ---- mask, reference, weights
+            if (masked) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        // last position the row sees
+                        const int lim = p.causal ? len - p.n_q + (g.row0 + n * 8 + 2 * t4 + c) % p.n_q : len - 1;
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int e = c; e < 4; e += 2) {
+                                const int at = m * 16 + gid + (e >> 1) * 8;
+                                if (!((valid >> at) & 1u) || at > lim - pos0) S[m][n][e] = neg_inf();
+                            }
+                    }
+            }
+            float mul[NT][2];    // rows 8*n + 2*t4 and the next: factor on q.k
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float2 x = NT == 1 ? mul1 : *reinterpret_cast<const float2 *>(qmul + n * 8 + 2 * t4);
+                mul[n][0] = x.x;
+                mul[n][1] = x.y;
+            }
+            float top[NT][2];
             bool grow = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) grow |= top[n][c] - mr[n][c] > kGrow;
+                for (int c = 0; c < 2; ++c) {
+                    top[n][c] = fmaxf(fmaxf(S[0][n][c], S[0][n][c + 2]), fmaxf(S[1][n][c], S[1][n][c + 2]));
+                    grow |= __fmaf_rn(top[n][c], mul[n][c], -mr[n][c]) > kGrow;
+                }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -439,70 +561,65 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                         float x = top[n][c];
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                        const float to = fmaxf(mr[n][c], x - kBelow);
-                        const float by = mr[n][c] == neg_inf() ? 0.f : fast_exp2(mr[n][c] - to);
-                        mr[n][c] = to;
+                        // (a row that still sees nothing keeps kNone)
+                        const float ref = fmaxf(mr[n][c], x * mul[n][c] - kBelow);
+                        const float by = fast_exp2(mr[n][c] - ref);
+                        mr[n][c] = ref;
                         l[n][c] *= by;
 #pragma unroll
-                        for (int h = 0; h < NH; ++h)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                O[h][j][n][c] *= by;
-                                O[h][j][n][c + 2] *= by;
-                            }
+                        for (int j = 0; j < 8; ++j) {
+                            O[j][n][c] *= by;
+                            O[j][n][c + 2] *= by;
+                        }
                     }
             }
-            uint32_t P[MT][NT][2];
+            uint32_t P[2][NT][2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float m0 = mr[n][0] == neg_inf() ? 0.f : mr[n][0];
-                const float m1 = mr[n][1] == neg_inf() ? 0.f : mr[n][1];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    const float w0 = fast_exp2(S[m][n][0] - m0), w1 = fast_exp2(S[m][n][1] - m1);
-                    const float w2 = fast_exp2(S[m][n][2] - m0), w3 = fast_exp2(S[m][n][3] - m1);
+                for (int m = 0; m < 2; ++m) {
+                    const float w0 = fast_exp2(__fmaf_rn(S[m][n][0], mul[n][0], -mr[n][0]));
+                    const float w1 = fast_exp2(__fmaf_rn(S[m][n][1], mul[n][1], -mr[n][1]));
+                    const float w2 = fast_exp2(__fmaf_rn(S[m][n][2], mul[n][0], -mr[n][0]));
+                    const float w3 = fast_exp2(__fmaf_rn(S[m][n][3], mul[n][1], -mr[n][1]));
                     l[n][0] += w0 + w2;
                     l[n][1] += w1 + w3;
                     P[m][n][0] = transpose8x8(pack_f16x2(w0, w1));
                     P[m][n][1] = transpose8x8(pack_f16x2(w2, w3));
                 }
-            }
 
-            // ---- O^T += V^T P^T
+            // ---- O^T += V^T P^T over this warp's 128 dimensions
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const unsigned char *vh = st + C::CODE + h * (SUB * 64) + (gid & 1) * 8;
-                const unsigned char *sc = st + 2 * C::CODE + C::SCALE + h * 8 + gid;
+            for (int m = 0; m < 2; ++m) {
+                const unsigned char *sc = st + 2 * kCode + kScale + m * 128 + 16 * t4 + gid;
+                uint2 x[4];
+                uint32_t s8[4];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    uint2 x[4];
-                    uint32_t s8[4];
+                for (int e = 0; e < 4; ++e) {
+                    const int at = 2 * t4 + (e & 1) + (e >> 1) * 8;
+                    x[e] = *reinterpret_cast<const uint2 *>(st + kCode + m * 1024 + chunk_at(at, gid >> 1) +
+                                                            (gid & 1) * 8);
+                    s8[e] = sc[(e & 1) * 8 + (e >> 1) * 64];
+                }
+                const uint32_t g01 = scales_to_f16x2(s8[0] | (s8[1] << 8));
+                const uint32_t g23 = scales_to_f16x2(s8[2] | (s8[3] << 8));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int at = m * 16 + 2 * t4 + (e & 1) + (e >> 1) * 8;
-                        x[e] = *reinterpret_cast<const uint2 *>(vh + chunk_at(at, gid >> 1));
-                        s8[e] = sc[at * (NH * 8)];
-                    }
-                    const uint32_t g01 = scales_to_f16x2(s8[0] | (s8[1] << 8));
-                    const uint32_t g23 = scales_to_f16x2(s8[2] | (s8[3] << 8));
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t x0 = w ? x[0].y : x[0].x, x1 = w ? x[1].y : x[1].x;
+                    const uint32_t x2 = w ? x[2].y : x[2].x, x3 = w ? x[3].y : x[3].x;
+                    constexpr uint32_t lo = 0x0f0f0f0fu;
+                    uint32_t a0[4], a1[4], a2[4], a3[4];
+                    codes_to_f16x2((x0 & lo) | ((x1 << 4) & ~lo), a0[0], a0[1], a0[2], a0[3]);
+                    codes_to_f16x2(((x0 >> 4) & lo) | (x1 & ~lo), a1[0], a1[1], a1[2], a1[3]);
+                    codes_to_f16x2((x2 & lo) | ((x3 << 4) & ~lo), a2[0], a2[1], a2[2], a2[3]);
+                    codes_to_f16x2(((x2 >> 4) & lo) | (x3 & ~lo), a3[0], a3[1], a3[2], a3[3]);
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t x0 = w ? x[0].y : x[0].x, x1 = w ? x[1].y : x[1].x;
-                        const uint32_t x2 = w ? x[2].y : x[2].x, x3 = w ? x[3].y : x[3].x;
-                        constexpr uint32_t lo = 0x0f0f0f0fu;
-                        uint32_t a0[4], a1[4], a2[4], a3[4];
-                        codes_to_f16x2((x0 & lo) | ((x1 << 4) & ~lo), a0[0], a0[1], a0[2], a0[3]);
-                        codes_to_f16x2(((x0 >> 4) & lo) | (x1 & ~lo), a1[0], a1[1], a1[2], a1[3]);
-                        codes_to_f16x2((x2 & lo) | ((x3 << 4) & ~lo), a2[0], a2[1], a2[2], a2[3]);
-                        codes_to_f16x2(((x2 >> 4) & lo) | (x3 & ~lo), a3[0], a3[1], a3[2], a3[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t f0 = mul_f16x2(a0[i], g01), f1 = mul_f16x2(a1[i], g01);
+                        const uint32_t f2 = mul_f16x2(a2[i], g23), f3 = mul_f16x2(a3[i], g23);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t f0 = mul_f16x2(a0[i], g01), f1 = mul_f16x2(a1[i], g01);
-                            const uint32_t f2 = mul_f16x2(a2[i], g23), f3 = mul_f16x2(a3[i], g23);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma(O[h][4 * w + i][n], f0, f1, f2, f3, P[m][n][0], P[m][n][1]);
-                        }
+                        for (int n = 0; n < NT; ++n)
+                            mma(O[4 * w + i][n], f0, f1, f2, f3, P[m][n][0], P[m][n][1]);
                     }
                 }
             }
@@ -518,32 +635,30 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             for (int c = 0; c < 2; ++c) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], o);
-                if (gid == 0) {
-                    wm[warp * ROWS + n * 8 + 2 * t4 + c] = mr[n][c];
-                    wl[warp * ROWS + n * 8 + 2 * t4 + c] = l[n][c];
+                if (gid == 0 && half == 0) {
+                    wm[stream * ROWS + n * 8 + 2 * t4 + c] = mr[n][c];
+                    wl[stream * ROWS + n * 8 + 2 * t4 + c] = l[n][c];
                 }
             }
         __syncthreads();
-        float *sums = reinterpret_cast<float *>(smem);   // [kWarps][ROWS][D + 4]
+        float *sums = reinterpret_cast<float *>(smem);   // [STREAMS][ROWS][D + 4]
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int r = n * 8 + 2 * t4 + c;
-                float M = neg_inf();
+                float M = kNone;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * ROWS + r]);
-                const float by = mr[n][c] == neg_inf() ? 0.f : fast_exp2(mr[n][c] - M);
+                for (int w = 0; w < STREAMS; ++w) M = fmaxf(M, wm[w * ROWS + r]);
+                const float by = fast_exp2(mr[n][c] - M);
                 // rows 2t and 2t + 1 apart, so that the 8 lanes of a 128-byte
                 // store (4 rows, 2 groups) fall on different banks
-                float *dst = sums + (warp * ROWS + n * 8 + c * 4 + t4) * (D + 4) + 16 * gid;
+                float *dst = sums + (stream * ROWS + n * 8 + c * 4 + t4) * (D + 4) + half * 128 + 16 * gid;
 #pragma unroll
-                for (int h = 0; h < NH; ++h)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float4 *>(dst + h * 128 + j * 4) =
-                            make_float4(O[h][2 * j][n][c] * by, O[h][2 * j][n][c + 2] * by,
-                                        O[h][2 * j + 1][n][c] * by, O[h][2 * j + 1][n][c + 2] * by);
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<float4 *>(dst + j * 4) =
+                        make_float4(O[2 * j][n][c] * by, O[2 * j][n][c + 2] * by,
+                                    O[2 * j + 1][n][c] * by, O[2 * j + 1][n][c + 2] * by);
             }
         __syncthreads();
         const int c_first = sp.owner(first), c_last = sp.owner(first + nt - 1);
@@ -551,18 +666,15 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
         float *slot = slot_ptr(p, s, cta);
         for (int e = tid; e < g.rows * (D / 8); e += kThreads) {
             const int r = e / (D / 8), col = (e % (D / 8)) * 8;
-            float M = neg_inf(), L = 0.f;
+            float M = kNone, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * ROWS + r]);
+            for (int w = 0; w < STREAMS; ++w) M = fmaxf(M, wm[w * ROWS + r]);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float x = wm[w * ROWS + r];
-                L += x == neg_inf() ? 0.f : wl[w * ROWS + r] * fast_exp2(x - M);
-            }
+            for (int w = 0; w < STREAMS; ++w) L += wl[w * ROWS + r] * fast_exp2(wm[w * ROWS + r] - M);
             float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             const int at = (r & ~7) + (r & 1) * 4 + ((r & 7) >> 1);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < STREAMS; ++w) {
                 const float4 *src = reinterpret_cast<const float4 *>(sums + (w * ROWS + at) * (D + 4) + col);
                 const float4 a = src[0], b = src[1];
                 o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
@@ -592,35 +704,68 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             __syncthreads();
             if (sh_last) {
                 __threadfence();
-                for (int e = tid; e < g.rows * (D / 8); e += kThreads) {
+                // (row, 8 columns) items, and `ways` groups of threads that
+                // take every ways-th piece each
+                const int items = g.rows * (D / 8);
+                const int ways = max(1, kThreads / items);
+                float *part = sums;   // [ways - 1][items][10]
+                for (int e0 = 0; e0 < items; e0 += kThreads) {
+                    const int way = items < kThreads ? tid / items : 0;
+                    const int e = items < kThreads ? tid - way * items : e0 + tid;
                     const int r = e / (D / 8), col = (e % (D / 8)) * 8;
-                    float M = neg_inf(), L = 0.f;
+                    float M = kNone, L = 0.f;
                     float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (way < ways && e < items) {
 #pragma unroll 4
-                    for (int c2 = c_first; c2 <= c_last; ++c2) {
-                        const float *sl = slot_ptr(p, s, c2);
-                        const float mv = __ldcg(sl + (int64_t)p.rows * D + r);
-                        const float lv = __ldcg(sl + (int64_t)p.rows * D + p.rows + r);
-                        const float4 a = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col));
-                        const float4 b = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col + 4));
-                        const float to = fmaxf(M, mv);
-                        const float u = M == neg_inf() ? 0.f : fast_exp2(M - to);
-                        const float w = mv == neg_inf() ? 0.f : fast_exp2(mv - to);
-                        M = to;
-                        L = L * u + w * lv;
-                        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                        for (int c2 = c_first + way; c2 <= c_last; c2 += ways) {
+                            const float *sl = slot_ptr(p, s, c2);
+                            const float mv = __ldcg(sl + (int64_t)p.rows * D + r);
+                            const float lv = __ldcg(sl + (int64_t)p.rows * D + p.rows + r);
+                            const float4 a = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col));
+                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col + 4));
+                            const float ref = fmaxf(M, mv);
+                            const float u = fast_exp2(M - ref), w = fast_exp2(mv - ref);
+                            M = ref;
+                            L = L * u + w * lv;
+                            const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * x[i];
+                            for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * x[i];
+                        }
                     }
-                    const float by = L > 0.f || L != L ? fp.v_global / L : 0.f;
+                    if (ways > 1) {
+                        if (way > 0 && way < ways) {
+                            float *dst = part + ((way - 1) * items + e) * 10;
+                            dst[0] = M;
+                            dst[1] = L;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] *= by;
-                    store8(out_off(g, r) + col, o);
+                            for (int i = 0; i < 8; ++i) dst[2 + i] = o[i];
+                        }
+                        __syncthreads();
+                    }
+                    if (way == 0 && e < items) {
+                        for (int k = 0; k < ways - 1; ++k) {
+                            const float *src = part + (k * items + e) * 10;
+                            const float ref = fmaxf(M, src[0]);
+                            const float u = fast_exp2(M - ref), w = fast_exp2(src[0] - ref);
+                            M = ref;
+                            L = L * u + w * src[1];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * src[2 + i];
+                        }
+                        const float by = L > 0.f || L != L ? fp.v_global / L : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] *= by;
+                        store8(out_off(g, r) + col, o);
+                    }
                 }
                 if (tid == 0) p.counters[s] = 0;
             }
         }
         t = piece_end;
+        if (t < t_end) {
+            finder.next(g);
+            __syncthreads();   // the sums are read before the ring is filled again
+        }
     }
 }
 
@@ -637,7 +782,7 @@ int launch(const Fp4Params &p, int G, cudaStream_t st) {
             return -5;
         opted.fetch_or(bit, std::memory_order_release);
     }
-    fp4_decode_kernel<NH, NT, PAGED><<<G, kThreads, C::SMEM, st>>>(p);
+    fp4_decode_kernel<NH, NT, PAGED><<<G, C::THREADS, C::SMEM, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
@@ -648,15 +793,14 @@ int launch_layout(const Fp4Params &p, int G, cudaStream_t st) {
 
 }  // namespace
 
-int fp4_max_rows(int d) { return d == 128 ? 32 : 16; }
+int fp4_max_rows(int) { return 32; }
 
-int fp4_tile_tokens(int d) { return d == 128 ? Cfg<1, 1>::TILE : Cfg<2, 1>::TILE; }
-
-int fp4_blocks_per_sm(int d, int rows) {
-    const int nt = (rows + 7) / 8;
-    if (d == 128) return nt <= 1 ? Cfg<1, 1>::OCC : nt == 2 ? Cfg<1, 2>::OCC : 1;
-    return nt <= 1 ? Cfg<2, 1>::OCC : 1;
+int fp4_tile_tokens(int d, int rows) {
+    static const int tile[4] = {Cfg<1, 1>::TILE, Cfg<1, 2>::TILE, Cfg<1, 3>::TILE, Cfg<1, 4>::TILE};
+    return tile[(rows - 1) / 8] / (d / 128);   // pairs of warps at d = 256
 }
+
+int fp4_blocks_per_sm(int rows) { return rows <= 16 ? Cfg<1, 1>::OCC : Cfg<1, 3>::OCC; }
 
 int launch_fp4_decode(const Fp4Params &p, int G, cudaStream_t st) {
     const int nt = (p.p.rows + 7) / 8;
@@ -668,6 +812,8 @@ int launch_fp4_decode(const Fp4Params &p, int G, cudaStream_t st) {
     } else if (p.p.d == 256) {
         if (nt <= 1) return launch_layout<2, 1>(p, G, st);
         if (nt == 2) return launch_layout<2, 2>(p, G, st);
+        if (nt == 3) return launch_layout<2, 3>(p, G, st);
+        if (nt == 4) return launch_layout<2, 4>(p, G, st);
     }
     return -2;
 }

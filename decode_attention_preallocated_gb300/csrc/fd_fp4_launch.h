@@ -21,10 +21,10 @@ struct Fp4Params {
 };
 // Rows that one part holds at most for this head_dim.
 int fp4_max_rows(int d);
-// Cache positions per tile of the partitioner.
-int fp4_tile_tokens(int d);
-// Blocks per SM of the kernel for this part size.
-int fp4_blocks_per_sm(int d, int rows);
+// Cache positions per tile of the partitioner, for parts of this many rows.
+int fp4_tile_tokens(int d, int rows);
+// Blocks of the kernel that an SM holds, for parts of this many rows.
+int fp4_blocks_per_sm(int rows);
 int launch_fp4_decode(const Fp4Params &p, int num_ctas, cudaStream_t stream);
 
 // The rows of a 4-bit cache between bf16 (or fp32) and its own format

@@ -682,8 +682,8 @@ def decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q=None, caus
     Hkv = max(k_cache.shape[1], 1)
     rows = Hq // Hkv * nq
     sh = _stream_handle(stream, device)
-    # at most a part for every 16 rows
-    ws = _workspace(workspace, device, sh, B * Hkv * ((rows + 15) // 16), min(rows, 32), max(num_ctas, 1))
+    # more than 32 rows: two halves of them
+    ws = _workspace(workspace, device, sh, B * Hkv * (2 if rows > 32 else 1), min(rows, 32), max(num_ctas, 1))
     with _on_device(device):
         rc = lib().fd_decode_fp4(_pack(q), _pack(k_cache), _pack(v_cache), _pack(k_scale),
                                  _pack(v_scale), k_global, v_global, table, max_pages, lens,

@@ -404,9 +404,9 @@ int fd_decode_noalloc(const fd_tensor *q, const fd_tensor *k_cache,
 /*
  * Dense prefix decode over a 4-bit cache: the visible set, causal window and
  * output of fd_decode (flat) or fd_decode_paged.  Up to 64 rows
- * ((Hq / Hkv) * n_q) share a kv head; above 32 (d = 128) or 16 (d = 256) the
- * rows are served in the fewest equal parts, each of which reads the prefix
- * and needs a segment of the workspace: B * Hkv * parts of them.
+ * ((Hq / Hkv) * n_q) share a kv head; more than 32 are served in two halves,
+ * each of which reads the prefix and needs a segment of the workspace:
+ * 2 * B * Hkv of them.
  * The scores and all sums are fp32 over exact products of the codes, the
  * scales and q (an entry of q below 2^-14 of its row's largest is off by up
  * to 2^-25 of that); each softmax weight is rounded to fp16, i.e. by up to

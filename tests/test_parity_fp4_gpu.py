@@ -433,3 +433,16 @@ def test_workspace_too_small_is_refused():
     with pytest.raises(fd.FdError) as e:
         fd.decode_fp4(q, kd, kd, ksd, ksd, ints([64]), workspace=ws)
     assert e.value.code == fd.FD_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1e-20])
+def test_other_scales(scale):
+    # 0 weighs every visible position alike; a negative one turns the order
+    rng = np.random.default_rng(34)
+    for d in (128, 256):
+        (k, ks), (v, vs) = (cache(rng, 2, 1, 150, d) for _ in range(2))
+        (kd, ksd), (vd, vsd) = to_dev(k, ks), to_dev(v, vs)
+        q = bf16(rng, (2, 3, 4, d))
+        got = fd.decode_fp4(q.cuda(), kd, vd, ksd, vsd, ints([150, 2]), causal=True, scale=scale, out_dtype=F32)
+        want, weight, size = fp4.decode(q.double().numpy(), k, v, ks, vs, [150, 2], True, scale)
+        check(got, want, decode_bound(want, weight, size, 150, np.abs(fp4.values(v, vs)).max(), F32), "scale")
