@@ -43,7 +43,7 @@ constexpr uint64_t kDefaultWaitNs = 2000000000ull;   // 2 s per internal wait
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 struct WsLayout {
-    size_t counters_off, status_off, partials_off, total;
+    size_t counters_off, groups_off, status_off, partials_off, total;
     size_t partial_floats;
 };
 
@@ -51,7 +51,8 @@ WsLayout ws_layout(int64_t max_segments, int32_t max_rows, int32_t head_dim,
                    int32_t max_ctas) {
     WsLayout L;
     L.counters_off = 0;
-    L.status_off = align_up((size_t)max_segments * 4, 256);
+    L.groups_off = align_up((size_t)max_segments * 4, 256);
+    L.status_off = L.groups_off + align_up((size_t)(max_segments + max_ctas) * 4, 256);
     L.partials_off = L.status_off + 256;
     L.partial_floats = (size_t)(max_segments + max_ctas) *
                        (size_t)fd::slot_floats(max_rows, head_dim);
@@ -450,6 +451,7 @@ int fd_workspace_create(int64_t max_segments, int32_t max_rows, int32_t head_dim
     ws->head_dim = head_dim;
     ws->max_ctas = max_ctas;
     ws->counters = reinterpret_cast<int32_t *>(static_cast<char *>(base) + L.counters_off);
+    ws->groups = reinterpret_cast<int32_t *>(static_cast<char *>(base) + L.groups_off);
     ws->status = reinterpret_cast<int32_t *>(static_cast<char *>(base) + L.status_off);
     ws->partials = reinterpret_cast<float *>(static_cast<char *>(base) + L.partials_off);
     ws->partial_floats = L.partial_floats;

@@ -12,7 +12,8 @@ struct fd_workspace {
     size_t bytes;
     int64_t max_segments;
     int32_t max_rows, head_dim, max_ctas;
-    int32_t *counters;
+    int32_t *counters;       // [max_segments], zero between launches
+    int32_t *groups;         // [max_segments + max_ctas], likewise
     int32_t *status;
     float *partials;
     size_t partial_floats;

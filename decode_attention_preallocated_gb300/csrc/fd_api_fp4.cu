@@ -189,12 +189,18 @@ int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor 
     p.out = out->data;
     p.counters = ws->counters; p.status = ws->status; p.partials = ws->partials;
     f.v_global = v_global; f.parts = parts; f.all_rows = (int32_t)rows;
+    f.groups = ws->groups;
+    f.q_aligned8 = reinterpret_cast<uintptr_t>(q->data) % 8 == 0 && q->stride[0] % 4 == 0 &&
+                   q->stride[1] % 4 == 0 && q->stride[2] % 4 == 0;
+    p.seg_units = fd::fp4_seg_units();
+    // work units are counted in 32 bits on the device
+    if (p.nseg * (fd::ceil_div(c.cap, p.tile) + p.seg_units) >= ((int64_t)1 << 31)) return FD_ERR_UNSUPPORTED;
 
-    int32_t G = opts->num_ctas;
+    int32_t G = opts->num_ctas < 65535 ? opts->num_ctas : 65535;
     if (G == 0) {
         const int sms = fd::sm_count_current();
         if (sms <= 0) return FD_ERR_CUDA;
-        const int64_t most = p.nseg * fd::ceil_div(c.cap, p.tile);
+        const int64_t most = p.nseg * (fd::ceil_div(c.cap, p.tile) + p.seg_units);
         const int64_t want = (int64_t)sms * fd::fp4_blocks_per_sm(part_rows);
         G = (int32_t)(want < most ? want : most);
     }

@@ -71,13 +71,19 @@ struct Cfg {
     static constexpr int MERGE = STREAMS * ROWS * (D + 4) * 4;
     static constexpr int SWAP = NH == 2 ? 2 * WARPS * NT * 1024 : 0;   // partial scores, two steps
     static constexpr int QFRAG = NH * NT * 2048;
-    static constexpr int NST = WARPS * 3 * kStage + SWAP + QFRAG <= 108 * 1024 * (3 - OCC) ? 3 : 2;
+    // The ring is apart from what the end of a piece uses: the next piece's
+    // first steps are on their way meanwhile.
+    static constexpr int TAIL = (SWAP > MERGE ? SWAP : MERGE) + QFRAG + ROWS * 4 + 2 * STREAMS * ROWS * 4 + WARPS * 12;
+    static constexpr int NST = (WARPS * 3 * kStage + TAIL + 1280) * OCC <= 228 * 1024 ? 3 : 2;
     static constexpr int RING = WARPS * NST * kStage;
-    static constexpr int BODY = RING + SWAP > MERGE ? RING + SWAP : MERGE;
-    static constexpr int SMEM = BODY + QFRAG + ROWS * 4 + WARPS * NST * 4;
-    static_assert((SMEM + 128 + 1024) * OCC <= 228 * 1024, "shared memory");
-    static_assert(QFRAG >= 2 * STREAMS * ROWS * 4, "the streams' statistics reuse the Q fragments");
+    static constexpr int SMEM = RING + TAIL;
+    static_assert((SMEM + 256 + 1024) * OCC <= 228 * 1024, "shared memory");
+    static constexpr int QROWS = (ROWS + WARPS - 1) / WARPS;   // query rows a warp prepares
 };
+
+// Pieces of a segment that are joined in groups of this many, when there are
+// more than kOneJoin of them.
+constexpr int kGroup8 = 8, kOneJoin = 12;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -131,57 +137,59 @@ struct Seg {
     int b, hp;               // sequence; kv head and part, hp = hk * parts + part
     int hk, row0, rows;      // kv head; first row of the part and its rows
     int len;
-    int64_t first, tiles;    // first partition tile and number of tiles
+    uint32_t first, tiles;   // work unit of its first tile, and number of tiles
 };
 
-// Walks the launch's tiles in order.  Every warp keeps its own copy (lane l
-// holds the tile count of sequence 32 * chunk + l), so that no barrier is
-// needed to find the next segment.
+// Walks the launch's work units in order: every segment that has tiles holds
+// p.seg_units units, the price of a piece's start and end, and then one per
+// tile.  Every warp keeps its own copy (lane l holds the tile count of sequence
+// 32 * chunk + l), so that no barrier is needed to find the next segment.
+template <int TILE>
 struct Finder {
     const Fp4Params &fp;
     int lane, chunk;
-    int64_t n;               // tiles per segment of this lane's sequence
+    uint32_t n;              // tiles per segment of this lane's sequence
     __device__ __forceinline__ Finder(const Fp4Params &f) : fp(f), lane(threadIdx.x & 31), chunk(0) { load(0); }
     __device__ __forceinline__ void load(int c) {
         chunk = c;
         const int b = c * 32 + lane;
-        n = b < fp.p.B ? ceil_div(seq_len(fp.p, b), fp.p.tile) : 0;
+        n = b < fp.p.B ? ((uint32_t)seq_len(fp.p, b) + (TILE - 1)) / TILE : 0;
     }
-    __device__ __forceinline__ int64_t total() {
-        int64_t sum = 0;
+    __device__ __forceinline__ uint32_t units() const { return n > 0 ? n + fp.p.seg_units : 0; }
+    __device__ __forceinline__ uint32_t total() {
+        uint32_t sum = 0;
         for (int c = 0; c * 32 < fp.p.B; ++c) {
             if (c != chunk) load(c);
-            sum += n;
+            sum += units();
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        return sum * fp.p.Hkv;
+        return __reduce_add_sync(0xffffffffu, sum) * (uint32_t)fp.p.Hkv;
     }
     __device__ __forceinline__ void fill(Seg &g) const {
-        g.hk = g.hp / fp.parts;
+        g.hk = fp.parts == 1 ? g.hp : g.hp / fp.parts;
         g.row0 = (g.hp - g.hk * fp.parts) * fp.p.rows;
         g.rows = min(fp.p.rows, fp.all_rows - g.row0);
     }
-    // The segment that holds tile t (below the total).
-    __device__ __forceinline__ void find(int64_t t, Seg &g) {
-        int64_t base = 0;
+    // The segment that holds unit t (below the total).
+    __device__ __forceinline__ void find(uint32_t t, Seg &g) {
+        uint32_t base = 0;
         for (int c = 0; c * 32 < fp.p.B; ++c) {
             if (c != chunk) load(c);
-            const int64_t mine = n * fp.p.Hkv;
-            int64_t upto = mine;
+            const uint32_t mine = units() * (uint32_t)fp.p.Hkv;
+            uint32_t upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
                 if (lane >= o) upto += x;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, t < base + upto);
+            const unsigned hit = __ballot_sync(0xffffffffu, t - base < upto);
             if (hit) {
                 const int src = __ffs(hit) - 1;
-                const int64_t before = base + __shfl_sync(0xffffffffu, upto - mine, src);
+                const uint32_t before = base + __shfl_sync(0xffffffffu, upto - mine, src);
                 g.tiles = __shfl_sync(0xffffffffu, n, src);
+                const uint32_t each = g.tiles + fp.p.seg_units;
                 g.b = c * 32 + src;
-                g.hp = (int)((t - before) / g.tiles);
-                g.first = before + g.hp * g.tiles;
+                g.hp = (int)((t - before) / each);
+                g.first = before + (uint32_t)g.hp * each + fp.p.seg_units;
                 g.len = (int)seq_len(fp.p, g.b);
                 fill(g);
                 return;
@@ -189,9 +197,9 @@ struct Finder {
             base += __shfl_sync(0xffffffffu, upto, 31);
         }
     }
-    // The segment after g (one exists: the caller has tiles left).
+    // The segment after g (one exists: the caller has units left).
     __device__ __forceinline__ void next(Seg &g) {
-        g.first += g.tiles;
+        g.first += g.tiles + fp.p.seg_units;
         if (++g.hp == fp.p.Hkv) {
             g.hp = 0;
             for (int c = (g.b + 1) / 32; c * 32 < fp.p.B; ++c) {
@@ -217,12 +225,13 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
     constexpr int D = C::D, NST = C::NST, ROWS = C::ROWS, STREAMS = C::STREAMS, kThreads = C::THREADS;
     const Params &p = fp.p;
     extern __shared__ __align__(128) unsigned char smem[];
+    // what the end of a piece sums, and during one the partial scores
+    float *sums = reinterpret_cast<float *>(smem + C::RING);         // [STREAMS][ROWS][D + 4]
     float4 *swap = reinterpret_cast<float4 *>(smem + C::RING);       // [2][WARPS][2 * NT][32]
-    uint4 *qfrag = reinterpret_cast<uint4 *>(smem + C::BODY);        // [NH][NT][4][32]
-    float *qmul = reinterpret_cast<float *>(smem + C::BODY + C::QFRAG);   // [ROWS]
-    uint32_t *seen = reinterpret_cast<uint32_t *>(qmul + ROWS);   // [WARPS][NST]: valid positions (paged)
-    // reference and sum of each stream's rows, once the Q fragments are done with
-    float *wm = reinterpret_cast<float *>(qfrag), *wl = wm + STREAMS * ROWS;   // [STREAMS][ROWS]
+    uint4 *qfrag = reinterpret_cast<uint4 *>(smem + C::RING + (C::SWAP > C::MERGE ? C::SWAP : C::MERGE));
+    float *qmul = reinterpret_cast<float *>(qfrag) + C::QFRAG / 4;   // qfrag: [NH][NT][4][32]; [ROWS]
+    float *wm = qmul + ROWS, *wl = wm + STREAMS * ROWS;              // each stream's references and sums
+    uint32_t *seen = reinterpret_cast<uint32_t *>(wl + STREAMS * ROWS);   // [WARPS][NST]: valid positions (paged)
     __shared__ int sh_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -258,156 +267,200 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
         }
     };
 
-    Finder finder(fp);
-    const int64_t total = finder.total();
-    // Sequences with nothing to attend still need their output rows zeroed.
-    for (int c = 0; c * 32 < p.B; ++c) {
-        if (c != finder.chunk) finder.load(c);
-        unsigned empty = __ballot_sync(0xffffffffu, finder.n == 0 && c * 32 + lane < p.B);
-        for (; empty; empty &= empty - 1) {
-            const int64_t s0 = (int64_t)(c * 32 + __ffs(empty) - 1) * p.Hkv;
-            for (int hp = (int)(((int64_t)cta - s0 % G + G) % G); hp < p.Hkv; hp += G) {
-                Seg g;
-                g.b = (int)(s0 / p.Hkv);
-                g.hp = hp;
-                finder.fill(g);
-                const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                for (int e = tid; e < g.rows * (D / 8); e += kThreads)
-                    store8(out_off(g, e / (D / 8)) + (e % (D / 8)) * 8, z);
-            }
-        }
-    }
-    if (total == 0) return;
-    const int32_t Gw = working_blocks(total, G);
-    if (cta >= Gw) return;
-    const Split sp{total, Gw};
-    const int64_t t_begin = sp.start(cta), t_end = sp.start(cta + 1);
+    Finder<C::TILE> finder(fp);
+    const uint32_t total = finder.total();
+    // Blocks [0, Gw) share the units; with few of them a block takes at least
+    // two, which costs less than one more piece to join.
+    const int32_t Gw = (int32_t)min((uint32_t)G, (total + 1) / 2);
+    if (cta >= Gw && total > 0) return;
+    // floor(c * total / Gw) in 32 bits: c and the remainder are below Gw
+    const uint32_t per = total > 0 ? total / (uint32_t)Gw : 0, rest = total - per * (uint32_t)Gw;
+    const auto begins = [&](int c) { return (uint32_t)c * per + (uint32_t)c * rest / (uint32_t)Gw; };
+    const Split sp{(int64_t)total, Gw};
+    const uint32_t t_begin = begins(cta), t_end = begins(cta + 1);
 
     unsigned char *ring = smem + warp * (NST * kStage);
     const uint32_t ring_a = smem_addr(ring);
 
-    Seg g;
-    finder.find(t_begin, g);
-    for (int64_t t = t_begin; t < t_end;) {
-        const int64_t s = (int64_t)g.b * p.Hkv + g.hp, first = g.first, nt = g.tiles;
-        const int64_t piece_end = min(t_end, first + nt);
-        const int len = g.len;
-
-        // ---- the warp's steps: step n covers positions start + n * TILE ..
-        const int start = (int)((t - first) * C::TILE) + stream * kSub;
-        const int ntile = (int)(piece_end - t);
-        // steps whose first position lies in the prefix
-        const int steps = start >= len ? 0 : min(ntile, (int)(((unsigned)(len - start) + (C::TILE - 1u)) / C::TILE));
-
-        // This lane's part of a step: 16-byte chunk lane & 3 of rows lane >> 2,
-        // + 8, .. (codes) and the scales of row `lane`.
-        const uint8_t *kb = static_cast<const uint8_t *>(p.k) + (int64_t)g.hk * p.ks[1] + half * 64 + t4 * 16;
-        const uint8_t *vb = static_cast<const uint8_t *>(p.v) + (int64_t)g.hk * p.vs[1] + half * 64 + t4 * 16;
-        const uint8_t *ksb = fp.ks + (int64_t)g.hk * fp.kss[1] + half * 8;
-        const uint8_t *vsb = fp.vs + (int64_t)g.hk * fp.vss[1] + half * 8;
+    // ---- a piece: the tiles of one segment that are this block's.  Step n of a
+    // warp covers positions start + n * TILE ..
+    const int t4x16 = t4 * 16 + half * 64;
+    const uint32_t to = ring_a + chunk_at(gid, t4);    // rows 8 further lie 512 bytes on
+    const bool runs = PAGED && (p.page_size & 7) == 0;
+    int start = 0, steps = 0, len = 0, seq = 0;
+    const uint8_t *kb = nullptr, *vb = nullptr, *ksb = nullptr, *vsb = nullptr;
+    // Page of each of a step's four runs of 8 rows (in lanes 0 .. 3), looked up
+    // a step ahead; -1 past the steps and where there is none.
+    int ahead = 0;
+    const auto lookup = [&](int n) {
+        int e = -1;
+        const int pos0 = start + n * C::TILE;
+        if (n < steps && lane < 4 && 8 * lane < len - pos0) e = page_of(p, seq, pos0 + 8 * lane);
+        return e;
+    };
+    // Copies step n into ring slot n % NST.  This lane's part: 16-byte chunk
+    // lane & 3 of rows lane >> 2, + 8, .. (codes) and the scales of row `lane`.
+    const auto fetch = [&](int n) {
+        if (n < steps) {
+            const int pos0 = start + n * C::TILE, left = len - pos0;   // positions that exist from here on
+            const int slot = n % NST;
+            const uint32_t dst = to + slot * kStage;
+            const uint32_t sd = ring_a + slot * kStage + 2 * kCode + lane * 8;
+            if (!PAGED) {
+                const int64_t far = (int64_t)n * C::TILE;
+                const uint8_t *k0 = kb + far * p.ks[2], *v0 = vb + far * p.vs[2];
+                const uint8_t *k1 = ksb + far * fp.kss[2], *v1 = vsb + far * fp.vss[2];
+                const int64_t k8 = 8 * p.ks[2], v8 = 8 * p.vs[2];
+                if (left >= kSub) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        copy16(dst + i * 512, k0 + i * k8);
+                        copy16(dst + i * 512 + kCode, v0 + i * v8);
+                    }
+                    copy8(sd, k1);
+                    copy8(sd + kScale, v1);
+                } else {   // rows past the length: zeros, from an address that exists
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool in = 8 * i + gid < left;
+                        copy16(dst + i * 512, in ? k0 + i * k8 : static_cast<const uint8_t *>(p.k), in);
+                        copy16(dst + i * 512 + kCode, in ? v0 + i * v8 : static_cast<const uint8_t *>(p.v), in);
+                    }
+                    const bool in = lane < left;
+                    copy8(sd, in ? k1 : fp.ks, in);
+                    copy8(sd + kScale, in ? v1 : fp.vs, in);
+                }
+            } else {
+                // row `lane`: its page and row in it
+                int page, row;
+                if (runs) {
+                    page = __shfl_sync(0xffffffffu, ahead, lane >> 3);
+                    row = page_row(p, pos0 + (lane & ~7)) + (lane & 7);
+                } else {
+                    page = lane < left ? page_of(p, seq, pos0 + lane) : -1;
+                    row = lane < left ? page_row(p, pos0 + lane) : 0;
+                }
+                const bool ok = lane < left && page >= 0;
+                if (page < 0) page = 0;
+                if (!ok) row = 0;
+                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+                if (lane == 0) seen[warp * NST + slot] = valid;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pg = __shfl_sync(0xffffffffu, page, 8 * i + gid);
+                    const int rw = __shfl_sync(0xffffffffu, row, 8 * i + gid);
+                    const bool in = (valid >> (8 * i + gid)) & 1u;
+                    copy16(dst + i * 512, kb + (int64_t)pg * p.ks[0] + (int64_t)rw * p.ks[2], in);
+                    copy16(dst + i * 512 + kCode, vb + (int64_t)pg * p.vs[0] + (int64_t)rw * p.vs[2], in);
+                }
+                copy8(sd, ksb + (int64_t)page * fp.kss[0] + (int64_t)row * fp.kss[2], ok);
+                copy8(sd + kScale, vsb + (int64_t)page * fp.vss[0] + (int64_t)row * fp.vss[2], ok);
+                if (runs) ahead = lookup(n + 1);
+            }
+        }
+        copy_commit();
+    };
+    // The query rows this warp prepares, as bf16 pairs.
+    uint2 qraw[C::QROWS][NH];
+    // Starts on the piece [t0, t1) of segment g: its first copies and its query.
+    const auto begin_piece = [&](const Seg &g, uint32_t t0, uint32_t t1) {
+        len = g.len;
+        seq = g.b;
+        start = (int)((t0 - g.first) * C::TILE) + stream * kSub;
+        steps = start >= len ? 0 : min((int)(t1 - t0), (int)(((unsigned)(len - start) + (C::TILE - 1u)) / C::TILE));
+        kb = static_cast<const uint8_t *>(p.k) + (int64_t)g.hk * p.ks[1] + t4x16;
+        vb = static_cast<const uint8_t *>(p.v) + (int64_t)g.hk * p.vs[1] + t4x16;
+        ksb = fp.ks + (int64_t)g.hk * fp.kss[1] + half * 8;
+        vsb = fp.vs + (int64_t)g.hk * fp.vss[1] + half * 8;
         if (!PAGED) {
             kb += (int64_t)g.b * p.ks[0] + (int64_t)(start + gid) * p.ks[2];
             vb += (int64_t)g.b * p.vs[0] + (int64_t)(start + gid) * p.vs[2];
             ksb += (int64_t)g.b * fp.kss[0] + (int64_t)(start + lane) * fp.kss[2];
             vsb += (int64_t)g.b * fp.vss[0] + (int64_t)(start + lane) * fp.vss[2];
         }
-        const uint32_t to = ring_a + chunk_at(gid, t4);    // rows 8 further lie 512 bytes on
-        // Page of each of the step's four runs of 8 rows (in lanes 0 .. 3),
-        // looked up a step ahead; -1 past the steps and where there is none.
-        const bool runs = PAGED && (p.page_size & 7) == 0;
-        const auto lookup = [&](int n) {
-            int e = -1;
-            const int at = start + n * C::TILE + 8 * lane;
-            if (n < steps && lane < 4 && 8 * lane < len - (start + n * C::TILE)) e = page_of(p, g.b, at);
-            return e;
-        };
-        int ahead = runs ? lookup(0) : 0;
-        // Copies step n into ring slot n % NST.
-        const auto fetch = [&](int n) {
-            if (n < steps) {
-                const int pos0 = start + n * C::TILE, left = len - pos0;   // positions that exist from here on
-                const int slot = n % NST;
-                const uint32_t dst = to + slot * kStage;
-                const uint32_t sd = ring_a + slot * kStage + 2 * kCode + lane * 8;
-                if (!PAGED) {
-                    const int64_t far = (int64_t)n * C::TILE;
-                    const uint8_t *k0 = kb + far * p.ks[2], *v0 = vb + far * p.vs[2];
-                    const uint8_t *k1 = ksb + far * fp.kss[2], *v1 = vsb + far * fp.vss[2];
-                    const int64_t k8 = 8 * p.ks[2], v8 = 8 * p.vs[2];
-                    if (left >= kSub) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            copy16(dst + i * 512, k0 + i * k8);
-                            copy16(dst + i * 512 + kCode, v0 + i * v8);
-                        }
-                        copy8(sd, k1);
-                        copy8(sd + kScale, v1);
-                    } else {   // rows past the length: zeros, from an address that exists
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool in = 8 * i + gid < left;
-                            copy16(dst + i * 512, in ? k0 + i * k8 : static_cast<const uint8_t *>(p.k), in);
-                            copy16(dst + i * 512 + kCode, in ? v0 + i * v8 : static_cast<const uint8_t *>(p.v), in);
-                        }
-                        const bool in = lane < left;
-                        copy8(sd, in ? k1 : fp.ks, in);
-                        copy8(sd + kScale, in ? v1 : fp.vs, in);
-                    }
-                } else {
-                    // row `lane`: its page and row in it
-                    int page, row;
-                    if (runs) {
-                        page = __shfl_sync(0xffffffffu, ahead, lane >> 3);
-                        row = page_row(p, pos0 + (lane & ~7)) + (lane & 7);
-                    } else {
-                        page = lane < left ? page_of(p, g.b, pos0 + lane) : -1;
-                        row = lane < left ? page_row(p, pos0 + lane) : 0;
-                    }
-                    const bool ok = lane < left && page >= 0;
-                    if (page < 0) page = 0;
-                    if (!ok) row = 0;
-                    const uint32_t valid = __ballot_sync(0xffffffffu, ok);
-                    if (lane == 0) seen[warp * NST + slot] = valid;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int pg = __shfl_sync(0xffffffffu, page, 8 * i + gid);
-                        const int rw = __shfl_sync(0xffffffffu, row, 8 * i + gid);
-                        const bool in = (valid >> (8 * i + gid)) & 1u;
-                        copy16(dst + i * 512, kb + (int64_t)pg * p.ks[0] + (int64_t)rw * p.ks[2], in);
-                        copy16(dst + i * 512 + kCode, vb + (int64_t)pg * p.vs[0] + (int64_t)rw * p.vs[2], in);
-                    }
-                    copy8(sd, ksb + (int64_t)page * fp.kss[0] + (int64_t)row * fp.kss[2], ok);
-                    copy8(sd + kScale, vsb + (int64_t)page * fp.vss[0] + (int64_t)row * fp.vss[2], ok);
-                    if (runs) ahead = lookup(n + 1);
-                }
-            }
-            copy_commit();
-        };
+        ahead = runs ? lookup(0) : 0;
 #pragma unroll
         for (int n = 0; n < NST - 1; ++n) fetch(n);
+#pragma unroll
+        for (int i = 0; i < C::QROWS; ++i) {
+            const int r = warp + i * C::WARPS, rr = g.row0 + r;
+            const uint16_t *src = p.q + (int64_t)g.b * p.qs[0] + (int64_t)(rr % p.n_q) * p.qs[1] +
+                                  (int64_t)(g.hk * p.g + rr / p.n_q) * p.qs[2] + lane * 4;
+#pragma unroll
+            for (int h = 0; h < NH; ++h) {
+                qraw[i][h] = make_uint2(0, 0);
+                if (r < g.rows) {
+                    if (fp.q_aligned8) qraw[i][h] = __ldg(reinterpret_cast<const uint2 *>(src + h * 128));
+                    else {
+                        const uint16_t *x = src + h * 128;
+                        qraw[i][h] = make_uint2(__ldg(x) | ((uint32_t)__ldg(x + 1) << 16),
+                                                __ldg(x + 2) | ((uint32_t)__ldg(x + 3) << 16));
+                    }
+                }
+            }
+        }
+    };
+    // The next piece of this block at or after unit t: false when there is none.
+    const auto piece_at = [&](Seg &g, uint32_t t, uint32_t &t0, uint32_t &t1) {
+        t0 = max(t, g.first);
+        t1 = min(t_end, g.first + g.tiles);
+        return t0 < t1;
+    };
 
+    Seg g;
+    uint32_t t0 = 0, t1 = 0;
+    bool more = false;
+    if (total > 0) {
+        finder.find(t_begin, g);
+        more = piece_at(g, t_begin, t0, t1);
+        if (!more && g.first + g.tiles < t_end) {   // (only the price of a segment that ends before it)
+            finder.next(g);
+            more = piece_at(g, t_begin, t0, t1);
+        }
+        if (more) begin_piece(g, t0, t1);
+    }
+    // Sequences with nothing to attend still need their output rows zeroed.
+    for (int c = 0; c * 32 < p.B; ++c) {
+        if (c != finder.chunk) finder.load(c);
+        unsigned empty = __ballot_sync(0xffffffffu, finder.n == 0 && c * 32 + lane < p.B);
+        for (; empty; empty &= empty - 1) {
+            const int b = c * 32 + __ffs(empty) - 1, Gz = total > 0 ? Gw : G;
+            const int64_t s0 = (int64_t)b * p.Hkv;
+            for (int hp = (int)(((int64_t)cta - s0 % Gz + Gz) % Gz); hp < p.Hkv; hp += Gz) {
+                Seg z;
+                z.b = b;
+                z.hp = hp;
+                finder.fill(z);
+                const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                for (int e = tid; e < z.rows * (D / 8); e += kThreads)
+                    store8(out_off(z, e / (D / 8)) + (e % (D / 8)) * 8, zero);
+            }
+        }
+    }
+
+    while (more) {
         // ---- Q: fp16 fragments and each row's factor, while K and V arrive
-        for (int r = warp; r < ROWS; r += C::WARPS) {
+#pragma unroll
+        for (int i = 0; i < C::QROWS; ++i) {
+            const int r = warp + i * C::WARPS;
+            if (r >= ROWS) break;
             float x[NH][4];
             float amax = 0.f;
-            const int rr = g.row0 + r;
-            const uint16_t *src = p.q + (int64_t)g.b * p.qs[0] + (int64_t)(rr % p.n_q) * p.qs[1] +
-                                  (int64_t)(g.hk * p.g + rr / p.n_q) * p.qs[2];
 #pragma unroll
-            for (int h = 0; h < NH; ++h)
+            for (int h = 0; h < NH; ++h) {
+                x[h][0] = bf16lo(qraw[i][h].x); x[h][1] = bf16hi(qraw[i][h].x);
+                x[h][2] = bf16lo(qraw[i][h].y); x[h][3] = bf16hi(qraw[i][h].y);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[h][e] = r < g.rows ? __uint_as_float((uint32_t)src[h * 128 + lane * 4 + e] << 16) : 0.f;
-                    amax = fmaxf(amax, fabsf(x[h][e]));
-                }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[h][e]));
+            }
+            // (of non-negative numbers: their bits order as they do)
+            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
             // 2^e <= amax < 2^(e+1); e within what 2^-e and 2^e can hold
             int e = (int)((__float_as_uint(amax) >> 23) & 255u) - 127;
             e = amax > 0.f ? max(-126, min(126, e)) : 0;
             // a negative scale turns the query instead: the factors stay >= 0
-            const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), p.scale_log2);
             // (and above 0, so that -inf stays -inf when multiplied)
+            const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), p.scale_log2);
             if (lane == 0)
                 qmul[r] = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1.1754944e-38f);
 #pragma unroll
@@ -443,12 +496,12 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             for (int w = 0; w < 4; ++w) qr[w] = qf[w * 32];
         const float2 mul1 = *reinterpret_cast<const float2 *>(qmul + 2 * t4);
 
-        for (int n0 = 0; n0 < steps; ++n0) {
+        for (int at_step = 0; at_step < steps; ++at_step) {
             copy_wait<NST - 2>();
             __syncwarp();
-            fetch(n0 + NST - 1);
-            const unsigned char *st = ring + (n0 % NST) * kStage;
-            const int pos0 = start + n0 * C::TILE;
+            fetch(at_step + NST - 1);
+            const unsigned char *st = ring + (at_step % NST) * kStage;
+            const int pos0 = start + at_step * C::TILE;
 
             // ---- S^T = K Q^T over this warp's 128 values
             float S[2][NT][4];
@@ -499,8 +552,8 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             // that follows.  Two buffers: one is written again only after the
             // next step's barrier, when the partner has read it.
             if (NH == 2) {
-                float4 *mine = swap + (((n0 & 1) * C::WARPS + warp) * (2 * NT)) * 32 + lane;
-                const float4 *theirs = swap + (((n0 & 1) * C::WARPS + (warp ^ 1)) * (2 * NT)) * 32 + lane;
+                float4 *mine = swap + (((at_step & 1) * C::WARPS + warp) * (2 * NT)) * 32 + lane;
+                const float4 *theirs = swap + (((at_step & 1) * C::WARPS + (warp ^ 1)) * (2 * NT)) * 32 + lane;
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -516,7 +569,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                     }
             }
             uint32_t valid;
-            if (PAGED) valid = seen[warp * NST + n0 % NST];
+            if (PAGED) valid = seen[warp * NST + at_step % NST];
             else valid = len - pos0 >= kSub ? 0xffffffffu : (1u << (len - pos0)) - 1u;
             const bool masked = valid != 0xffffffffu || (p.causal && pos0 + (kSub - 1) > len - p.n_q);
 
@@ -626,7 +679,16 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             __syncwarp();   // the slot may be filled again
         }
         copy_wait<0>();
-        __syncthreads();   // every warp is past its ring and the Q fragments
+
+        // ---- the next piece sets out (the ring is this warp's own)
+        const Seg now = g;
+        const uint32_t n0 = t0, n1 = t1;
+        more = t1 + p.seg_units < t_end;   // (t1 < t_end: the segment ended)
+        if (more) {
+            finder.next(g);
+            more = piece_at(g, t1, t0, t1);
+        }
+        if (more) begin_piece(g, t0, t1);
 
         // ---- the block's warps together
 #pragma unroll
@@ -641,7 +703,6 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                 }
             }
         __syncthreads();
-        float *sums = reinterpret_cast<float *>(smem);   // [STREAMS][ROWS][D + 4]
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -661,10 +722,10 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                                     O[2 * j + 1][n][c] * by, O[2 * j + 1][n][c + 2] * by);
             }
         __syncthreads();
-        const int c_first = sp.owner(first), c_last = sp.owner(first + nt - 1);
-        const bool alone = c_first == c_last;
+        const int64_t s = (int64_t)now.b * p.Hkv + now.hp;
+        const bool alone = n1 - n0 == now.tiles;
         float *slot = slot_ptr(p, s, cta);
-        for (int e = tid; e < g.rows * (D / 8); e += kThreads) {
+        for (int e = tid; e < now.rows * (D / 8); e += kThreads) {
             const int r = e / (D / 8), col = (e % (D / 8)) * 8;
             float M = kNone, L = 0.f;
 #pragma unroll
@@ -684,7 +745,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                 const float by = L > 0.f || L != L ? fp.v_global / L : 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] *= by;
-                store8(out_off(g, r) + col, o);
+                store8(out_off(now, r) + col, o);
             } else {
                 float4 *dst = reinterpret_cast<float4 *>(slot + (int64_t)r * D + col);
                 dst[0] = make_float4(o[0], o[1], o[2], o[3]);
@@ -695,76 +756,100 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                 }
             }
         }
+        if (alone) continue;
 
-        // ---- split segments: the last block to finish joins the pieces
-        if (!alone) {
+        // ---- split segments: whoever finishes last joins the pieces; many of
+        // them in two levels, groups of 8 and then the groups
+        const int c_first = sp.owner(now.first), c_last = sp.owner((int64_t)now.first + now.tiles - 1);
+        const int pieces = c_last - c_first + 1;
+        const auto last_of = [&](int32_t *counter, int of) {
             __threadfence();
             __syncthreads();
-            if (tid == 0) sh_last = atomicAdd(p.counters + s, 1) == c_last - c_first;
+            if (tid == 0) {
+                sh_last = atomicAdd(counter, 1) == of - 1;
+                if (sh_last) *counter = 0;
+            }
             __syncthreads();
-            if (sh_last) {
-                __threadfence();
-                // (row, 8 columns) items, and `ways` groups of threads that
-                // take every ways-th piece each
-                const int items = g.rows * (D / 8);
-                const int ways = max(1, kThreads / items);
-                float *part = sums;   // [ways - 1][items][10]
-                for (int e0 = 0; e0 < items; e0 += kThreads) {
-                    const int way = items < kThreads ? tid / items : 0;
-                    const int e = items < kThreads ? tid - way * items : e0 + tid;
-                    const int r = e / (D / 8), col = (e % (D / 8)) * 8;
-                    float M = kNone, L = 0.f;
-                    float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (way < ways && e < items) {
+            const bool yes = sh_last;
+            if (yes) __threadfence();
+            return yes;
+        };
+        // Joins pieces c0, c0 + step, .. (`count` of them) into the slot of
+        // c0, or into the output.
+        const auto join = [&](int c0, int step, int count, bool final) {
+            // (row, 8 columns) items, and `ways` groups of threads that take
+            // every ways-th piece each
+            const int items = now.rows * (D / 8);
+            const int ways = max(1, kThreads / items);
+            for (int e0 = 0; e0 < items; e0 += kThreads) {
+                const int way = items < kThreads ? tid / items : 0;
+                const int e = items < kThreads ? tid - way * items : e0 + tid;
+                const int r = e / (D / 8), col = (e % (D / 8)) * 8;
+                float M = kNone, L = 0.f;
+                float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (way < ways && e < items) {
 #pragma unroll 4
-                        for (int c2 = c_first + way; c2 <= c_last; c2 += ways) {
-                            const float *sl = slot_ptr(p, s, c2);
-                            const float mv = __ldcg(sl + (int64_t)p.rows * D + r);
-                            const float lv = __ldcg(sl + (int64_t)p.rows * D + p.rows + r);
-                            const float4 a = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col));
-                            const float4 b = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col + 4));
-                            const float ref = fmaxf(M, mv);
-                            const float u = fast_exp2(M - ref), w = fast_exp2(mv - ref);
-                            M = ref;
-                            L = L * u + w * lv;
-                            const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    for (int k = way; k < count; k += ways) {
+                        const float *sl = slot_ptr(p, s, c0 + k * step);
+                        const float mv = __ldcg(sl + (int64_t)p.rows * D + r);
+                        const float lv = __ldcg(sl + (int64_t)p.rows * D + p.rows + r);
+                        const float4 a = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col));
+                        const float4 b = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col + 4));
+                        const float ref = fmaxf(M, mv);
+                        const float u = fast_exp2(M - ref), w = fast_exp2(mv - ref);
+                        M = ref;
+                        L = L * u + w * lv;
+                        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * x[i];
-                        }
+                        for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * x[i];
                     }
-                    if (ways > 1) {
-                        if (way > 0 && way < ways) {
-                            float *dst = part + ((way - 1) * items + e) * 10;
-                            dst[0] = M;
-                            dst[1] = L;
+                }
+                if (way > 0 && way < ways) {
+                    float *dst = sums + ((way - 1) * items + e) * 10;   // [ways - 1][items][10]
+                    dst[0] = M;
+                    dst[1] = L;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) dst[2 + i] = o[i];
-                        }
-                        __syncthreads();
+                    for (int i = 0; i < 8; ++i) dst[2 + i] = o[i];
+                }
+                __syncthreads();
+                if (way == 0 && e < items) {
+                    for (int k = 0; k < ways - 1; ++k) {
+                        const float *src = sums + (k * items + e) * 10;
+                        const float ref = fmaxf(M, src[0]);
+                        const float u = fast_exp2(M - ref), w = fast_exp2(src[0] - ref);
+                        M = ref;
+                        L = L * u + w * src[1];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * src[2 + i];
                     }
-                    if (way == 0 && e < items) {
-                        for (int k = 0; k < ways - 1; ++k) {
-                            const float *src = part + (k * items + e) * 10;
-                            const float ref = fmaxf(M, src[0]);
-                            const float u = fast_exp2(M - ref), w = fast_exp2(src[0] - ref);
-                            M = ref;
-                            L = L * u + w * src[1];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * src[2 + i];
-                        }
+                    if (final) {
                         const float by = L > 0.f || L != L ? fp.v_global / L : 0.f;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) o[i] *= by;
-                        store8(out_off(g, r) + col, o);
+                        store8(out_off(now, r) + col, o);
+                    } else {
+                        float *sl = slot_ptr(p, s, c0);
+                        float4 *dst = reinterpret_cast<float4 *>(sl + (int64_t)r * D + col);
+                        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+                        if (col == 0) {
+                            sl[(int64_t)p.rows * D + r] = M;
+                            sl[(int64_t)p.rows * D + p.rows + r] = L;
+                        }
                     }
                 }
-                if (tid == 0) p.counters[s] = 0;
             }
-        }
-        t = piece_end;
-        if (t < t_end) {
-            finder.next(g);
-            __syncthreads();   // the sums are read before the ring is filled again
+        };
+        if (pieces <= kOneJoin) {
+            if (last_of(p.counters + s, pieces)) join(c_first, 1, pieces, true);
+        } else {
+            const int group = (cta - c_first) / kGroup8, lead = c_first + group * kGroup8;
+            const int groups = (pieces + kGroup8 - 1) / kGroup8;
+            const int size = min(kGroup8, pieces - group * kGroup8);
+            if (last_of(fp.groups + (s + lead), size)) {
+                if (size > 1) join(lead, 1, size, false);
+                if (last_of(p.counters + s, groups)) join(c_first, kGroup8, groups, true);
+            }
         }
     }
 }
@@ -799,6 +884,8 @@ int fp4_tile_tokens(int d, int rows) {
     static const int tile[4] = {Cfg<1, 1>::TILE, Cfg<1, 2>::TILE, Cfg<1, 3>::TILE, Cfg<1, 4>::TILE};
     return tile[(rows - 1) / 8] / (d / 128);   // pairs of warps at d = 256
 }
+
+int fp4_seg_units() { return 2; }
 
 int fp4_blocks_per_sm(int rows) { return rows <= 16 ? Cfg<1, 1>::OCC : Cfg<1, 3>::OCC; }
 

@@ -414,7 +414,9 @@ int fd_decode_noalloc(const fd_tensor *q, const fd_tensor *k_cache,
  * length must hold numbers: a NaN scale (fd_append_fp4 writes one for a row
  * that is not finite) reaches every query row of its kv head, those that the
  * causal window hides it from too.  Positions at or past the length and pages
- * past it are never read.  opts->kernel must be FD_KERNEL_AUTO.
+ * past it are never read.  opts->kernel must be FD_KERNEL_AUTO.  The work of a
+ * call is counted in 32 bits: FD_ERR_UNSUPPORTED where B * Hkv * cap / 96 (for
+ * both halves, where there are two) comes near 2^31.
  */
 int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_cache,
                   const fd_tensor *k_scale, const fd_tensor *v_scale, float k_global,
