@@ -10,8 +10,9 @@
 // What bounds these: a few thousand table entries and reference counts are
 // read and written, so the time is dependent loads and barriers, not bytes.
 // reserve and compact need ranks over the whole pool, hence barriers; they run
-// as one thread-block cluster, whose barrier costs far less than another
-// launch, with a warp per run of sequences and per run of pages.
+// as one block, or one thread-block cluster for large pools, whose barrier costs
+// far less than another launch, with a thread per table entry and 128 pages per
+// warp step.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -121,20 +122,29 @@ __global__ void fork_kernel(const Books k, const int32_t *src, const int32_t *ds
 }
 
 // ------------------------------------------------------------ one cluster
-// Totals that each warp of the cluster contributes, and the sums over the
-// warps before this one and over all.
-struct Totals {
-    int need, spare, copies;
+// What a thread contributes to the ranks, and the sums over the threads before
+// it and over all.
+struct __align__(16) Totals {
+    int need, spare, copies, unused;
 };
 
+__device__ __forceinline__ Totals operator+(const Totals &a, const Totals &b) {
+    return Totals{a.need + b.need, a.spare + b.spare, a.copies + b.copies, 0};
+}
+
+__device__ __forceinline__ Totals shift_up(const Totals &x, int by) {
+    return Totals{__shfl_up_sync(kAll, x.need, by), __shfl_up_sync(kAll, x.spare, by),
+                  __shfl_up_sync(kAll, x.copies, by), 0};
+}
+
 struct Cluster {
-    int rank, size, warp, warps;   // block in the cluster; warp in the cluster
+    int rank, size, thread, threads;   // block in the cluster; thread in the cluster
     __device__ __forceinline__ Cluster() {
         auto c = cg::this_cluster();
         rank = (int)c.block_rank();
         size = (int)c.num_blocks();
-        warp = rank * kWarps + (int)(threadIdx.x >> 5);
-        warps = size * kWarps;
+        thread = rank * kThreads + (int)threadIdx.x;
+        threads = size * kThreads;
     }
     __device__ __forceinline__ void sync() const {
         if (size == 1) __syncthreads();
@@ -142,31 +152,115 @@ struct Cluster {
     }
 };
 
-// Sums `mine` over the warps before this one (before) and over all (all).
-// `shared`: kWarps entries of this block; every thread of the cluster calls
-// it, `mine` is uniform over a warp.
-__device__ __forceinline__ void scan(const Cluster &c, Totals *shared, const Totals &mine,
-                                     Totals &before, Totals &all) {
+// Inclusive sums over the lanes of a warp.
+__device__ __forceinline__ Totals warp_scan(Totals x) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) shared[threadIdx.x >> 5] = mine;
-    c.sync();
-    before = all = Totals{0, 0, 0};
-    for (int r = 0; r < c.size; ++r) {
-        const Totals *t = c.size == 1 ? shared : cg::this_cluster().map_shared_rank(shared, r);
-        Totals x = t[lane], y = x;
-        if (r * kWarps + lane >= c.warp) y = Totals{0, 0, 0};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            x.need += __shfl_xor_sync(kAll, x.need, o);
-            x.spare += __shfl_xor_sync(kAll, x.spare, o);
-            x.copies += __shfl_xor_sync(kAll, x.copies, o);
-            y.need += __shfl_xor_sync(kAll, y.need, o);
-            y.spare += __shfl_xor_sync(kAll, y.spare, o);
-            y.copies += __shfl_xor_sync(kAll, y.copies, o);
-        }
-        all.need += x.need; all.spare += x.spare; all.copies += x.copies;
-        before.need += y.need; before.spare += y.spare; before.copies += y.copies;
+    for (int o = 1; o < 32; o <<= 1) {
+        const Totals y = shift_up(x, o);
+        if (lane >= o) x = x + y;
     }
+    return x;
+}
+
+__device__ __forceinline__ Totals from_lane(const Totals &x, int src) {
+    return Totals{__shfl_sync(kAll, x.need, src), __shfl_sync(kAll, x.spare, src),
+                  __shfl_sync(kAll, x.copies, src), 0};
+}
+
+// Sums `mine` over the threads before this one (before) and over all (all).
+// `at`: kWarps + 1 entries of this block's shared memory that nothing else
+// uses until the next barrier; every thread of the cluster calls it.  One
+// barrier of the block, one of the cluster, one read from each other block.
+__device__ __forceinline__ void scan(const Cluster &c, Totals *at, const Totals &mine, Totals &before,
+                                     Totals &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Totals upto = warp_scan(mine);
+    if (lane == 31) at[warp] = upto;
+    __syncthreads();
+    const Totals warps = warp_scan(at[lane]);
+    const Totals block = from_lane(warps, 31);
+    const Totals early = from_lane(warps, warp > 0 ? warp - 1 : 0);
+    before = shift_up(upto, 1);
+    if (lane == 0) before = Totals{0, 0, 0, 0};
+    if (warp > 0) before = before + early;
+    all = block;
+    if (c.size > 1) {
+        if (threadIdx.x == 0) at[kWarps] = block;
+        c.sync();
+        Totals x{0, 0, 0, 0};
+        if (lane < c.size) x = *cg::this_cluster().map_shared_rank(at + kWarps, lane);
+        x = warp_scan(x);
+        all = from_lane(x, 31);
+        if (c.rank > 0) before = before + from_lane(x, c.rank - 1);
+    }
+}
+
+// The pages of a pool in runs of 128 per warp step, four to a lane; bit i of a
+// flag word's nibble n says whether page i of this lane's four in step n is
+// free.  A warp's steps are consecutive, so ranks follow the numbers.
+struct PageRun {
+    int p0, steps;   // first page of this warp, and its steps
+    int P;
+    const int32_t *refs;
+    uint32_t kept;   // the flags, where there are at most 8 steps
+    __device__ __forceinline__ PageRun(const Books &k, const Cluster &c) : P(k.num_pages), refs(k.refs), kept(0) {
+        const int warps = c.threads / 32, warp = c.thread / 32;
+        const int all = (P + 127) / 128, per = (all + warps - 1) / warps;
+        p0 = (int)min((int64_t)P, (int64_t)warp * per * 128);
+        steps = min(per, (P - p0 + 127) / 128);
+    }
+    __device__ __forceinline__ int page(int step) const { return p0 + step * 128 + (int)(threadIdx.x & 31) * 4; }
+    // Free pages among this lane's four in `step`, as bits.
+    __device__ __forceinline__ uint32_t look(int step) const {
+        const int q = page(step);
+        int4 r = make_int4(1, 1, 1, 1);
+        if (q + 3 < P && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+            r = *reinterpret_cast<const int4 *>(refs + q);
+        } else {
+            if (q < P) r.x = refs[q];
+            if (q + 1 < P) r.y = refs[q + 1];
+            if (q + 2 < P) r.z = refs[q + 2];
+            if (q + 3 < P) r.w = refs[q + 3];
+        }
+        return (r.x <= 0 ? 1u : 0u) | (r.y <= 0 ? 2u : 0u) | (r.z <= 0 ? 4u : 0u) | (r.w <= 0 ? 8u : 0u);
+    }
+    // Free pages of this lane.
+    __device__ __forceinline__ int count() {
+        int n = 0;
+        if (steps <= 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < steps) kept |= look(i) << (4 * i);
+            n = __popc(kept);
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < steps; ++i) n += __popc(look(i));
+        }
+        return n;
+    }
+    __device__ __forceinline__ uint32_t flags(int step) const {
+        return steps <= 8 ? (kept >> (4 * step)) & 15u : look(step);
+    }
+    // Pages that exist among this lane's four.
+    __device__ __forceinline__ uint32_t real(int step) const {
+        const int left = P - page(step);
+        return left >= 4 ? 15u : (left <= 0 ? 0u : (1u << left) - 1u);
+    }
+};
+
+// Rank within the warp's step of the lowest page of this lane that `bits`
+// marks (those of one lane follow one another), and how many there are.
+__device__ __forceinline__ int step_rank(uint32_t bits, int &all) {
+    const int lane = threadIdx.x & 31, mine = __popc(bits);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += y;
+    }
+    all = __shfl_sync(kAll, upto, 31);
+    return upto - mine;
 }
 
 struct ReserveArgs {
@@ -177,143 +271,194 @@ struct ReserveArgs {
     int32_t *writers, *first, *list;   // scratch, num_pages words each
 };
 
-// Table entries [lo, hi) of sequence b that will be written, and its length.
-__device__ __forceinline__ void write_range(const ReserveArgs &a, int b, int &lo, int &hi, int64_t &L,
-                                            bool report) {
-    const Books &k = a.k;
-    const int64_t cap = (int64_t)k.max_pages * k.page_size;
-    const int64_t raw = k.lengths[b];
-    const int64_t want = a.n_new ? a.n_new[b] : a.n_each;
-    L = clamp_len(raw, cap);
-    const int64_t end = clamp_len(L + (want < 0 ? 0 : want), cap);
-    if (report && (raw != L || want < 0 || L + want > cap)) flag(k, FD_DEV_BAD_LENGTH);
-    lo = (int)(L / k.page_size);
-    hi = end > L ? pages_of(end, k.page_size) : lo;
-}
+constexpr int kSeqs = 4096;   // sequences whose ranges are looked at together
+
+// The table entries that a run of sequences will write, numbered in order:
+// entries start[b] .. start[b + 1] - 1 belong to sequence c0 + b, whose length
+// is len[b].
+struct Ranges {
+    int *start, *len;
+    int n, total;        // sequences and entries
+    int c0;
+    __device__ __forceinline__ void load(const ReserveArgs &a, int from, Totals *at, bool report) {
+        const Books &k = a.k;
+        const int64_t cap = (int64_t)k.max_pages * k.page_size;
+        c0 = from;
+        n = min(kSeqs, k.B - from);
+        __syncthreads();   // the last run's ranges are done with
+        int base = 0;
+        for (int i0 = 0; i0 < n; i0 += kThreads) {
+            const int i = i0 + (int)threadIdx.x;
+            int entries = 0;
+            if (i < n) {
+                const int64_t raw = k.lengths[from + i];
+                const int64_t want = a.n_new ? a.n_new[from + i] : a.n_each;
+                const int64_t L = clamp_len(raw, cap);
+                const int64_t end = clamp_len(L + (want < 0 ? 0 : want), cap);
+                if (report && (raw != L || want < 0 || L + want > cap)) flag(k, FD_DEV_BAD_LENGTH);
+                if (end > L) entries = pages_of(end, k.page_size) - (int)(L / k.page_size);
+                len[i] = (int)L;
+            }
+            const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+            int upto = entries;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kAll, upto, o);
+                if (lane >= o) upto += y;
+            }
+            if (lane == 31) at[warp].need = upto;
+            __syncthreads();
+            int w = at[lane].need;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kAll, w, o);
+                if (lane >= o) w += y;
+            }
+            const int before = warp > 0 ? __shfl_sync(kAll, w, warp - 1) : 0;
+            const int sum = __shfl_sync(kAll, w, 31);
+            if (i < n) start[i + 1] = base + before + upto;
+            base += sum;
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) start[0] = 0;
+        total = base;
+        __syncthreads();
+    }
+    // Calls f(entry's address, key, whether it holds positions that are kept)
+    // for this thread's entries, in order.
+    template <typename F>
+    __device__ __forceinline__ void each(const Books &k, const Cluster &c, F f) const {
+        const int per = (total + c.threads - 1) / c.threads;
+        const int64_t from = (int64_t)c.thread * per;
+        if (from >= total) return;
+        const int lo = (int)from, hi = min(total, lo + per);
+        int b = 0, top = n;   // the last sequence that starts at or before lo
+        while (top - b > 1) {
+            const int mid = (b + top) >> 1;
+            if (start[mid] <= lo) b = mid;
+            else top = mid;
+        }
+        for (int t = lo; t < hi; ++t) {
+            while (t >= start[b + 1]) ++b;
+            const int j = len[b] / k.page_size + (t - start[b]);
+            const int64_t key = (int64_t)(c0 + b) * k.max_pages + j;
+            f(k.table + key, (int)key, (int64_t)j * k.page_size < len[b]);
+        }
+    }
+};
 
 // Entries of the write ranges that name no page, or a page that others name
 // too, get pages of their own; the rest stay.  A sharer keeps the page when
 // every holder writes in this call and it is the first of them (in order of
 // sequences, then pages).
 __global__ void __launch_bounds__(kThreads) reserve_kernel(const ReserveArgs a) {
-    __shared__ Totals sums[kWarps], sums2[kWarps];
+    __shared__ Totals sums[4][kWarps + 1];
+    __shared__ int starts[kSeqs + 1], lens[kSeqs];
     const Books &k = a.k;
     const Cluster c;
-    const int lane = threadIdx.x & 31;
-    // sequences [b0, b1) and pages [p0, p1) of this warp
-    const int per_b = (k.B + c.warps - 1) / c.warps;
-    const int b0 = min(k.B, c.warp * per_b), b1 = min(k.B, b0 + per_b);
-    const int per_p = ((k.num_pages + c.warps - 1) / c.warps + 31) / 32 * 32;
-    const int p0 = (int)min((int64_t)k.num_pages, (int64_t)c.warp * per_p);
-    const int p1 = min(k.num_pages, p0 + per_p);
+    PageRun run(k, c);
+    const int spare = run.count();
+    Ranges r{starts, lens, 0, 0, 0};
+    const bool one = k.B <= kSeqs;
 
-    Totals mine{0, 0, 0}, before, all;
-    // free pages of the warp's run, and how many of its entries are shared
-    for (int q = p0; q < p1; q += 32)
-        mine.spare += __popc(__ballot_sync(kAll, q + lane < p1 && k.refs[q + lane] <= 0));
-    int shared = 0;
-    for (int b = b0; b < b1; ++b) {
-        int lo, hi;
-        int64_t L;
-        write_range(a, b, lo, hi, L, lane == 0);
-        int32_t *row = k.table + (int64_t)b * k.max_pages;
-        for (int j = lo + lane; j < hi; j += 32) {
-            const int e = row[j];
+    Totals mine{0, spare, 0, 0}, before, all;
+    for (int c0 = 0; c0 < k.B; c0 += kSeqs) {
+        r.load(a, c0, sums[0], c.rank == 0);
+        r.each(k, c, [&](int32_t *at, int, bool) {
+            const int e = *at;
             if (e < 0 || e >= k.num_pages) {
-                if (e != -1) row[j] = -1;
+                if (e != -1) *at = -1;
                 ++mine.need;
             } else if (k.refs[e] > 1) {
                 a.writers[e] = 0;
                 a.first[e] = 0x7fffffff;
-                ++shared;
+                ++mine.copies;
             }
-        }
+        });
     }
-    mine.need = __reduce_add_sync(kAll, mine.need);
-    mine.copies = __reduce_add_sync(kAll, shared);
-    scan(c, sums, mine, before, all);
+    scan(c, sums[1], mine, before, all);
     if (all.copies > 0) {
         // some written pages are shared: find each one's writers, then mark
         // the entries that part from it as -(page + 2)
-        for (int b = b0; b < b1; ++b) {
-            int lo, hi;
-            int64_t L;
-            write_range(a, b, lo, hi, L, false);
-            const int32_t *row = k.table + (int64_t)b * k.max_pages;
-            for (int j = lo + lane; j < hi; j += 32) {
-                const int e = row[j];
+        for (int c0 = 0; c0 < k.B; c0 += kSeqs) {
+            if (!one) r.load(a, c0, sums[0], false);
+            r.each(k, c, [&](int32_t *at, int key, bool) {
+                const int e = *at;
                 if (e >= 0 && k.refs[e] > 1) {
                     atomicAdd(a.writers + e, 1);
-                    atomicMin(a.first + e, (int)((int64_t)b * k.max_pages + j));
+                    atomicMin(a.first + e, key);
                 }
-            }
+            });
         }
         c.sync();
-        int parted = 0, copies = 0;
-        for (int b = b0; b < b1; ++b) {
-            int lo, hi;
-            int64_t L;
-            write_range(a, b, lo, hi, L, false);
-            int32_t *row = k.table + (int64_t)b * k.max_pages;
-            for (int j = lo + lane; j < hi; j += 32) {
-                const int e = row[j];
-                if (e < 0 || k.refs[e] <= 1) continue;
-                if (a.writers[e] == k.refs[e] && a.first[e] == (int)((int64_t)b * k.max_pages + j)) continue;
-                row[j] = -(e + 2);
-                ++parted;
-                if ((int64_t)j * k.page_size < L) ++copies;
-            }
+        mine.copies = 0;
+        for (int c0 = 0; c0 < k.B; c0 += kSeqs) {
+            if (!one) r.load(a, c0, sums[0], false);
+            r.each(k, c, [&](int32_t *at, int key, bool held) {
+                const int e = *at;
+                if (e < 0 || k.refs[e] <= 1) return;
+                if (a.writers[e] == k.refs[e] && a.first[e] == key) return;
+                *at = -(e + 2);
+                ++mine.need;
+                if (held) ++mine.copies;
+            });
         }
-        mine.need += __reduce_add_sync(kAll, parted);
-        mine.copies = __reduce_add_sync(kAll, copies);
-        scan(c, sums2, mine, before, all);
+        scan(c, sums[2], mine, before, all);
     }
     const bool fits = all.need <= all.spare;
 
     // the free pages, lowest first, as far as they are needed
-    if (fits && before.spare < all.need) {
-        int rank = before.spare;
-        for (int q = p0; q < p1 && rank < all.need; q += 32) {
-            const bool is = q + lane < p1 && k.refs[q + lane] <= 0;
-            const unsigned m = __ballot_sync(kAll, is);
-            if (is) a.list[rank + __popc(m & ((1u << lane) - 1))] = q + lane;
-            rank += __popc(m);
+    if (fits) {
+        int rank = __shfl_sync(kAll, before.spare, 0);   // of the warp's first
+        for (int i = 0; i < run.steps && rank < all.need; ++i) {
+            const uint32_t bits = run.flags(i) & run.real(i);
+            int got;
+            int at = rank + step_rank(bits, got);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if ((bits >> q) & 1u) a.list[at++] = run.page(i) + q;
+            rank += got;
         }
     }
     c.sync();
-    int rank = before.need, pair = before.copies;
-    for (int b = b0; b < b1; ++b) {
-        int lo, hi;
-        int64_t L;
-        write_range(a, b, lo, hi, L, false);
-        int32_t *row = k.table + (int64_t)b * k.max_pages;
-        for (int j0 = lo; j0 < hi; j0 += 32) {
-            const int j = j0 + lane;
-            const int e = j < hi ? row[j] : 0;
-            const bool need = e < 0;
-            const unsigned m = __ballot_sync(kAll, need);
-            const bool copy = e <= -2 && (int64_t)j * k.page_size < L;
-            const unsigned mc = __ballot_sync(kAll, copy);
-            if (need) {
-                if (!fits) {
-                    if (e <= -2) row[j] = -(e + 2);   // as it was
-                } else {
-                    const int got = a.list[rank + __popc(m & ((1u << lane) - 1))];
-                    if (e <= -2) atomicSub(k.refs - (e + 2), 1);
-                    if (copy) {
-                        const int at = pair + __popc(mc & ((1u << lane) - 1));
-                        a.pairs[2 * at] = -(e + 2);
-                        a.pairs[2 * at + 1] = got;
-                    }
-                    k.refs[got] = 1;
-                    row[j] = got;
+    Totals base{0, 0, 0, 0};   // of the runs of sequences before
+    for (int c0 = 0; c0 < k.B; c0 += kSeqs) {
+        int rank = before.need, pair = before.copies;
+        if (!one) {
+            // this run's share of the ranks
+            r.load(a, c0, sums[0], false);
+            Totals here{0, 0, 0, 0}, early, sum;
+            r.each(k, c, [&](int32_t *at, int, bool held) {
+                if (*at < 0) ++here.need;
+                if (*at <= -2 && held) ++here.copies;
+            });
+            scan(c, sums[3], here, early, sum);
+            rank = base.need + early.need;
+            pair = base.copies + early.copies;
+            base = base + sum;
+            c.sync();
+        }
+        r.each(k, c, [&](int32_t *at, int, bool held) {
+            const int e = *at;
+            if (e >= 0) return;
+            if (!fits) {
+                if (e <= -2) *at = -(e + 2);   // as it was
+                return;
+            }
+            const int got = a.list[rank++];
+            if (e <= -2) {
+                atomicSub(k.refs - (e + 2), 1);
+                if (held) {
+                    a.pairs[2 * pair] = -(e + 2);
+                    a.pairs[2 * pair + 1] = got;
+                    ++pair;
                 }
             }
-            rank += __popc(m);
-            pair += __popc(mc);
-        }
+            k.refs[got] = 1;
+            *at = got;
+        });
     }
-    if (c.warp == 0 && lane == 0) {
+    if (c.thread == 0) {
         *a.count = fits ? all.copies : -(all.need - all.spare);
         if (!fits) flag(k, FD_DEV_NO_PAGES);
     }
@@ -331,41 +476,45 @@ struct CompactArgs {
 
 // The i-th used page at or past n_used moves to the i-th free page below it.
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) {
-    __shared__ Totals sums[kWarps], sums2[kWarps];
+    __shared__ Totals sums[2][kWarps + 1];
     const Books &k = a.k;
     const Cluster c;
-    const int lane = threadIdx.x & 31;
-    const int per_p = ((k.num_pages + c.warps - 1) / c.warps + 31) / 32 * 32;
-    const int p0 = (int)min((int64_t)k.num_pages, (int64_t)c.warp * per_p);
-    const int p1 = min(k.num_pages, p0 + per_p);
-    Totals mine{0, 0, 0}, before, all;
-    for (int q = p0; q < p1; q += 32)
-        mine.need += __popc(__ballot_sync(kAll, q + lane < p1 && k.refs[q + lane] > 0));
-    scan(c, sums, mine, before, all);
-    const int used = all.need;
-    mine = Totals{0, 0, 0};
-    for (int q = p0; q < p1; q += 32) {
-        const int at = q + lane;
-        const bool in = at < p1, is = in && k.refs[at] > 0;
-        mine.spare += __popc(__ballot_sync(kAll, in && !is && at < used));
-        mine.copies += __popc(__ballot_sync(kAll, is && at >= used));
-        if (in && !is && at >= used) a.goes[at] = -1;
+    PageRun run(k, c);
+    Totals mine{0, run.count(), 0, 0}, before, all;
+    scan(c, sums[0], mine, before, all);
+    const int used = k.num_pages - all.spare;
+    // bits of the pages below `used`
+    const auto low = [&](int i) {
+        const int left = used - run.page(i);
+        return left >= 4 ? 15u : (left <= 0 ? 0u : (1u << left) - 1u);
+    };
+    mine = Totals{0, 0, 0, 0};
+    for (int i = 0; i < run.steps; ++i) {
+        const uint32_t free = run.flags(i), real = run.real(i);
+        mine.spare += __popc(free & low(i) & real);
+        mine.copies += __popc(~free & ~low(i) & real);
     }
-    scan(c, sums2, mine, before, all);
-    int hole = before.spare, mover = before.copies;
-    for (int q = p0; q < p1; q += 32) {
-        const int at = q + lane;
-        const bool in = at < p1, is = in && k.refs[at] > 0;
-        const bool h = in && !is && at < used, m = is && at >= used;
-        const unsigned bh = __ballot_sync(kAll, h), bm = __ballot_sync(kAll, m);
-        const unsigned below = (1u << lane) - 1;
-        if (h) a.holes[hole + __popc(bh & below)] = at;
-        if (m) a.movers[mover + __popc(bm & below)] = at;
-        hole += __popc(bh);
-        mover += __popc(bm);
+    scan(c, sums[1], mine, before, all);
+    int hole = __shfl_sync(kAll, before.spare, 0), mover = __shfl_sync(kAll, before.copies, 0);
+    for (int i = 0; i < run.steps; ++i) {
+        const uint32_t free = run.flags(i), real = run.real(i);
+        const uint32_t h = free & low(i) & real, m = ~free & ~low(i) & real, none = free & ~low(i) & real;
+        int got;
+        int at = hole + step_rank(h, got);
+        hole += got;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if ((h >> q) & 1u) a.holes[at++] = run.page(i) + q;
+        at = mover + step_rank(m, got);
+        mover += got;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if ((m >> q) & 1u) a.movers[at++] = run.page(i) + q;
+            if ((none >> q) & 1u) a.goes[run.page(i) + q] = -1;
+        }
     }
     c.sync();
-    for (int i = c.warp * 32 + lane; i < all.copies; i += c.warps * 32) {
+    for (int i = c.thread; i < all.copies; i += c.threads) {
         const int from = a.movers[i], to = a.holes[i];
         a.pairs[2 * i] = from;
         a.pairs[2 * i + 1] = to;
@@ -373,7 +522,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
         k.refs[to] = k.refs[from];
         k.refs[from] = 0;
     }
-    if (c.warp == 0 && lane == 0) {
+    if (c.thread == 0) {
         *a.count = all.copies;
         *a.n_used = used;
     }
@@ -450,7 +599,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     }
 }
 
-int cluster_for(const Books &k) { return k.num_pages > 4096 || k.B > 64 ? kMaxCluster : 1; }
+int cluster_for(const Books &k) { return k.num_pages > 32768 ? kMaxCluster : 1; }
 
 template <typename Args>
 int launch_cluster(void (*kernel)(const Args), const Args &a, int size, cudaStream_t st) {
