@@ -601,38 +601,49 @@ def decode_gather(q, k_cache, v_cache, idx, scale=None, out=None,
 _TENSOR = struct.Struct("Pii4q4q")     # fd_tensor
 _OPTS = struct.Struct("PPiifi2i")      # fd_opts
 _PAD = ((), (0, 0, 0), (0, 0), (0,), ())
+_I32 = torch.int32
 
 
-def _pack(t: torch.Tensor) -> bytes:
+def _pack(t: torch.Tensor, _pack4=_TENSOR.pack, _types=_DTYPES) -> bytes:
     """fd_tensor of a CUDA tensor, as bytes (a fraction of the time that a
     ctypes structure takes to fill)."""
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        raise TypeError("unsupported dtype %s" % t.dtype)
     shape = t.shape
+    if len(shape) == 4 and t.dtype in _types:
+        return _pack4(t.data_ptr(), _types[t.dtype], 4, *shape, *t.stride())
+    if t.dtype not in _types:
+        raise TypeError("unsupported dtype %s" % t.dtype)
     n = len(shape)
-    if not 1 <= n <= 4:
+    if not 1 <= n <= 3:
         raise ValueError("1 to 4 dimensions")
     pad = _PAD[n]
-    return _TENSOR.pack(t.data_ptr(), dt, n, *shape, *pad, *t.stride(), *pad)
+    return _pack4(t.data_ptr(), _types[t.dtype], n, *shape, *pad, *t.stride(), *pad)
 
 
-def _pack_opts(sh, ws, num_ctas=0) -> bytes:
-    return _OPTS.pack(sh, ws.handle.value, num_ctas, FD_KERNEL_AUTO, 0.0, 0, 0, 0)
+def _call(name, device, *args):
+    """One C call with `device` current."""
+    f = getattr(_lib or lib(), name)
+    cur = torch.cuda.current_device()
+    if cur == device.index:
+        rc = f(*args)
+    else:
+        torch.cuda.set_device(device)
+        try:
+            rc = f(*args)
+        finally:
+            torch.cuda.set_device(cur)
+    if rc != FD_OK:
+        raise FdError(rc, name)
 
 
-def _on(device, **tensors):
-    """Every tensor given lies on `device`."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s must be on %s" % (name, device))
+def _off_device(device):
+    raise ValueError("all tensors must be CUDA tensors on one device (%s)" % device)
 
 
 def _ints(t, shape, device, name) -> int:
     """Address of a contiguous int32 tensor of this shape (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous int32 %s tensor on %s" % (name, list(shape), device))
     return t.data_ptr()
 
@@ -640,10 +651,10 @@ def _ints(t, shape, device, name) -> int:
 def _table(block_table, B, device):
     if block_table is None:
         return 0, 0
-    if block_table.dim() != 2:
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != B:
         raise ValueError("block_table must be a contiguous int32 [B, max_pages] tensor")
-    max_pages = block_table.shape[1]
-    return _ints(block_table, (B, max_pages), device, "block_table"), max_pages
+    return _ints(block_table, shape, device, "block_table"), shape[1]
 
 
 def _empty(shape, dtype, device, stream):
@@ -654,10 +665,15 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _workspace(workspace, device, sh, segments=1, rows=1, ctas=1):
-    """The call's workspace: the given one, or the stream's, which has room
-    for 1024 blocks and grows with the segments."""
-    return workspace if workspace is not None else workspace_for(device, sh, segments, rows, 256, ctas)
+def _opts_for(workspace, device, stream, segments=1, rows=1, ctas=1, num_ctas=0) -> bytes:
+    """fd_opts of a call: its stream, and the given workspace or the stream's,
+    which has room for 1024 blocks and grows with the segments."""
+    sh = _stream_handle(stream, device)
+    if workspace is None:
+        workspace = _ws_cache.get((device.index, sh))
+        if workspace is None or not workspace.fits(segments, rows, 256, ctas):
+            workspace = workspace_for(device, sh, segments, rows, 256, ctas)
+    return _OPTS.pack(sh, workspace.handle.value, num_ctas, FD_KERNEL_AUTO, 0.0, 0, 0, 0)
 
 
 def decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q=None, causal=False,
@@ -672,25 +688,21 @@ def decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q=None, caus
     [num_pages, Hkv, page_size, ...], as in ``decode_paged``."""
     B, nq, Hq, d = q.shape
     device = q.device
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
-    _on(device, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out=out)
-    lens = _ints(kv_lengths, (B,), device, "kv_lengths")
-    table, max_pages = _table(block_table, B, device)
     if out is None:
         out = _empty(q.shape, out_dtype, device, stream)
+    if not (q.is_cuda and k_cache.device == device and v_cache.device == device
+            and k_scale.device == device and v_scale.device == device and out.device == device):
+        _off_device(device)
+    lens = _ints(kv_lengths, (B,), device, "kv_lengths")
+    table, max_pages = _table(block_table, B, device)
     Hkv = max(k_cache.shape[1], 1)
     rows = Hq // Hkv * nq
-    sh = _stream_handle(stream, device)
     # more than 32 rows: two halves of them
-    ws = _workspace(workspace, device, sh, B * Hkv * (2 if rows > 32 else 1), min(rows, 32), max(num_ctas, 1))
-    with _on_device(device):
-        rc = lib().fd_decode_fp4(_pack(q), _pack(k_cache), _pack(v_cache), _pack(k_scale),
-                                 _pack(v_scale), k_global, v_global, table, max_pages, lens,
-                                 nq if n_q is None else n_q, bool(causal),
-                                 1.0 / math.sqrt(d) if scale is None else scale, _pack(out),
-                                 _pack_opts(sh, ws, num_ctas))
-    _check(rc, "fd_decode_fp4")
+    _call("fd_decode_fp4", device, _pack(q), _pack(k_cache), _pack(v_cache), _pack(k_scale),
+          _pack(v_scale), k_global, v_global, table, max_pages, lens, nq if n_q is None else n_q,
+          bool(causal), 1.0 / math.sqrt(d) if scale is None else scale, _pack(out),
+          _opts_for(workspace, device, stream, B * Hkv * (2 if rows > 32 else 1), min(rows, 32),
+                    max(num_ctas, 1), num_ctas))
     return out
 
 
@@ -704,20 +716,16 @@ def append_fp4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, kv_lengths, new
     lengths with the new rows."""
     B = k_new.shape[0]
     device = k_new.device
-    if not k_new.is_cuda:
-        raise ValueError("k_new must be a CUDA tensor")
-    _on(device, v_new=v_new, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    lens = _ints(kv_lengths, (B,), device, "kv_lengths")
-    new = _ints(new_lengths, (B,), device, "new_lengths")
-    after = _ints(lengths_out, (B,), device, "lengths_out")
+    if not (k_new.is_cuda and v_new.device == device and k_cache.device == device
+            and v_cache.device == device and k_scale.device == device and v_scale.device == device):
+        _off_device(device)
+    shape = (B,)
     table, max_pages = _table(block_table, B, device)
-    sh = _stream_handle(stream, device)
-    ws = _workspace(workspace, device, sh)
-    with _on_device(device):
-        rc = lib().fd_append_fp4(_pack(k_new), _pack(v_new), new, _pack(k_cache), _pack(v_cache),
-                                 _pack(k_scale), _pack(v_scale), k_global, v_global, table,
-                                 max_pages, lens, after, _pack_opts(sh, ws))
-    _check(rc, "fd_append_fp4")
+    _call("fd_append_fp4", device, _pack(k_new), _pack(v_new),
+          _ints(new_lengths, shape, device, "new_lengths"), _pack(k_cache), _pack(v_cache),
+          _pack(k_scale), _pack(v_scale), k_global, v_global, table, max_pages,
+          _ints(kv_lengths, shape, device, "kv_lengths"),
+          _ints(lengths_out, shape, device, "lengths_out"), _opts_for(workspace, device, stream))
 
 
 def read_fp4(k_cache, v_cache, k_scale, v_scale, kv_lengths, n, start=None, k_global=1.0,
@@ -728,48 +736,39 @@ def read_fp4(k_cache, v_cache, k_scale, v_scale, kv_lengths, n, start=None, k_gl
     [B, n, Hkv, d], zeros at or past kv_lengths[b].  out: such a pair to fill."""
     B = kv_lengths.shape[0]
     device = k_cache.device
-    if not k_cache.is_cuda:
-        raise ValueError("k_cache must be a CUDA tensor")
     if out is None:
         shape = (B, int(n), k_cache.shape[1], 2 * k_cache.shape[3])
         out = (_empty(shape, out_dtype, device, stream), _empty(shape, out_dtype, device, stream))
     k, v = out
-    _on(device, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, out=k, out_v=v)
+    if not (k_cache.is_cuda and v_cache.device == device and k_scale.device == device
+            and v_scale.device == device and k.device == device and v.device == device):
+        _off_device(device)
     if k.dim() != 4 or k.shape[0] != B or k.shape[1] != n:
         raise ValueError("out must be two [B, n, Hkv, d] tensors")
-    lens = _ints(kv_lengths, (B,), device, "kv_lengths")
-    first = _ints(start, (B,), device, "start")
     table, max_pages = _table(block_table, B, device)
-    sh = _stream_handle(stream, device)
-    ws = _workspace(workspace, device, sh)
-    with _on_device(device):
-        rc = lib().fd_read_fp4(_pack(k_cache), _pack(v_cache), _pack(k_scale), _pack(v_scale),
-                               k_global, v_global, table, max_pages, first, lens, _pack(k),
-                               _pack(v), _pack_opts(sh, ws))
-    _check(rc, "fd_read_fp4")
+    _call("fd_read_fp4", device, _pack(k_cache), _pack(v_cache), _pack(k_scale), _pack(v_scale),
+          k_global, v_global, table, max_pages, _ints(start, (B,), device, "start"),
+          _ints(kv_lengths, (B,), device, "kv_lengths"), _pack(k), _pack(v),
+          _opts_for(workspace, device, stream))
     return k, v
 
 
 def _books(block_table, kv_lengths, refs):
     """Checked addresses of a paged cache's books: (device, table, B,
     max_pages, lengths, refs, num_pages)."""
-    device = block_table.device
-    if not block_table.is_cuda or block_table.dim() != 2 or refs.dim() != 1:
+    device, shape, pages = block_table.device, block_table.shape, refs.shape
+    if not block_table.is_cuda or len(shape) != 2 or len(pages) != 1:
         raise ValueError("block_table must be a CUDA [B, max_pages] tensor and refs [num_pages]")
-    B, max_pages = block_table.shape
-    num_pages = refs.shape[0]
-    return (device, _ints(block_table, (B, max_pages), device, "block_table"), B, max_pages,
-            _ints(kv_lengths, (B,), device, "kv_lengths"),
-            _ints(refs, (num_pages,), device, "refs"), num_pages)
+    B, max_pages = shape
+    return (device, _ints(block_table, shape, device, "block_table"), B, max_pages,
+            _ints(kv_lengths, (B,), device, "kv_lengths"), _ints(refs, pages, device, "refs"),
+            pages[0])
 
 
-def _pages_workspace(workspace, device, sh, num_pages):
-    if workspace is not None:
-        return workspace
+def _pages_opts(workspace, device, stream, num_pages) -> bytes:
     # room for the scratch in slots of the default 16 rows at head_dim 256,
     # beyond those of its 1024 blocks
-    extra = 3 * num_pages // slot_floats(16, 256) - 1000
-    return workspace_for(device, sh, max(extra, 1), 1, 256, 1)
+    return _opts_for(workspace, device, stream, max(3 * num_pages // slot_floats(16, 256) - 1000, 1))
 
 
 def pages_reserve(block_table, kv_lengths, refs, page_size, n_new, pairs=None, count=None,
@@ -791,13 +790,9 @@ def pages_reserve(block_table, kv_lengths, refs, page_size, n_new, pairs=None, c
         pairs = _empty((B, 2), torch.int32, device, stream)
     if count is None:
         count = _empty((1,), torch.int32, device, stream)
-    sh = _stream_handle(stream, device)
-    ws = _pages_workspace(workspace, device, sh, num_pages)
-    with _on_device(device):
-        rc = lib().fd_pages_reserve(table, B, max_pages, lens, new, each, page_size, counts,
-                                    num_pages, _ints(pairs, (B, 2), device, "pairs"),
-                                    _ints(count, (1,), device, "count"), _pack_opts(sh, ws))
-    _check(rc, "fd_pages_reserve")
+    _call("fd_pages_reserve", device, table, B, max_pages, lens, new, each, page_size, counts,
+          num_pages, _ints(pairs, (B, 2), device, "pairs"), _ints(count, (1,), device, "count"),
+          _pages_opts(workspace, device, stream, num_pages))
     return pairs, count
 
 
@@ -808,13 +803,9 @@ def pages_fork(block_table, kv_lengths, refs, page_size, src, dst, lengths=None,
     lengths is given; kv_lengths[dst[i]] follows."""
     device, table, B, max_pages, lens, counts, num_pages = _books(block_table, kv_lengths, refs)
     n = src.shape[0]
-    sh = _stream_handle(stream, device)
-    ws = _workspace(workspace, device, sh)
-    with _on_device(device):
-        rc = lib().fd_pages_fork(table, B, max_pages, lens, page_size, counts, num_pages,
-                                 _ints(src, (n,), device, "src"), _ints(dst, (n,), device, "dst"),
-                                 _ints(lengths, (n,), device, "lengths"), n, _pack_opts(sh, ws))
-    _check(rc, "fd_pages_fork")
+    _call("fd_pages_fork", device, table, B, max_pages, lens, page_size, counts, num_pages,
+          _ints(src, (n,), device, "src"), _ints(dst, (n,), device, "dst"),
+          _ints(lengths, (n,), device, "lengths"), n, _opts_for(workspace, device, stream))
 
 
 def pages_free(block_table, kv_lengths, refs, page_size, seqs=None, lengths=None, stream=None,
@@ -823,13 +814,9 @@ def pages_free(block_table, kv_lengths, refs, page_size, seqs=None, lengths=None
     [n]; None: 0) where that is less, and let go of the pages past it."""
     device, table, B, max_pages, lens, counts, num_pages = _books(block_table, kv_lengths, refs)
     n = B if seqs is None else seqs.shape[0]
-    sh = _stream_handle(stream, device)
-    ws = _workspace(workspace, device, sh)
-    with _on_device(device):
-        rc = lib().fd_pages_free(table, B, max_pages, lens, page_size, counts, num_pages,
-                                 _ints(seqs, (n,), device, "seqs"),
-                                 _ints(lengths, (n,), device, "lengths"), n, _pack_opts(sh, ws))
-    _check(rc, "fd_pages_free")
+    _call("fd_pages_free", device, table, B, max_pages, lens, page_size, counts, num_pages,
+          _ints(seqs, (n,), device, "seqs"), _ints(lengths, (n,), device, "lengths"), n,
+          _opts_for(workspace, device, stream))
 
 
 def pages_compact(block_table, refs, pairs=None, count=None, stream=None,
@@ -847,14 +834,10 @@ def pages_compact(block_table, refs, pairs=None, count=None, stream=None,
         pairs = _empty((half, 2), torch.int32, device, stream)
     if count is None:
         count = _empty((1,), torch.int32, device, stream)
-    sh = _stream_handle(stream, device)
-    ws = _pages_workspace(workspace, device, sh, num_pages)
-    with _on_device(device):
-        rc = lib().fd_pages_compact(_ints(block_table, (B, max_pages), device, "block_table"), B,
-                                    max_pages, _ints(refs, (num_pages,), device, "refs"),
-                                    num_pages, _ints(pairs, (half, 2), device, "pairs"),
-                                    _ints(count, (1,), device, "count"), _pack_opts(sh, ws))
-    _check(rc, "fd_pages_compact")
+    _call("fd_pages_compact", device, _ints(block_table, (B, max_pages), device, "block_table"), B,
+          max_pages, _ints(refs, (num_pages,), device, "refs"), num_pages,
+          _ints(pairs, (half, 2), device, "pairs"), _ints(count, (1,), device, "count"),
+          _pages_opts(workspace, device, stream, num_pages))
     return pairs, count
 
 
@@ -882,9 +865,5 @@ def pages_copy(pools, pairs, count, stream=None, workspace: Optional[Workspace] 
         pools = PagePools(pools)
     device = pools.device
     n = pairs.shape[0]
-    sh = _stream_handle(stream, device)
-    ws = _workspace(workspace, device, sh)
-    with _on_device(device):
-        rc = lib().fd_pages_copy(pools.packed, len(pools.pools), _ints(pairs, (n, 2), device, "pairs"),
-                                 _ints(count, (1,), device, "count"), n, _pack_opts(sh, ws))
-    _check(rc, "fd_pages_copy")
+    _call("fd_pages_copy", device, pools.packed, len(pools.pools), _ints(pairs, (n, 2), device, "pairs"),
+          _ints(count, (1,), device, "count"), n, _opts_for(workspace, device, stream))
