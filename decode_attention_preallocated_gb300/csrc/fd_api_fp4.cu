@@ -112,6 +112,15 @@ void fill_rows(fd::Fp4Rows *p, const fd_tensor *k, const fd_tensor *v, const fd_
     p->block_table = table;
     p->page_size = c.page_size; p->page_shift = c.page_shift; p->max_pages = c.max_pages;
     p->num_pages = c.lead;
+    p->head_shift = -1;
+    for (int sh = 0; sh < 13; ++sh)
+        if (((int64_t)1 << sh) == c.Hkv) p->head_shift = sh;
+}
+
+// Base and strides of bf16 rows are multiples of 32 bytes.
+bool aligned32(const fd_tensor *t) {
+    return reinterpret_cast<uintptr_t>(t->data) % 32 == 0 && t->stride[0] % 16 == 0 &&
+           t->stride[1] % 16 == 0 && t->stride[2] % 16 == 0;
 }
 
 // The books of a paged cache.
@@ -241,6 +250,7 @@ int fd_append_fp4(const fd_tensor *k_new, const fd_tensor *v_new, const int32_t 
     p.k_new = static_cast<const uint16_t *>(k_new->data);
     p.v_new = static_cast<const uint16_t *>(v_new->data);
     for (int i = 0; i < 3; ++i) { p.kns[i] = k_new->stride[i]; p.vns[i] = v_new->stride[i]; }
+    p.aligned32 = aligned32(k_new) && aligned32(v_new);
     p.new_lengths = new_lengths;
     p.lengths_out = lengths_out;
     p.grid = lengths_out == kv_lengths ? opts->ws->status + 34 : nullptr;
@@ -275,6 +285,7 @@ int fd_read_fp4(const fd_tensor *k_cache, const fd_tensor *v_cache, const fd_ten
     p.k_out = k_out->data; p.v_out = v_out->data;
     for (int i = 0; i < 3; ++i) { p.kos[i] = k_out->stride[i]; p.vos[i] = v_out->stride[i]; }
     p.out_f32 = k_out->dtype == FD_F32;
+    p.aligned32 = aligned32(k_out) && aligned32(v_out);
     return status_of(fd::launch_fp4_read(p, static_cast<cudaStream_t>(opts->stream)));
 }
 

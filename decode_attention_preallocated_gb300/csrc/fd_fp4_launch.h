@@ -36,6 +36,8 @@ int launch_fp4_decode(const Fp4Params &p, int num_ctas, cudaStream_t stream);
 // (fd_fp4_rows.cu).  Cache strides in bytes: [sequence or page, kv head, row].
 struct Fp4Rows {
     int32_t B, n, Hkv, d;
+    int32_t head_shift;           // log2(Hkv) where it is a power of two, else -1
+    int32_t aligned32;            // the bf16 rows' bases and strides are multiples of 32 bytes
     int64_t cap;
     uint8_t *k, *v, *ks, *vs;
     int64_t kst[3], vst[3], kss[3], vss[3];
