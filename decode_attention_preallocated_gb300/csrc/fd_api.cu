@@ -38,7 +38,7 @@ int sm_count_current() {
 namespace {
 
 constexpr int kVersion = 1;
-constexpr uint64_t kDefaultWaitNs = 2000000000ull;   // 2 s per internal wait
+using fd::kDefaultWaitNs;
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -22,6 +22,8 @@ struct fd_workspace {
 
 namespace fd {
 
+constexpr uint64_t kDefaultWaitNs = 2000000000ull;   // 2 s per internal wait
+
 inline int esize(int32_t dt) {
     switch (dt) {
         case FD_BF16: return 2;

@@ -169,8 +169,7 @@ int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor 
     if ((rc = check_opts(opts))) return rc;
 
     fd_workspace *ws = opts->ws;
-    const int max_rows = fd::fp4_max_rows((int)c.d);
-    const int parts = (int)((rows + max_rows - 1) / max_rows);
+    const int parts = (int)((rows + fd::kFp4PartRows - 1) / fd::kFp4PartRows);
     const int part_rows = (int)((rows + parts - 1) / parts);
     fd::Fp4Params f;
     memset(&f, 0, sizeof f);
@@ -201,7 +200,7 @@ int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor 
     f.groups = ws->groups;
     f.q_aligned8 = reinterpret_cast<uintptr_t>(q->data) % 8 == 0 && q->stride[0] % 4 == 0 &&
                    q->stride[1] % 4 == 0 && q->stride[2] % 4 == 0;
-    p.seg_units = fd::fp4_seg_units();
+    p.seg_units = fd::kFp4SegUnits;
     // work units are counted in 32 bits on the device
     if (p.nseg * (fd::ceil_div(c.cap, p.tile) + p.seg_units) >= ((int64_t)1 << 31)) return FD_ERR_UNSUPPORTED;
 

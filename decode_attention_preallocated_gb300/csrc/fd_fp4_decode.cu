@@ -34,22 +34,13 @@
 
 #include <atomic>
 
-#include "fd_device.cuh"
-#include "fd_fp4.cuh"
-#include "fd_fp4_launch.h"
+#include "fd_fp4_split.cuh"
 
 namespace fd {
 
 namespace {
 
 using namespace fp4;
-
-// The reference of a row is its running maximum less 4 when it was last set;
-// it is set again only when a weight would pass 2^14, which keeps every weight
-// within fp16 and spares most steps the shuffles and the rescaling.
-constexpr float kBelow = 4.f, kGrow = 14.f;
-// The reference of a row that has seen nothing yet.
-constexpr float kNone = -3.402823466e38f;
 
 constexpr int kSub = 32;               // positions per warp step
 constexpr int kCode = kSub * 64;       // a step's K (or V) codes of 128 dimensions
@@ -81,143 +72,6 @@ struct Cfg {
     static constexpr int QROWS = (ROWS + WARPS - 1) / WARPS;   // query rows a warp prepares
 };
 
-// Pieces of a segment that are joined in groups of this many, when there are
-// more than kOneJoin of them.
-constexpr int kGroup8 = 8, kOneJoin = 12;
-
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 (or 8) bytes into shared memory; with `ok`, zeros where that is false
-// (src is then not read).
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const uint8_t *src, bool ok) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-                 "r"(ok ? 8 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void mma(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                    uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
-        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t r;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
-
-// Where 16-byte chunk c of position p's 64-byte half row lies in its array.
-// Two positions share 128 bytes, and pairs of positions are rotated so that
-// the K reads (8 lanes: 2 positions x 4 chunks) and the V reads (16 lanes: 4
-// even or 4 odd positions x 2 chunks) each touch all 32 banks once.
-__device__ __forceinline__ uint32_t chunk_at(int p, int c) {
-    return (uint32_t)((p >> 1) * 128 + ((((p & 1) * 4 + c) ^ (2 * ((p >> 1) & 3))) * 16));
-}
-
-// A segment: one part of the query rows of one (sequence, kv head).
-struct Seg {
-    int b, hp;               // sequence; kv head and part, hp = hk * parts + part
-    int hk, row0, rows;      // kv head; first row of the part and its rows
-    int len;
-    uint32_t first, tiles;   // work unit of its first tile, and number of tiles
-};
-
-// Walks the launch's work units in order: every segment that has tiles holds
-// p.seg_units units, the price of a piece's start and end, and then one per
-// tile.  Every warp keeps its own copy (lane l holds the tile count of sequence
-// 32 * chunk + l), so that no barrier is needed to find the next segment.
-template <int TILE>
-struct Finder {
-    const Fp4Params &fp;
-    int lane, chunk;
-    uint32_t n;              // tiles per segment of this lane's sequence
-    __device__ __forceinline__ Finder(const Fp4Params &f) : fp(f), lane(threadIdx.x & 31), chunk(0) { load(0); }
-    __device__ __forceinline__ void load(int c) {
-        chunk = c;
-        const int b = c * 32 + lane;
-        n = b < fp.p.B ? ((uint32_t)seq_len(fp.p, b) + (TILE - 1)) / TILE : 0;
-    }
-    __device__ __forceinline__ uint32_t units() const { return n > 0 ? n + fp.p.seg_units : 0; }
-    __device__ __forceinline__ uint32_t total() {
-        uint32_t sum = 0;
-        for (int c = 0; c * 32 < fp.p.B; ++c) {
-            if (c != chunk) load(c);
-            sum += units();
-        }
-        return __reduce_add_sync(0xffffffffu, sum) * (uint32_t)fp.p.Hkv;
-    }
-    __device__ __forceinline__ void fill(Seg &g) const {
-        g.hk = fp.parts == 1 ? g.hp : g.hp / fp.parts;
-        g.row0 = (g.hp - g.hk * fp.parts) * fp.p.rows;
-        g.rows = min(fp.p.rows, fp.all_rows - g.row0);
-    }
-    // The segment that holds unit t (below the total).
-    __device__ __forceinline__ void find(uint32_t t, Seg &g) {
-        uint32_t base = 0;
-        for (int c = 0; c * 32 < fp.p.B; ++c) {
-            if (c != chunk) load(c);
-            const uint32_t mine = units() * (uint32_t)fp.p.Hkv;
-            uint32_t upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, t - base < upto);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                const uint32_t before = base + __shfl_sync(0xffffffffu, upto - mine, src);
-                g.tiles = __shfl_sync(0xffffffffu, n, src);
-                const uint32_t each = g.tiles + fp.p.seg_units;
-                g.b = c * 32 + src;
-                g.hp = (int)((t - before) / each);
-                g.first = before + (uint32_t)g.hp * each + fp.p.seg_units;
-                g.len = (int)seq_len(fp.p, g.b);
-                fill(g);
-                return;
-            }
-            base += __shfl_sync(0xffffffffu, upto, 31);
-        }
-    }
-    // The segment after g (one exists: the caller has units left).
-    __device__ __forceinline__ void next(Seg &g) {
-        g.first += g.tiles + fp.p.seg_units;
-        if (++g.hp == fp.p.Hkv) {
-            g.hp = 0;
-            for (int c = (g.b + 1) / 32; c * 32 < fp.p.B; ++c) {
-                if (c != chunk) load(c);
-                const unsigned live = __ballot_sync(0xffffffffu, n > 0 && c * 32 + lane > g.b);
-                if (live) {
-                    const int src = __ffs(live) - 1;
-                    g.b = c * 32 + src;
-                    g.tiles = __shfl_sync(0xffffffffu, n, src);
-                    break;
-                }
-            }
-            g.len = (int)seq_len(fp.p, g.b);
-        }
-        fill(g);
-    }
-};
-
 template <int NH, int NT, bool PAGED>
 __global__ void __launch_bounds__((Cfg<NH, NT>::THREADS), (Cfg<NH, NT>::OCC))
 fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
@@ -239,45 +93,10 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
     const int half = NH == 2 ? warp & 1 : 0, stream = warp / NH;
     const int G = gridDim.x, cta = blockIdx.x;
 
-    // Output pointer offset of row r of a segment.
-    const auto out_off = [&](const Seg &g, int r) {
-        const int rr = g.row0 + r;
-        return (int64_t)g.b * p.os[0] + (int64_t)(rr % p.n_q) * p.os[1] +
-               (int64_t)(g.hk * p.g + rr / p.n_q) * p.os[2];
-    };
-    const auto store8 = [&](int64_t off, const float *o) {
-        if (p.out_f32) {
-            float *dst = reinterpret_cast<float *>(p.out) + off;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = o[e];
-        } else {
-            uint16_t *dst = reinterpret_cast<uint16_t *>(p.out) + off;
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
-            if ((reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    dst[2 * e] = (uint16_t)(w[e] & 0xffffu);
-                    dst[2 * e + 1] = (uint16_t)(w[e] >> 16);
-                }
-            }
-        }
-    };
-
     Finder<C::TILE> finder(fp);
-    const uint32_t total = finder.total();
-    // Blocks [0, Gw) share the units; with few of them a block takes at least
-    // two, which costs less than one more piece to join.
-    const int32_t Gw = (int32_t)min((uint32_t)G, (total + 1) / 2);
-    if (cta >= Gw && total > 0) return;
-    // floor(c * total / Gw) in 32 bits: c and the remainder are below Gw
-    const uint32_t per = total > 0 ? total / (uint32_t)Gw : 0, rest = total - per * (uint32_t)Gw;
-    const auto begins = [&](int c) { return (uint32_t)c * per + (uint32_t)c * rest / (uint32_t)Gw; };
-    const Split sp{(int64_t)total, Gw};
-    const uint32_t t_begin = begins(cta), t_end = begins(cta + 1);
+    const Share share(finder.total(), G);
+    if (cta >= share.blocks && share.total > 0) return;
+    const uint32_t t_begin = share.begin(cta), t_end = share.begin(cta + 1);
 
     unsigned char *ring = smem + warp * (NST * kStage);
     const uint32_t ring_a = smem_addr(ring);
@@ -382,61 +201,14 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
 #pragma unroll
         for (int n = 0; n < NST - 1; ++n) fetch(n);
 #pragma unroll
-        for (int i = 0; i < C::QROWS; ++i) {
-            const int r = warp + i * C::WARPS, rr = g.row0 + r;
-            const uint16_t *src = p.q + (int64_t)g.b * p.qs[0] + (int64_t)(rr % p.n_q) * p.qs[1] +
-                                  (int64_t)(g.hk * p.g + rr / p.n_q) * p.qs[2] + lane * 4;
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                qraw[i][h] = make_uint2(0, 0);
-                if (r < g.rows) {
-                    if (fp.q_aligned8) qraw[i][h] = __ldg(reinterpret_cast<const uint2 *>(src + h * 128));
-                    else {
-                        const uint16_t *x = src + h * 128;
-                        qraw[i][h] = make_uint2(__ldg(x) | ((uint32_t)__ldg(x + 1) << 16),
-                                                __ldg(x + 2) | ((uint32_t)__ldg(x + 3) << 16));
-                    }
-                }
-            }
-        }
+        for (int i = 0; i < C::QROWS; ++i) load_query<NH>(fp, g, warp + i * C::WARPS, qraw[i]);
     };
-    // The next piece of this block at or after unit t: false when there is none.
-    const auto piece_at = [&](Seg &g, uint32_t t, uint32_t &t0, uint32_t &t1) {
-        t0 = max(t, g.first);
-        t1 = min(t_end, g.first + g.tiles);
-        return t0 < t1;
-    };
-
     Seg g;
     uint32_t t0 = 0, t1 = 0;
-    bool more = false;
-    if (total > 0) {
-        finder.find(t_begin, g);
-        more = piece_at(g, t_begin, t0, t1);
-        if (!more && g.first + g.tiles < t_end) {   // (only the price of a segment that ends before it)
-            finder.next(g);
-            more = piece_at(g, t_begin, t0, t1);
-        }
-        if (more) begin_piece(g, t0, t1);
-    }
+    bool more = share.total > 0 && first_piece(finder, t_begin, t_end, g, t0, t1);
+    if (more) begin_piece(g, t0, t1);
     // Sequences with nothing to attend still need their output rows zeroed.
-    for (int c = 0; c * 32 < p.B; ++c) {
-        if (c != finder.chunk) finder.load(c);
-        unsigned empty = __ballot_sync(0xffffffffu, finder.n == 0 && c * 32 + lane < p.B);
-        for (; empty; empty &= empty - 1) {
-            const int b = c * 32 + __ffs(empty) - 1, Gz = total > 0 ? Gw : G;
-            const int64_t s0 = (int64_t)b * p.Hkv;
-            for (int hp = (int)(((int64_t)cta - s0 % Gz + Gz) % Gz); hp < p.Hkv; hp += Gz) {
-                Seg z;
-                z.b = b;
-                z.hp = hp;
-                finder.fill(z);
-                const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                for (int e = tid; e < z.rows * (D / 8); e += kThreads)
-                    store8(out_off(z, e / (D / 8)) + (e % (D / 8)) * 8, zero);
-            }
-        }
-    }
+    zero_empty<D>(p, finder, cta, share.total > 0 ? share.blocks : G, tid, kThreads);
 
     while (more) {
         // ---- Q: fp16 fragments and each row's factor, while K and V arrive
@@ -444,33 +216,13 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
         for (int i = 0; i < C::QROWS; ++i) {
             const int r = warp + i * C::WARPS;
             if (r >= ROWS) break;
-            float x[NH][4];
-            float amax = 0.f;
+            const float factor = scale_query<NH>(p, qraw[i]);
+            if (lane == 0) qmul[r] = factor;
 #pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                x[h][0] = bf16lo(qraw[i][h].x); x[h][1] = bf16hi(qraw[i][h].x);
-                x[h][2] = bf16lo(qraw[i][h].y); x[h][3] = bf16hi(qraw[i][h].y);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[h][e]));
-            }
-            // (of non-negative numbers: their bits order as they do)
-            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-            // 2^e <= amax < 2^(e+1); e within what 2^-e and 2^e can hold
-            int e = (int)((__float_as_uint(amax) >> 23) & 255u) - 127;
-            e = amax > 0.f ? max(-126, min(126, e)) : 0;
-            // a negative scale turns the query instead: the factors stay >= 0
-            // (and above 0, so that -inf stays -inf when multiplied)
-            const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), p.scale_log2);
-            if (lane == 0)
-                qmul[r] = fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1.1754944e-38f);
-#pragma unroll
-            for (int h = 0; h < NH; ++h) {
-                const uint2 f = make_uint2(pack_f16x2(x[h][0] * down, x[h][1] * down),
-                                           pack_f16x2(x[h][2] * down, x[h][3] * down));
+            for (int h = 0; h < NH; ++h)
                 // values 4*lane .. +3 of the half: owner lane t = lane / 8, k step lane % 8
                 reinterpret_cast<uint2 *>(qfrag)[((((h * NT + (r >> 3)) * 4 + ((lane & 7) >> 1)) * 32 +
-                                                   (r & 7) * 4 + (lane >> 3)) * 2) + (lane & 1)] = f;
-            }
+                                                   (r & 7) * 4 + (lane >> 3)) * 2) + (lane & 1)] = qraw[i][h];
         }
         __syncthreads();
 
@@ -683,11 +435,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
         // ---- the next piece sets out (the ring is this warp's own)
         const Seg now = g;
         const uint32_t n0 = t0, n1 = t1;
-        more = t1 + p.seg_units < t_end;   // (t1 < t_end: the segment ended)
-        if (more) {
-            finder.next(g);
-            more = piece_at(g, t1, t0, t1);
-        }
+        more = next_piece(finder, p, t_end, g, t0, t1);
         if (more) begin_piece(g, t0, t1);
 
         // ---- the block's warps together
@@ -722,135 +470,10 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                                     O[2 * j + 1][n][c] * by, O[2 * j + 1][n][c + 2] * by);
             }
         __syncthreads();
-        const int64_t s = (int64_t)now.b * p.Hkv + now.hp;
-        const bool alone = n1 - n0 == now.tiles;
-        float *slot = slot_ptr(p, s, cta);
-        for (int e = tid; e < now.rows * (D / 8); e += kThreads) {
-            const int r = e / (D / 8), col = (e % (D / 8)) * 8;
-            float M = kNone, L = 0.f;
-#pragma unroll
-            for (int w = 0; w < STREAMS; ++w) M = fmaxf(M, wm[w * ROWS + r]);
-#pragma unroll
-            for (int w = 0; w < STREAMS; ++w) L += wl[w * ROWS + r] * fast_exp2(wm[w * ROWS + r] - M);
-            float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            const int at = (r & ~7) + (r & 1) * 4 + ((r & 7) >> 1);
-#pragma unroll
-            for (int w = 0; w < STREAMS; ++w) {
-                const float4 *src = reinterpret_cast<const float4 *>(sums + (w * ROWS + at) * (D + 4) + col);
-                const float4 a = src[0], b = src[1];
-                o[0] += a.x; o[1] += a.y; o[2] += a.z; o[3] += a.w;
-                o[4] += b.x; o[5] += b.y; o[6] += b.z; o[7] += b.w;
-            }
-            if (alone) {
-                const float by = L > 0.f || L != L ? fp.v_global / L : 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] *= by;
-                store8(out_off(now, r) + col, o);
-            } else {
-                float4 *dst = reinterpret_cast<float4 *>(slot + (int64_t)r * D + col);
-                dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-                dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-                if (col == 0) {
-                    slot[(int64_t)p.rows * D + r] = M;
-                    slot[(int64_t)p.rows * D + p.rows + r] = L;
-                }
-            }
-        }
-        if (alone) continue;
-
-        // ---- split segments: whoever finishes last joins the pieces; many of
-        // them in two levels, groups of 8 and then the groups
-        const int c_first = sp.owner(now.first), c_last = sp.owner((int64_t)now.first + now.tiles - 1);
-        const int pieces = c_last - c_first + 1;
-        const auto last_of = [&](int32_t *counter, int of) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                sh_last = atomicAdd(counter, 1) == of - 1;
-                if (sh_last) *counter = 0;
-            }
-            __syncthreads();
-            const bool yes = sh_last;
-            if (yes) __threadfence();
-            return yes;
-        };
-        // Joins pieces c0, c0 + step, .. (`count` of them) into the slot of
-        // c0, or into the output.
-        const auto join = [&](int c0, int step, int count, bool final) {
-            // (row, 8 columns) items, and `ways` groups of threads that take
-            // every ways-th piece each
-            const int items = now.rows * (D / 8);
-            const int ways = max(1, kThreads / items);
-            for (int e0 = 0; e0 < items; e0 += kThreads) {
-                const int way = items < kThreads ? tid / items : 0;
-                const int e = items < kThreads ? tid - way * items : e0 + tid;
-                const int r = e / (D / 8), col = (e % (D / 8)) * 8;
-                float M = kNone, L = 0.f;
-                float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (way < ways && e < items) {
-#pragma unroll 4
-                    for (int k = way; k < count; k += ways) {
-                        const float *sl = slot_ptr(p, s, c0 + k * step);
-                        const float mv = __ldcg(sl + (int64_t)p.rows * D + r);
-                        const float lv = __ldcg(sl + (int64_t)p.rows * D + p.rows + r);
-                        const float4 a = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col));
-                        const float4 b = __ldcg(reinterpret_cast<const float4 *>(sl + (int64_t)r * D + col + 4));
-                        const float ref = fmaxf(M, mv);
-                        const float u = fast_exp2(M - ref), w = fast_exp2(mv - ref);
-                        M = ref;
-                        L = L * u + w * lv;
-                        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * x[i];
-                    }
-                }
-                if (way > 0 && way < ways) {
-                    float *dst = sums + ((way - 1) * items + e) * 10;   // [ways - 1][items][10]
-                    dst[0] = M;
-                    dst[1] = L;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) dst[2 + i] = o[i];
-                }
-                __syncthreads();
-                if (way == 0 && e < items) {
-                    for (int k = 0; k < ways - 1; ++k) {
-                        const float *src = sums + (k * items + e) * 10;
-                        const float ref = fmaxf(M, src[0]);
-                        const float u = fast_exp2(M - ref), w = fast_exp2(src[0] - ref);
-                        M = ref;
-                        L = L * u + w * src[1];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = o[i] * u + w * src[2 + i];
-                    }
-                    if (final) {
-                        const float by = L > 0.f || L != L ? fp.v_global / L : 0.f;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] *= by;
-                        store8(out_off(now, r) + col, o);
-                    } else {
-                        float *sl = slot_ptr(p, s, c0);
-                        float4 *dst = reinterpret_cast<float4 *>(sl + (int64_t)r * D + col);
-                        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-                        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
-                        if (col == 0) {
-                            sl[(int64_t)p.rows * D + r] = M;
-                            sl[(int64_t)p.rows * D + p.rows + r] = L;
-                        }
-                    }
-                }
-            }
-        };
-        if (pieces <= kOneJoin) {
-            if (last_of(p.counters + s, pieces)) join(c_first, 1, pieces, true);
-        } else {
-            const int group = (cta - c_first) / kGroup8, lead = c_first + group * kGroup8;
-            const int groups = (pieces + kGroup8 - 1) / kGroup8;
-            const int size = min(kGroup8, pieces - group * kGroup8);
-            if (last_of(fp.groups + (s + lead), size)) {
-                if (size > 1) join(lead, 1, size, false);
-                if (last_of(p.counters + s, groups)) join(c_first, kGroup8, groups, true);
-            }
-        }
+                const bool alone = n1 - n0 == now.tiles;
+        add_streams<D, ROWS, STREAMS, kThreads>(fp, now, alone, cta, sums, wm, wl);
+        if (!alone)
+            join_pieces<D, kThreads>(fp, share, now, cta, tid, sums, &sh_last, [] { __syncthreads(); });
     }
 }
 
@@ -878,14 +501,10 @@ int launch_layout(const Fp4Params &p, int G, cudaStream_t st) {
 
 }  // namespace
 
-int fp4_max_rows(int) { return 32; }
-
 int fp4_tile_tokens(int d, int rows) {
     static const int tile[4] = {Cfg<1, 1>::TILE, Cfg<1, 2>::TILE, Cfg<1, 3>::TILE, Cfg<1, 4>::TILE};
     return tile[(rows - 1) / 8] / (d / 128);   // pairs of warps at d = 256
 }
-
-int fp4_seg_units() { return 2; }
 
 int fp4_blocks_per_sm(int rows) { return rows <= 16 ? Cfg<1, 1>::OCC : Cfg<1, 3>::OCC; }
 

@@ -22,13 +22,13 @@ struct Fp4Params {
     int32_t *groups;     // counters of the joins of 8 pieces, one per slot, zero
                          // between launches
 };
-// Rows that one part holds at most for this head_dim.
-int fp4_max_rows(int d);
-// Cache positions per tile of the partitioner, for parts of this many rows.
-int fp4_tile_tokens(int d, int rows);
+// Rows that one part holds at most.
+constexpr int kFp4PartRows = 32;
 // Work units charged for the start and end of a piece, in tiles.
-int fp4_seg_units();
-// Blocks of the kernel that an SM holds, for parts of this many rows.
+constexpr int kFp4SegUnits = 2;
+// Cache positions per tile of the partitioner, and blocks that an SM holds, for
+// parts of this many rows.
+int fp4_tile_tokens(int d, int rows);
 int fp4_blocks_per_sm(int rows);
 int launch_fp4_decode(const Fp4Params &p, int num_ctas, cudaStream_t stream);
 

@@ -696,8 +696,7 @@ def decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q=None, caus
     lens = _ints(kv_lengths, (B,), device, "kv_lengths")
     table, max_pages = _table(block_table, B, device)
     Hkv = max(k_cache.shape[1], 1)
-    rows = Hq // Hkv * nq
-    # more than 32 rows: two halves of them
+    rows = Hq // Hkv * nq   # more than 32: two halves of them
     _call("fd_decode_fp4", device, _pack(q), _pack(k_cache), _pack(v_cache), _pack(k_scale),
           _pack(v_scale), k_global, v_global, table, max_pages, lens, nq if n_q is None else n_q,
           bool(causal), 1.0 / math.sqrt(d) if scale is None else scale, _pack(out),
