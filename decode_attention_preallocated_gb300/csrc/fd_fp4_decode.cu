@@ -108,14 +108,14 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
     const bool runs = PAGED && (p.page_size & 7) == 0;
     int start = 0, steps = 0, len = 0, seq = 0;
     const uint8_t *kb = nullptr, *vb = nullptr, *ksb = nullptr, *vsb = nullptr;
-    // Page of each of a step's four runs of 8 rows (in lanes 0 .. 3), looked up
-    // a step ahead; -1 past the steps and where there is none.
-    int ahead = 0;
-    const auto lookup = [&](int n) {
-        int e = -1;
+    // Pages of the runs of 8 rows of eight steps: lane 4 * (n % 8) + i has run i
+    // of step n, -1 past the steps and where there is none.  The next eight are
+    // looked up halfway through these.
+    int pages = 0, later = 0;
+    const auto lookup = [&](int n0) {
+        const int n = n0 + (lane >> 2), i = lane & 3;
         const int pos0 = start + n * C::TILE;
-        if (n < steps && lane < 4 && 8 * lane < len - pos0) e = page_of(p, seq, pos0 + 8 * lane);
-        return e;
+        return n < steps && 8 * i < len - pos0 ? page_of(p, seq, pos0 + 8 * i) : -1;
     };
     // Copies step n into ring slot n % NST.  This lane's part: 16-byte chunk
     // lane & 3 of rows lane >> 2, + 8, .. (codes) and the scales of row `lane`.
@@ -150,31 +150,46 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                     copy8(sd + kScale, in ? v1 : fp.vs, in);
                 }
             } else {
-                // row `lane`: its page and row in it
-                int page, row;
+                uint32_t valid;
                 if (runs) {
-                    page = __shfl_sync(0xffffffffu, ahead, lane >> 3);
-                    row = page_row(p, pos0 + (lane & ~7)) + (lane & 7);
-                } else {
-                    page = lane < left ? page_of(p, seq, pos0 + lane) : -1;
-                    row = lane < left ? page_row(p, pos0 + lane) : 0;
-                }
-                const bool ok = lane < left && page >= 0;
-                if (page < 0) page = 0;
-                if (!ok) row = 0;
-                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
-                if (lane == 0) seen[warp * NST + slot] = valid;
+                    // runs of 8 rows lie on one page: four pages a step
+                    if ((n & 7) == 4) later = lookup(n + 4);
+                    if ((n & 7) == 0 && n > 0) pages = later;
+                    const int at = (n & 7) * 4;
+                    const int mine = __shfl_sync(0xffffffffu, pages, at + (lane >> 3));
+                    const bool ok = lane < left && mine >= 0;
+                    valid = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pg = __shfl_sync(0xffffffffu, page, 8 * i + gid);
-                    const int rw = __shfl_sync(0xffffffffu, row, 8 * i + gid);
-                    const bool in = (valid >> (8 * i + gid)) & 1u;
-                    copy16(dst + i * 512, kb + (int64_t)pg * p.ks[0] + (int64_t)rw * p.ks[2], in);
-                    copy16(dst + i * 512 + kCode, vb + (int64_t)pg * p.vs[0] + (int64_t)rw * p.vs[2], in);
+                    for (int i = 0; i < 4; ++i) {
+                        const int pg = __shfl_sync(0xffffffffu, pages, at + i);
+                        const int rw = page_row(p, pos0 + 8 * i) + gid;
+                        const bool in = pg >= 0 && 8 * i + gid < left;
+                        const int64_t first = in ? pg : 0, row = in ? rw : 0;
+                        copy16(dst + i * 512, kb + first * p.ks[0] + row * p.ks[2], in);
+                        copy16(dst + i * 512 + kCode, vb + first * p.vs[0] + row * p.vs[2], in);
+                    }
+                    const int64_t first = ok ? mine : 0, row = ok ? page_row(p, pos0 + (lane & ~7)) + (lane & 7) : 0;
+                    copy8(sd, ksb + first * fp.kss[0] + row * fp.kss[2], ok);
+                    copy8(sd + kScale, vsb + first * fp.vss[0] + row * fp.vss[2], ok);
+                } else {
+                    // any page size: row by row
+                    int page = lane < left ? page_of(p, seq, pos0 + lane) : -1;
+                    const bool ok = page >= 0;
+                    const int row = ok ? page_row(p, pos0 + lane) : 0;
+                    if (!ok) page = 0;
+                    valid = __ballot_sync(0xffffffffu, ok);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int pg = __shfl_sync(0xffffffffu, page, 8 * i + gid);
+                        const int rw = __shfl_sync(0xffffffffu, row, 8 * i + gid);
+                        const bool in = (valid >> (8 * i + gid)) & 1u;
+                        copy16(dst + i * 512, kb + (int64_t)pg * p.ks[0] + (int64_t)rw * p.ks[2], in);
+                        copy16(dst + i * 512 + kCode, vb + (int64_t)pg * p.vs[0] + (int64_t)rw * p.vs[2], in);
+                    }
+                    copy8(sd, ksb + (int64_t)page * fp.kss[0] + (int64_t)row * fp.kss[2], ok);
+                    copy8(sd + kScale, vsb + (int64_t)page * fp.vss[0] + (int64_t)row * fp.vss[2], ok);
                 }
-                copy8(sd, ksb + (int64_t)page * fp.kss[0] + (int64_t)row * fp.kss[2], ok);
-                copy8(sd + kScale, vsb + (int64_t)page * fp.vss[0] + (int64_t)row * fp.vss[2], ok);
-                if (runs) ahead = lookup(n + 1);
+                if (lane == 0) seen[warp * NST + slot] = valid;
             }
         }
         copy_commit();
@@ -197,7 +212,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             ksb += (int64_t)g.b * fp.kss[0] + (int64_t)(start + lane) * fp.kss[2];
             vsb += (int64_t)g.b * fp.vss[0] + (int64_t)(start + lane) * fp.vss[2];
         }
-        ahead = runs ? lookup(0) : 0;
+        if (runs) pages = lookup(0);
 #pragma unroll
         for (int n = 0; n < NST - 1; ++n) fetch(n);
 #pragma unroll

@@ -150,14 +150,18 @@ struct Finder {
     }
 };
 
+// Work units that a block takes at least.  4 rows x 4 heads over 3,000 positions
+// of a 256-wide cache: 19.4 us with 2, 18.1 with 4, 23.4 with 6.
+constexpr uint32_t kLeastUnits = 4;
+
 // The range of work units of each of the launch's working blocks.
 struct Share {
     uint32_t total, per, rest;
     int32_t blocks;          // working blocks
-    // With few units a block takes at least two, which costs less than one
-    // more piece to join.
+    // With few units a block takes at least kLeastUnits, which costs less than
+    // more pieces to join.
     __device__ __forceinline__ Share(uint32_t units, int grid)
-        : total(units), blocks(max(1, (int32_t)min((uint32_t)grid, (units + 1) / 2))) {
+        : total(units), blocks(max(1, (int32_t)min((uint32_t)grid, units / kLeastUnits))) {
         per = units > 0 ? units / (uint32_t)blocks : 0;
         rest = units - per * (uint32_t)blocks;
     }
@@ -385,7 +389,7 @@ __device__ __forceinline__ void join_pieces(const Fp4Params &fp, const Share &sh
             float M = kNone, L = 0.f;
             float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             if (way < ways && e < items) {
-#pragma unroll 4
+#pragma unroll 8
                 for (int k = way; k < count; k += ways) {
                     const float *sl = slot_ptr(p, s, c0 + k * step);
                     const float mv = __ldcg(sl + (int64_t)p.rows * D + r);
