@@ -45,7 +45,7 @@ class Books:
         rows, lens = self.table.copy(), [self._len(b) for b in range(B)]
         for i in range(n):
             s, d = int(src[i]), int(dst[i])
-            if not (0 <= s < B and 0 <= d < B) or s == d or d in list(dst[:i]):
+            if not (0 <= s < B and 0 <= d < B) or s == d or d in dst[:i]:
                 continue
             if any(src[o] == d and dst[o] != d for o in range(n) if o != i):
                 continue
@@ -97,7 +97,10 @@ class Books:
         n = len(used)
         holes = [p for p in range(n) if self.refs[p] <= 0]
         pairs = list(zip([p for p in used if p >= n], holes))
+        goes = np.arange(len(self.refs) + 1)       # the last: for entries of -1
+        goes[-1] = -1
         for a, b in pairs:
             self.refs[b], self.refs[a] = self.refs[a], 0
-            self.table[self.table == a] = b
+            goes[a] = b
+        self.table = goes[self.table].astype(np.int32)
         return pairs

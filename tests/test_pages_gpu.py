@@ -284,3 +284,25 @@ def test_serving_loop(d):
     step(9, [0, 9, 2, 9, 1])
     attend(6)
     assert books.consistent() and dev.ws.device_status() == 0
+
+
+@pytest.mark.parametrize("B,max_pages,pages,ps", [(300, 40, 50000, 8), (5000, 3, 9000, 4), (9000, 2, 40000, 3)])
+def test_large_books(B, max_pages, pages, ps):
+    """Pools large enough for the cluster, and more sequences than are looked
+    at together; shared rows, rows that are full, and a request too large."""
+    rng = np.random.default_rng(B)
+    k = random_books(rng, B, max_pages, pages, ps, share=0.2)
+    d = Dev(k)
+    for n in ([int(x) for x in rng.integers(-1, ps + 2, B)], 1):
+        d.reserve(n, k.reserve(n))
+        d.same(k)
+    assert k.consistent()
+    gone = [int(x) for x in rng.choice(B, B // 2, replace=False)]
+    k.free(gone)
+    fd.pages_free(*d.books, seqs=ints(gone), workspace=d.ws)
+    d.same(k)
+    pairs, count = fd.pages_compact(d.table, d.refs, workspace=d.ws)
+    want = k.compact()
+    assert count.item() == len(want) and pairs[:len(want)].tolist() == [list(p) for p in want]
+    d.same(k)
+    assert k.consistent()

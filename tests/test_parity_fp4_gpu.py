@@ -446,3 +446,46 @@ def test_other_scales(scale):
         got = fd.decode_fp4(q.cuda(), kd, vd, ksd, vsd, ints([150, 2]), causal=True, scale=scale, out_dtype=F32)
         want, weight, size = fp4.decode(q.double().numpy(), k, v, ks, vs, [150, 2], True, scale)
         check(got, want, decode_bound(want, weight, size, 150, np.abs(fp4.values(v, vs)).max(), F32), "scale")
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n_q,g", [(6, 4), (4, 8), (6, 10)])
+@pytest.mark.parametrize("ctas", [0, 1, 5, 60])
+def test_many_rows_split(d, n_q, g, ctas):
+    # 24, 32 and 60 rows (two parts) over several pieces
+    decode_case(40, 2, n_q, 2 * g, 2, d, 1500, [1500, 333], True, num_ctas=ctas, out_dtype=F32)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("page", [8, 24, 11])
+@pytest.mark.parametrize("n_q,g", [(1, 4), (3, 4), (6, 4), (5, 8)])
+def test_rows_and_pages(d, page, n_q, g):
+    # runs of eight rows on a page, and pages that end inside one
+    decode_case(41, 2, n_q, 2 * g, 2, d, 700 // page * page + page, [700, 95], n_q > 1, page=page, kg=0.5)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("ctas", [0, 1, 9, 200])
+def test_a_large_batch_with_empty_sequences(d, ctas):
+    # more sequences than a warp has lanes, some of them empty (the first and
+    # the last too), many of less than a tile
+    rng = np.random.default_rng(42)
+    lengths = [int(x) for x in rng.integers(0, 400, 70)]
+    for b in (0, 5, 31, 32, 33, 64, 69):
+        lengths[b] = 0
+    got, _, _ = decode_case(43, 70, 2, 2, 1, d, 400, lengths, True, num_ctas=ctas)
+    for b in (0, 5, 31, 32, 33, 64, 69):
+        assert not got[b].any()
+
+
+def test_all_sequences_empty():
+    got, _, _ = decode_case(44, 40, 1, 4, 2, 128, 64, [0] * 40, False)
+    assert not got.any()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("rows", [1, 16, 24])
+def test_many_pieces_of_one_segment(d, rows):
+    # one kv head over every block: joined in two levels
+    decode_case(45, 1, 1, rows, 1, d, 30000, [29999], False, out_dtype=F32, num_ctas=150)
+    decode_case(45, 1, 1, rows, 1, d, 6000, [5999], False, out_dtype=F32, num_ctas=13)
