@@ -267,7 +267,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             copy_wait<NST - 2>();
             __syncwarp();
             fetch(at_step + NST - 1);
-            const unsigned char *st = ring + (at_step % NST) * kStage;
+            unsigned char *st = ring + (at_step % NST) * kStage;
             const int pos0 = start + at_step * C::TILE;
 
             // ---- S^T = K Q^T over this warp's 128 values
@@ -408,6 +408,36 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                     P[m][n][1] = transpose8x8(pack_f16x2(w2, w3));
                 }
 
+            // A weight of 0 does not hide a NaN: where the window hides positions
+            // from some rows, NaN scales of V become 0 and what they stand for
+            // goes to the sums of the rows that see them.
+            if (masked && p.causal) {
+                uint2 *mine = reinterpret_cast<uint2 *>(st + 2 * kCode + kScale) + lane;
+                const uint2 s8 = *mine;
+                const uint2 hit = make_uint2(__vcmpeq4(s8.x & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                                             __vcmpeq4(s8.y & 0x7f7f7f7fu, 0x7f7f7f7fu));
+                if (__any_sync(0xffffffffu, (hit.x | hit.y) != 0)) {
+                    uint32_t bad = 0;   // positions of this lane's 16 dimensions
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t at = __ballot_sync(0xffffffffu, (((i < 4 ? hit.x : hit.y) >> (8 * (i & 3))) & 1u) != 0);
+                        if (gid == i) bad = at;
+                    }
+                    *mine = make_uint2(s8.x & ~hit.x, s8.y & ~hit.y);
+                    __syncwarp();
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int see = len - p.n_q + (g.row0 + n * 8 + 2 * t4 + c) % p.n_q + 1 - pos0;
+                            const uint32_t seen_at = see >= kSub ? 0xffffffffu : see > 0 ? (1u << see) - 1u : 0u;
+                            if (bad & valid & seen_at)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) O[j][n][c] = O[j][n][c + 2] = __uint_as_float(0x7fffffffu);
+                        }
+                }
+            }
+
             // ---- O^T += V^T P^T over this warp's 128 dimensions
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
@@ -485,7 +515,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                                     O[2 * j + 1][n][c] * by, O[2 * j + 1][n][c + 2] * by);
             }
         __syncthreads();
-                const bool alone = n1 - n0 == now.tiles;
+        const bool alone = n1 - n0 == now.tiles;
         add_streams<D, ROWS, STREAMS, kThreads>(fp, now, alone, cta, sums, wm, wl);
         if (!alone)
             join_pieces<D, kThreads>(fp, share, now, cta, tid, sums, &sh_last, [] { __syncthreads(); });

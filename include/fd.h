@@ -410,11 +410,11 @@ int fd_decode_noalloc(const fd_tensor *q, const fd_tensor *k_cache,
  * The scores and all sums are fp32 over exact products of the codes, the
  * scales and q (an entry of q below 2^-14 of its row's largest is off by up
  * to 2^-25 of that); each softmax weight is rounded to fp16, i.e. by up to
- * 2^-11 of itself or 2^-29 of the row's largest weight.  Positions below the
- * length must hold numbers: a NaN scale (fd_append_fp4 writes one for a row
- * that is not finite) reaches every query row of its kv head, those that the
- * causal window hides it from too.  Positions at or past the length and pages
- * past it are never read.  opts->kernel must be FD_KERNEL_AUTO.  The work of a
+ * 2^-11 of itself or 2^-29 of the row's largest weight.  A NaN scale
+ * (fd_append_fp4 writes one for a row that is not finite) makes NaN of what
+ * it stands for in the query rows that see its position, and reaches no
+ * other.  Positions at or past the length and pages past it are never read.
+ * opts->kernel must be FD_KERNEL_AUTO.  The work of a
  * call is counted in 32 bits: FD_ERR_UNSUPPORTED where B * Hkv * cap / 96 (for
  * both halves, where there are two) comes near 2^31.
  */

@@ -489,3 +489,32 @@ def test_many_pieces_of_one_segment(d, rows):
     # one kv head over every block: joined in two levels
     decode_case(45, 1, 1, rows, 1, d, 30000, [29999], False, out_dtype=F32, num_ctas=150)
     decode_case(45, 1, 1, rows, 1, d, 6000, [5999], False, out_dtype=F32, num_ctas=13)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("page", [0, 16, 11])
+@pytest.mark.parametrize("n_q,g", [(6, 1), (3, 4), (4, 6), (6, 5), (5, 8)])
+@pytest.mark.parametrize("hole", ["k", "v"])
+def test_nan_hidden_by_the_window(d, page, n_q, g, hole):
+    rng = np.random.default_rng(61)
+    lengths, cap = [301, 96, 4], 304
+    mp = -(-cap // page) if page else 0
+    table = scattered(rng, 3, mp) if page else None
+    lead, rows = (3 * mp + 3, page) if page else (3, cap)
+    (k, ks), (v, vs) = (cache(rng, lead, 2, rows, d) for _ in range(2))
+    bad = ks if hole == "k" else vs
+    for b, L in enumerate(lengths):
+        for back, group, value in ((1, 0, 0x7F), (2, 3, 0xFF), (2, d // 16 - 1, 0x7F)):   # the last two positions
+            at = (table[b, (L - back) // page], 0, (L - back) % page) if page else (b, 0, L - back)
+            bad[at + (group,)] = value
+    q = bf16(rng, (3, n_q, 2 * g, d))
+    want, weight, size = fp4.decode(q.double().numpy(), k, v, ks, vs, lengths, True, scale_of(d), block_table=table)
+    (kd, ksd), (vd, vsd) = to_dev(k, ks), to_dev(v, vs)
+    got = fd.decode_fp4(q.cuda(), kd, vd, ksd, vsd, ints(lengths), causal=True, out_dtype=F32,
+                        block_table=None if table is None else torch.from_numpy(table).cuda()).cpu()
+    nan = np.isnan(want)
+    assert nan[:, -2:, :g].any() and not nan[:, :-2].any() and not nan[:, :, g:].any()
+    assert (torch.isnan(got).numpy() == nan).all()
+    top = np.nan_to_num(np.abs(fp4.values(v, vs))).max()
+    clean = [np.where(np.isnan(x), 0, x) for x in (want, weight)] + [np.nan_to_num(size)]
+    check(torch.nan_to_num(got), clean[0], decode_bound(clean[0], clean[1], clean[2], 301, top, F32), "hidden")
