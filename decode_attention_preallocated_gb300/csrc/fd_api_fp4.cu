@@ -112,9 +112,6 @@ void fill_rows(fd::Fp4Rows *p, const fd_tensor *k, const fd_tensor *v, const fd_
     p->block_table = table;
     p->page_size = c.page_size; p->page_shift = c.page_shift; p->max_pages = c.max_pages;
     p->num_pages = c.lead;
-    p->head_shift = -1;
-    for (int sh = 0; sh < 13; ++sh)
-        if (((int64_t)1 << sh) == c.Hkv) p->head_shift = sh;
 }
 
 // Base and strides of bf16 rows are multiples of 32 bytes.

@@ -36,9 +36,12 @@ int launch_fp4_decode(const Fp4Params &p, int num_ctas, cudaStream_t stream);
 // (fd_fp4_rows.cu).  Cache strides in bytes: [sequence or page, kv head, row].
 struct Fp4Rows {
     int32_t B, n, Hkv, d;
-    int32_t head_shift;           // log2(Hkv) where it is a power of two, else -1
     int32_t aligned32;            // the bf16 rows' bases and strides are multiples of 32 bytes
     int64_t cap;
+    // (row, kv head) units per block, and how far the units of one thread lie
+    // apart; set by the launch
+    int64_t span;
+    int32_t step_i, step_hk;
     uint8_t *k, *v, *ks, *vs;
     int64_t kst[3], vst[3], kss[3], vss[3];
     float k_global, v_global;
@@ -63,7 +66,7 @@ struct Fp4Rows {
     int64_t kos[3], vos[3];
     int32_t out_f32;
 };
-int launch_fp4_append(const Fp4Rows &p, cudaStream_t stream);
-int launch_fp4_read(const Fp4Rows &p, cudaStream_t stream);
+int launch_fp4_append(Fp4Rows p, cudaStream_t stream);
+int launch_fp4_read(Fp4Rows p, cudaStream_t stream);
 
 }  // namespace fd
