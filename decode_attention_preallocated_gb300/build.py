@@ -1,7 +1,8 @@
 """Build libfd.so in-tree with nvcc for sm_103a (GB300).
 
 Each ``csrc/*.cu`` file compiles to an object in parallel, then one link
-step makes ``libfd.so`` next to this file.  The CUDA runtime is linked
+step makes ``libfd.so`` next to this file; ``csrc/fd_torch.cpp``, the marshalling
+extension of ``fd.py``, becomes ``_fd_torch.so`` with g++ at the same time.  The CUDA runtime is linked
 statically, so loading the library needs no libcudart on the search path.
 """
 from __future__ import annotations
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfd.so")
+NATIVE_SRC = os.path.join(CSRC, "fd_torch.cpp")
+NATIVE = os.path.join(HERE, "_fd_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", "--expt-relaxed-constexpr",
@@ -41,15 +45,39 @@ def _deps():
         glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "fd.h"), __file__]
 
 
+def _newer(out, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps())
+
+
+def build_native(force: bool = False) -> str:
+    """The marshalling extension, against the headers and libraries of the
+    installed PyTorch."""
+    if not force and _newer(NATIVE, [NATIVE_SRC, os.path.join(INCLUDE, "fd.h"), __file__]):
+        return NATIVE
+    import torch
+    home = os.path.dirname(torch.__file__)
+    include = os.path.join(home, "include")
+    tmp = NATIVE + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", include,
+           "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           NATIVE_SRC, "-o", tmp, "-L", os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed on %s:\n%s%s" % (cmd[0], NATIVE_SRC, r.stdout, r.stderr))
+    os.replace(tmp, NATIVE)
+    return NATIVE
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and up_to_date():
+        build_native()
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
@@ -65,8 +93,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        native = ex.submit(build_native, force)
         objs = list(ex.map(compile_one, srcs))
+        native.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -21,6 +21,8 @@ workspace per (device, stream).
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import struct
@@ -31,6 +33,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfd.so")
+NATIVE_PATH = os.path.join(_HERE, "_fd_torch.so")
 
 # constants from include/fd.h
 FD_OK, FD_ERR_ARG, FD_ERR_UNSUPPORTED, FD_ERR_ALIGN, FD_ERR_WORKSPACE, FD_ERR_CUDA = 0, -1, -2, -3, -4, -5
@@ -102,8 +105,8 @@ _SIGNATURES = [
     ("fd_decode_noalloc", ctypes.c_int,
      [_P(FdTensor), _P(FdTensor), _P(FdTensor), ctypes.c_void_p, ctypes.c_int32,
       ctypes.c_int32, ctypes.c_float, _P(FdTensor), ctypes.c_void_p, ctypes.c_int32]),
-    # the 4-bit cache and the page calls take their descriptors as packed
-    # bytes (or any pointer): see _pack
+    # the 4-bit cache and the page calls are called through the marshalling
+    # extension; here they take descriptors as bytes or any pointer
     ("fd_decode_fp4", ctypes.c_int,
      [ctypes.c_void_p] * 5 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_int32,
                               ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
@@ -601,12 +604,10 @@ def decode_gather(q, k_cache, v_cache, idx, scale=None, out=None,
 _TENSOR = struct.Struct("Pii4q4q")     # fd_tensor
 _OPTS = struct.Struct("PPiifi2i")      # fd_opts
 _PAD = ((), (0, 0, 0), (0, 0), (0,), ())
-_I32 = torch.int32
 
 
 def _pack(t: torch.Tensor, _pack4=_TENSOR.pack, _types=_DTYPES) -> bytes:
-    """fd_tensor of a CUDA tensor, as bytes (a fraction of the time that a
-    ctypes structure takes to fill)."""
+    """fd_tensor of a tensor, as bytes."""
     shape = t.shape
     if len(shape) == 4 and t.dtype in _types:
         return _pack4(t.data_ptr(), _types[t.dtype], 4, *shape, *t.stride())
@@ -619,61 +620,49 @@ def _pack(t: torch.Tensor, _pack4=_TENSOR.pack, _types=_DTYPES) -> bytes:
     return _pack4(t.data_ptr(), _types[t.dtype], n, *shape, *pad, *t.stride(), *pad)
 
 
-def _call(name, device, *args):
-    """One C call with `device` current."""
-    f = getattr(_lib or lib(), name)
-    cur = torch.cuda.current_device()
-    if cur == device.index:
-        rc = f(*args)
-    else:
-        torch.cuda.set_device(device)
-        try:
-            rc = f(*args)
-        finally:
-            torch.cuda.set_device(cur)
-    if rc != FD_OK:
-        raise FdError(rc, name)
-
-
-def _off_device(device):
-    raise ValueError("all tensors must be CUDA tensors on one device (%s)" % device)
-
-
-def _ints(t, shape, device, name) -> int:
-    """Address of a contiguous int32 tensor of this shape (0 for None)."""
-    if t is None:
-        return 0
-    if t.dtype is not _I32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 %s tensor on %s" % (name, list(shape), device))
-    return t.data_ptr()
-
-
-def _table(block_table, B, device):
-    if block_table is None:
-        return 0, 0
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != B:
-        raise ValueError("block_table must be a contiguous int32 [B, max_pages] tensor")
-    return _ints(block_table, shape, device, "block_table"), shape[1]
-
-
-def _empty(shape, dtype, device, stream):
-    """New memory that belongs to the stream the call runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _empty(shape, dtype, index, stream):
+    """New memory that belongs to the given stream."""
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
 
 
-def _opts_for(workspace, device, stream, segments=1, rows=1, ctas=1, num_ctas=0) -> bytes:
+def _opts_for(workspace, index, stream, segments, rows, ctas, num_ctas) -> bytes:
     """fd_opts of a call: its stream, and the given workspace or the stream's,
     which has room for 1024 blocks and grows with the segments."""
+    device = torch.device("cuda", index)
     sh = _stream_handle(stream, device)
     if workspace is None:
-        workspace = _ws_cache.get((device.index, sh))
-        if workspace is None or not workspace.fits(segments, rows, 256, ctas):
-            workspace = workspace_for(device, sh, segments, rows, 256, ctas)
+        workspace = workspace_for(device, sh, segments, rows, 256, ctas)
     return _OPTS.pack(sh, workspace.handle.value, num_ctas, FD_KERNEL_AUTO, 0.0, 0, 0, 0)
+
+
+class _Unloaded:
+    """Stands for the marshalling extension (csrc/fd_torch.cpp) until the first
+    call, which loads it and libfd.so."""
+
+    def __getattr__(self, name):
+        global _native
+        with _native_lock:
+            if _native is self:
+                _native = self.load()
+        return getattr(_native, name)
+
+    @staticmethod
+    def load():
+        if not os.path.exists(NATIVE_PATH):
+            raise ImportError("%s is missing: build it first" % NATIVE_PATH)
+        loader = importlib.machinery.ExtensionFileLoader("_fd_torch", NATIVE_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fd_torch", loader))
+        loader.exec_module(m)
+        calls = ("fd_decode_fp4", "fd_append_fp4", "fd_read_fp4", "fd_pages_reserve", "fd_pages_fork",
+                 "fd_pages_free", "fd_pages_compact", "fd_pages_copy")
+        m.bind(tuple(ctypes.cast(getattr(lib(), c), ctypes.c_void_p).value for c in calls),
+               _ws_cache, _opts_for, _empty, FdError)
+        return m
+
+
+_native = _Unloaded()
+_native_lock = threading.Lock()
 
 
 def decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q=None, causal=False,
@@ -686,23 +675,9 @@ def decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q=None, caus
     values); a value is code * scale * k_global (v_global).  With block_table
     [B, max_pages] (int32, contiguous) the four are pools
     [num_pages, Hkv, page_size, ...], as in ``decode_paged``."""
-    B, nq, Hq, d = q.shape
-    device = q.device
-    if out is None:
-        out = _empty(q.shape, out_dtype, device, stream)
-    if not (q.is_cuda and k_cache.device == device and v_cache.device == device
-            and k_scale.device == device and v_scale.device == device and out.device == device):
-        _off_device(device)
-    lens = _ints(kv_lengths, (B,), device, "kv_lengths")
-    table, max_pages = _table(block_table, B, device)
-    Hkv = max(k_cache.shape[1], 1)
-    rows = Hq // Hkv * nq   # more than 32: two halves of them
-    _call("fd_decode_fp4", device, _pack(q), _pack(k_cache), _pack(v_cache), _pack(k_scale),
-          _pack(v_scale), k_global, v_global, table, max_pages, lens, nq if n_q is None else n_q,
-          bool(causal), 1.0 / math.sqrt(d) if scale is None else scale, _pack(out),
-          _opts_for(workspace, device, stream, B * Hkv * (2 if rows > 32 else 1), min(rows, 32),
-                    max(num_ctas, 1), num_ctas))
-    return out
+    return _native.decode_fp4(q, k_cache, v_cache, k_scale, v_scale, kv_lengths, n_q, causal, scale,
+                              k_global, v_global, block_table, out, out_dtype, num_ctas, stream,
+                              workspace)
 
 
 def append_fp4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, kv_lengths, new_lengths=None,
@@ -713,18 +688,8 @@ def append_fp4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, kv_lengths, new
     new_lengths[b] - 1 (int32 [B]; None: n for every sequence; rows past it
     are padding).  lengths_out (int32 [B], may be kv_lengths) receives the
     lengths with the new rows."""
-    B = k_new.shape[0]
-    device = k_new.device
-    if not (k_new.is_cuda and v_new.device == device and k_cache.device == device
-            and v_cache.device == device and k_scale.device == device and v_scale.device == device):
-        _off_device(device)
-    shape = (B,)
-    table, max_pages = _table(block_table, B, device)
-    _call("fd_append_fp4", device, _pack(k_new), _pack(v_new),
-          _ints(new_lengths, shape, device, "new_lengths"), _pack(k_cache), _pack(v_cache),
-          _pack(k_scale), _pack(v_scale), k_global, v_global, table, max_pages,
-          _ints(kv_lengths, shape, device, "kv_lengths"),
-          _ints(lengths_out, shape, device, "lengths_out"), _opts_for(workspace, device, stream))
+    _native.append_fp4(k_new, v_new, k_cache, v_cache, k_scale, v_scale, kv_lengths, new_lengths,
+                       lengths_out, k_global, v_global, block_table, stream, workspace)
 
 
 def read_fp4(k_cache, v_cache, k_scale, v_scale, kv_lengths, n, start=None, k_global=1.0,
@@ -733,41 +698,8 @@ def read_fp4(k_cache, v_cache, k_scale, v_scale, kv_lengths, n, start=None, k_gl
     """Positions start[b] .. start[b] + n - 1 (int32 [B]; None: from 0) of a
     4-bit cache (see ``decode_fp4``) as numbers: returns (k, v)
     [B, n, Hkv, d], zeros at or past kv_lengths[b].  out: such a pair to fill."""
-    B = kv_lengths.shape[0]
-    device = k_cache.device
-    if out is None:
-        shape = (B, int(n), k_cache.shape[1], 2 * k_cache.shape[3])
-        out = (_empty(shape, out_dtype, device, stream), _empty(shape, out_dtype, device, stream))
-    k, v = out
-    if not (k_cache.is_cuda and v_cache.device == device and k_scale.device == device
-            and v_scale.device == device and k.device == device and v.device == device):
-        _off_device(device)
-    if k.dim() != 4 or k.shape[0] != B or k.shape[1] != n:
-        raise ValueError("out must be two [B, n, Hkv, d] tensors")
-    table, max_pages = _table(block_table, B, device)
-    _call("fd_read_fp4", device, _pack(k_cache), _pack(v_cache), _pack(k_scale), _pack(v_scale),
-          k_global, v_global, table, max_pages, _ints(start, (B,), device, "start"),
-          _ints(kv_lengths, (B,), device, "kv_lengths"), _pack(k), _pack(v),
-          _opts_for(workspace, device, stream))
-    return k, v
-
-
-def _books(block_table, kv_lengths, refs):
-    """Checked addresses of a paged cache's books: (device, table, B,
-    max_pages, lengths, refs, num_pages)."""
-    device, shape, pages = block_table.device, block_table.shape, refs.shape
-    if not block_table.is_cuda or len(shape) != 2 or len(pages) != 1:
-        raise ValueError("block_table must be a CUDA [B, max_pages] tensor and refs [num_pages]")
-    B, max_pages = shape
-    return (device, _ints(block_table, shape, device, "block_table"), B, max_pages,
-            _ints(kv_lengths, (B,), device, "kv_lengths"), _ints(refs, pages, device, "refs"),
-            pages[0])
-
-
-def _pages_opts(workspace, device, stream, num_pages) -> bytes:
-    # room for the scratch in slots of the default 16 rows at head_dim 256,
-    # beyond those of its 1024 blocks
-    return _opts_for(workspace, device, stream, max(3 * num_pages // slot_floats(16, 256) - 1000, 1))
+    return _native.read_fp4(k_cache, v_cache, k_scale, v_scale, kv_lengths, n, start, k_global,
+                            v_global, block_table, out, out_dtype, stream, workspace)
 
 
 def pages_reserve(block_table, kv_lengths, refs, page_size, n_new, pairs=None, count=None,
@@ -778,21 +710,8 @@ def pages_reserve(block_table, kv_lengths, refs, page_size, n_new, pairs=None, c
     pairs int32 [B, 2] (old, new) pages for ``pages_copy``, count int32 [1] of
     them, or minus the pages that are missing (nothing is then reserved).
     refs int32 [num_pages] counts the entries that name each page."""
-    device, table, B, max_pages, lens, counts, num_pages = _books(block_table, kv_lengths, refs)
-    each = 0
-    new = 0
-    if isinstance(n_new, torch.Tensor):
-        new = _ints(n_new, (B,), device, "n_new")
-    else:
-        each = int(n_new)
-    if pairs is None:
-        pairs = _empty((B, 2), torch.int32, device, stream)
-    if count is None:
-        count = _empty((1,), torch.int32, device, stream)
-    _call("fd_pages_reserve", device, table, B, max_pages, lens, new, each, page_size, counts,
-          num_pages, _ints(pairs, (B, 2), device, "pairs"), _ints(count, (1,), device, "count"),
-          _pages_opts(workspace, device, stream, num_pages))
-    return pairs, count
+    return _native.pages_reserve(block_table, kv_lengths, refs, page_size, n_new, pairs, count, stream,
+                                 workspace)
 
 
 def pages_fork(block_table, kv_lengths, refs, page_size, src, dst, lengths=None, stream=None,
@@ -800,22 +719,14 @@ def pages_fork(block_table, kv_lengths, refs, page_size, src, dst, lengths=None,
     """Row dst[i] of the block table lets go of its pages and shares those of
     row src[i] (int32 [n]), the first lengths[i] positions of them where
     lengths is given; kv_lengths[dst[i]] follows."""
-    device, table, B, max_pages, lens, counts, num_pages = _books(block_table, kv_lengths, refs)
-    n = src.shape[0]
-    _call("fd_pages_fork", device, table, B, max_pages, lens, page_size, counts, num_pages,
-          _ints(src, (n,), device, "src"), _ints(dst, (n,), device, "dst"),
-          _ints(lengths, (n,), device, "lengths"), n, _opts_for(workspace, device, stream))
+    _native.pages_fork(block_table, kv_lengths, refs, page_size, src, dst, lengths, stream, workspace)
 
 
 def pages_free(block_table, kv_lengths, refs, page_size, seqs=None, lengths=None, stream=None,
                workspace: Optional[Workspace] = None):
     """Sequences seqs (int32 [n]; None: every one) shrink to lengths (int32
     [n]; None: 0) where that is less, and let go of the pages past it."""
-    device, table, B, max_pages, lens, counts, num_pages = _books(block_table, kv_lengths, refs)
-    n = B if seqs is None else seqs.shape[0]
-    _call("fd_pages_free", device, table, B, max_pages, lens, page_size, counts, num_pages,
-          _ints(seqs, (n,), device, "seqs"), _ints(lengths, (n,), device, "lengths"), n,
-          _opts_for(workspace, device, stream))
+    _native.pages_free(block_table, kv_lengths, refs, page_size, seqs, lengths, stream, workspace)
 
 
 def pages_compact(block_table, refs, pairs=None, count=None, stream=None,
@@ -823,21 +734,7 @@ def pages_compact(block_table, refs, pairs=None, count=None, stream=None,
     """Renumbers the pages in use to 0 .. used - 1 in block_table and refs.
     Returns (pairs, count): int32 [num_pages // 2, 2] (from, to) pages for
     ``pages_copy`` and int32 [1], how many."""
-    device = block_table.device
-    if not block_table.is_cuda or block_table.dim() != 2 or refs.dim() != 1:
-        raise ValueError("block_table must be a CUDA [B, max_pages] tensor and refs [num_pages]")
-    B, max_pages = block_table.shape
-    num_pages = refs.shape[0]
-    half = max(num_pages // 2, 1)
-    if pairs is None:
-        pairs = _empty((half, 2), torch.int32, device, stream)
-    if count is None:
-        count = _empty((1,), torch.int32, device, stream)
-    _call("fd_pages_compact", device, _ints(block_table, (B, max_pages), device, "block_table"), B,
-          max_pages, _ints(refs, (num_pages,), device, "refs"), num_pages,
-          _ints(pairs, (half, 2), device, "pairs"), _ints(count, (1,), device, "count"),
-          _pages_opts(workspace, device, stream, num_pages))
-    return pairs, count
+    return _native.pages_compact(block_table, refs, pairs, count, stream, workspace)
 
 
 class PagePools:
@@ -862,7 +759,4 @@ def pages_copy(pools, pairs, count, stream=None, workspace: Optional[Workspace] 
     ``pages_compact`` return them."""
     if not isinstance(pools, PagePools):
         pools = PagePools(pools)
-    device = pools.device
-    n = pairs.shape[0]
-    _call("fd_pages_copy", device, pools.packed, len(pools.pools), _ints(pairs, (n, 2), device, "pairs"),
-          _ints(count, (1,), device, "count"), n, _opts_for(workspace, device, stream))
+    _native.pages_copy(pools.packed, pools.device.index, pairs, count, stream, workspace)

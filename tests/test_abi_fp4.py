@@ -204,3 +204,13 @@ def test_the_binding_refuses_host_tensors_and_wrong_lists():
     assert len(fd._pack(k)) == ctypes.sizeof(fd.FdTensor) and fd._OPTS.size == ctypes.sizeof(fd.FdOpts)
     t = fd.FdTensor.from_buffer_copy(fd._pack(k[0, 0]))
     assert list(t.shape) == [8, 64, 0, 0] and list(t.stride)[:2] == [64, 1] and t.ndim == 2 and t.dtype == fd.FD_U8
+
+
+def test_the_binding_refuses_what_is_no_tensor():
+    k, s = torch.zeros(1, 1, 8, 64, dtype=torch.uint8), torch.zeros(1, 1, 8, 8).to(torch.float8_e4m3fn)
+    with pytest.raises(TypeError):
+        fd.decode_fp4(None, k, k, s, s, [8])
+    with pytest.raises(TypeError):
+        fd.pages_free([[0]], [1], [1], 16)
+    with pytest.raises(TypeError):
+        fd.pages_compact(None, None)

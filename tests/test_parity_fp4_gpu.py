@@ -2,6 +2,8 @@
 against the 64-bit oracle: both head dims, every row count class, lengths from
 0 and 1 up, split counts, causal windows that leave rows empty, layouts, pages
 of any size, poisoned memory past the lengths, streams and graphs."""
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -518,3 +520,64 @@ def test_nan_hidden_by_the_window(d, page, n_q, g, hole):
     top = np.nan_to_num(np.abs(fp4.values(v, vs))).max()
     clean = [np.where(np.isnan(x), 0, x) for x in (want, weight)] + [np.nan_to_num(size)]
     check(torch.nan_to_num(got), clean[0], decode_bound(clean[0], clean[1], clean[2], 301, top, F32), "hidden")
+
+
+def test_the_binding_refuses_and_keeps_no_references():
+    rng = np.random.default_rng(71)
+    (kd, ksd), (vd, vsd) = to_dev(*cache(rng, 2, 2, 32, 128)), to_dev(*cache(rng, 2, 2, 32, 128))
+    q, lens = bf16(rng, (2, 1, 4, 128)).cuda(), ints([32, 7])
+    new = bf16(rng, (2, 3, 2, 128)).cuda()
+    good = fd.decode_fp4(q, kd, vd, ksd, vsd, lens)
+    out = torch.zeros_like(good)
+    bad = [
+        (ValueError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens.long())),
+        (ValueError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, ints([1, 2, 3]))),
+        (ValueError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, ints([1, 2, 3, 4])[::2])),
+        (ValueError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens.cpu())),
+        (ValueError, lambda: fd.decode_fp4(q, kd, vd.cpu(), ksd, vsd, lens)),
+        (ValueError, lambda: fd.decode_fp4(q[0], kd, vd, ksd, vsd, lens)),
+        (ValueError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens, block_table=ints([0, 1]))),
+        (ValueError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens, n_q=1 << 40)),
+        (TypeError, lambda: fd.decode_fp4(q.half(), kd, vd, ksd, vsd, lens)),
+        (TypeError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens, scale="x")),
+        (TypeError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens, out_dtype="bf16")),
+        (fd.FdError, lambda: fd.decode_fp4(q.float(), kd, vd, ksd, vsd, lens)),
+        (fd.FdError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens, out=out[:, :, :2])),
+        (fd.FdError, lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens, n_q=2)),
+        (ValueError, lambda: fd.append_fp4(new, new, kd, vd, ksd, vsd, lens, new_lengths=ints([1]))),
+        (fd.FdError, lambda: fd.append_fp4(new, new[:, :2], kd, vd, ksd, vsd, lens)),
+        (ValueError, lambda: fd.read_fp4(kd, vd, ksd, vsd, lens, 3, out=(new,))),
+        (ValueError, lambda: fd.read_fp4(kd, vd, ksd, vsd, lens, 4, out=(new, new))),
+        (ValueError, lambda: fd.read_fp4(kd, vd, ksd, vsd, lens, -1)),
+        (fd.FdError, lambda: fd.read_fp4(kd, vd, ksd, vsd, lens, 0)),
+        (ValueError, lambda: fd.read_fp4(kd[0, 0, 0], vd, ksd, vsd, lens, 3)),
+    ]
+    kept = (q, kd, vd, ksd, vsd, lens, new, out)
+    counts = [sys.getrefcount(t) for t in kept]
+    for _ in range(3):
+        for i, (kind, call) in enumerate(bad):
+            with pytest.raises(kind):
+                call()
+                pytest.fail("call %d was accepted" % i)
+        assert fd.decode_fp4(q, kd, vd, ksd, vsd, lens, out=out) is out
+        k, v = fd.read_fp4(kd, vd, ksd, vsd, lens, 3, out=(new, new.clone()))
+        del k, v
+    assert [sys.getrefcount(t) for t in kept] == counts
+    assert (out == good).all()
+
+
+def test_a_given_stream_owns_what_the_call_makes():
+    rng = np.random.default_rng(72)
+    (kd, ksd), (vd, vsd) = to_dev(*cache(rng, 2, 2, 32, 128)), to_dev(*cache(rng, 2, 2, 32, 128))
+    q, lens = bf16(rng, (2, 1, 4, 128)).cuda(), ints([32, 7])
+    want = fd.decode_fp4(q, kd, vd, ksd, vsd, lens, out_dtype=F32)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = fd.decode_fp4(q, kd, vd, ksd, vsd, lens, out_dtype=F32, stream=side)
+    k, v = fd.read_fp4(kd, vd, ksd, vsd, lens, 5, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert (got == want).all() and got.shape == want.shape
+    for a, b in zip(fd.read_fp4(kd, vd, ksd, vsd, lens, 5), (k, v)):
+        assert (a == b).all()
+    torch.cuda.synchronize()
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
