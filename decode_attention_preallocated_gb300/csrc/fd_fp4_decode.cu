@@ -72,6 +72,9 @@ struct Cfg {
     static constexpr int QROWS = (ROWS + WARPS - 1) / WARPS;   // query rows a warp prepares
 };
 
+// A page or row number times a stride (neither is negative).
+__device__ __forceinline__ uint64_t wide(uint32_t x, int64_t stride) { return x * (uint64_t)stride; }
+
 template <int NH, int NT, bool PAGED>
 __global__ void __launch_bounds__((Cfg<NH, NT>::THREADS), (Cfg<NH, NT>::OCC))
 fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
@@ -105,7 +108,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
     // warp covers positions start + n * TILE ..
     const int t4x16 = t4 * 16 + half * 64;
     const uint32_t to = ring_a + chunk_at(gid, t4);    // rows 8 further lie 512 bytes on
-    const bool runs = PAGED && (p.page_size & 7) == 0;
+    const bool runs = PAGED && (p.page_size & 7) == 0, runs16 = PAGED && (p.page_size & 15) == 0;
     int start = 0, steps = 0, len = 0, seq = 0;
     const uint8_t *kb = nullptr, *vb = nullptr, *ksb = nullptr, *vsb = nullptr;
     // Pages of the runs of 8 rows of eight steps: lane 4 * (n % 8) + i has run i
@@ -152,25 +155,33 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             } else {
                 uint32_t valid;
                 if (runs) {
-                    // runs of 8 rows lie on one page: four pages a step
+                    // runs of 8 rows lie on one page: four pages a step, or two
+                    // where the pages hold whole runs of 16
                     if ((n & 7) == 4) later = lookup(n + 4);
                     if ((n & 7) == 0 && n > 0) pages = later;
                     const int at = (n & 7) * 4;
                     const int mine = __shfl_sync(0xffffffffu, pages, at + (lane >> 3));
                     const bool ok = lane < left && mine >= 0;
                     valid = __ballot_sync(0xffffffffu, ok);
+                    const uint8_t *k0 = kb, *v0 = vb;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int pg = __shfl_sync(0xffffffffu, pages, at + i);
-                        const int rw = page_row(p, pos0 + 8 * i) + gid;
-                        const bool in = pg >= 0 && 8 * i + gid < left;
-                        const int64_t first = in ? pg : 0, row = in ? rw : 0;
-                        copy16(dst + i * 512, kb + first * p.ks[0] + row * p.ks[2], in);
-                        copy16(dst + i * 512 + kCode, vb + first * p.vs[0] + row * p.vs[2], in);
+                        bool in = (valid >> (8 * i + gid)) & 1u;
+                        if (i % 2 && runs16) {
+                            k0 += 8 * p.ks[2];
+                            v0 += 8 * p.vs[2];
+                        } else {
+                            const int pg = __shfl_sync(0xffffffffu, pages, at + i);
+                            const uint32_t first = pg >= 0 ? pg : 0, row = page_row(p, pos0 + 8 * i) + gid;
+                            k0 = kb + wide(first, p.ks[0]) + wide(row, p.ks[2]);
+                            v0 = vb + wide(first, p.vs[0]) + wide(row, p.vs[2]);
+                        }
+                        copy16(dst + i * 512, in ? k0 : kb, in);
+                        copy16(dst + i * 512 + kCode, in ? v0 : vb, in);
                     }
-                    const int64_t first = ok ? mine : 0, row = ok ? page_row(p, pos0 + (lane & ~7)) + (lane & 7) : 0;
-                    copy8(sd, ksb + first * fp.kss[0] + row * fp.kss[2], ok);
-                    copy8(sd + kScale, vsb + first * fp.vss[0] + row * fp.vss[2], ok);
+                    const uint32_t first = ok ? mine : 0, row = ok ? page_row(p, pos0 + (lane & ~7)) + (lane & 7) : 0;
+                    copy8(sd, ksb + wide(first, fp.kss[0]) + wide(row, fp.kss[2]), ok);
+                    copy8(sd + kScale, vsb + wide(first, fp.vss[0]) + wide(row, fp.vss[2]), ok);
                 } else {
                     // any page size: row by row
                     int page = lane < left ? page_of(p, seq, pos0 + lane) : -1;
