@@ -197,7 +197,7 @@ int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor 
     f.groups = ws->groups;
     f.q_aligned8 = reinterpret_cast<uintptr_t>(q->data) % 8 == 0 && q->stride[0] % 4 == 0 &&
                    q->stride[1] % 4 == 0 && q->stride[2] % 4 == 0;
-    p.seg_units = fd::kFp4SegUnits;
+    p.seg_units = fd::fp4_seg_units(p.tile);
     // work units are counted in 32 bits on the device
     if (p.nseg * (fd::ceil_div(c.cap, p.tile) + p.seg_units) >= ((int64_t)1 << 31)) return FD_ERR_UNSUPPORTED;
 

@@ -129,29 +129,31 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             const uint32_t dst = to + slot * kStage;
             const uint32_t sd = ring_a + slot * kStage + 2 * kCode + lane * 8;
             if (!PAGED) {
-                const int64_t far = (int64_t)n * C::TILE;
-                const uint8_t *k0 = kb + far * p.ks[2], *v0 = vb + far * p.vs[2];
-                const uint8_t *k1 = ksb + far * fp.kss[2], *v1 = vsb + far * fp.vss[2];
                 const int64_t k8 = 8 * p.ks[2], v8 = 8 * p.vs[2];
                 if (left >= kSub) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        copy16(dst + i * 512, k0 + i * k8);
-                        copy16(dst + i * 512 + kCode, v0 + i * v8);
+                        copy16(dst + i * 512, kb + i * k8);
+                        copy16(dst + i * 512 + kCode, vb + i * v8);
                     }
-                    copy8(sd, k1);
-                    copy8(sd + kScale, v1);
+                    copy8(sd, ksb);
+                    copy8(sd + kScale, vsb);
                 } else {   // rows past the length: zeros, from an address that exists
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const bool in = 8 * i + gid < left;
-                        copy16(dst + i * 512, in ? k0 + i * k8 : static_cast<const uint8_t *>(p.k), in);
-                        copy16(dst + i * 512 + kCode, in ? v0 + i * v8 : static_cast<const uint8_t *>(p.v), in);
+                        copy16(dst + i * 512, in ? kb + i * k8 : static_cast<const uint8_t *>(p.k), in);
+                        copy16(dst + i * 512 + kCode, in ? vb + i * v8 : static_cast<const uint8_t *>(p.v), in);
                     }
                     const bool in = lane < left;
-                    copy8(sd, in ? k1 : fp.ks, in);
-                    copy8(sd + kScale, in ? v1 : fp.vs, in);
+                    copy8(sd, in ? ksb : fp.ks, in);
+                    copy8(sd + kScale, in ? vsb : fp.vs, in);
                 }
+                // (steps are fetched in order)
+                kb += C::TILE * p.ks[2];
+                vb += C::TILE * p.vs[2];
+                ksb += C::TILE * fp.kss[2];
+                vsb += C::TILE * fp.vss[2];
             } else {
                 uint32_t valid;
                 if (runs) {

@@ -24,8 +24,13 @@ struct Fp4Params {
 };
 // Rows that one part holds at most.
 constexpr int kFp4PartRows = 32;
-// Work units charged for the start and end of a piece, in tiles.
-constexpr int kFp4SegUnits = 2;
+// What the start and end of a piece are charged, in positions; at least two of
+// its tiles.  24 rows at d = 256 (tiles of 128), ragged: 79.5 us with 2 tiles,
+// 77.7 with 4, 78.8 with 6.  4 rows at d = 128 (256), 64 ragged sequences over
+// pages: 61 with 2, 63 with 3, 66 with 4.  16 rows at d = 128 (192): 24.9 with
+// 2, 26.2 with 3.
+constexpr int kFp4PiecePositions = 512;
+inline int fp4_seg_units(int tile) { return kFp4PiecePositions / tile > 2 ? kFp4PiecePositions / tile : 2; }
 // Cache positions per tile of the partitioner, and blocks that an SM holds, for
 // parts of this many rows.
 int fp4_tile_tokens(int d, int rows);

@@ -151,7 +151,8 @@ struct Finder {
 };
 
 // Work units that a block takes at least.  4 rows x 4 heads over 3,000 positions
-// of a 256-wide cache: 19.4 us with 2, 18.1 with 4, 23.4 with 6.
+// of a 256-wide cache: 19.3 us with 3, 18.9 with 4, 23.5 with 6; 4 x 2 heads
+// over 1,000 of a 128-wide one: 9.5, 8.6, 8.8.
 constexpr uint32_t kLeastUnits = 4;
 
 // The range of work units of each of the launch's working blocks.
@@ -347,8 +348,11 @@ __device__ __forceinline__ float scale_query(const Params &p, uint2 *q) {
     return fmaxf(fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + e) << 23), 1.1754944e-38f);
 }
 
-// Pieces of a segment that are joined in groups of this many, when there are
-// more than kOneJoin of them.
+// Pieces of a segment are joined in groups of 8 where a thread of a single join
+// would walk over more than kOneJoin of them.  24 rows at d = 256, 32,768
+// positions (38 pieces, one way): 40 us in groups, 48 at once.  4 rows at d =
+// 128 (four ways, 9 or 10 pieces each): 17.7 in groups, 15.1 at once.  16 at d =
+// 256 over 3,000 positions: 21.8 in groups, 18.1 at once.
 constexpr int kGroup8 = 8, kOneJoin = 12;
 
 // The end of a piece of a split segment whose partial result is in this
@@ -375,13 +379,12 @@ __device__ __forceinline__ void join_pieces(const Fp4Params &fp, const Share &sh
         if (yes) __threadfence();
         return yes;
     };
+    // (row, 8 columns) items, and `ways` groups of threads that take every
+    // ways-th piece each
+    const int items = g.rows * (D / 8), ways = max(1, THREADS / items);
     // Joins pieces c0, c0 + step, .. (`count` of them) into the slot of c0, or
     // into the output.
     const auto join = [&](int c0, int step, int count, bool final) {
-        // (row, 8 columns) items, and `ways` groups of threads that take every
-        // ways-th piece each
-        const int items = g.rows * (D / 8);
-        const int ways = max(1, THREADS / items);
         for (int e0 = 0; e0 < items; e0 += THREADS) {
             const int way = items < THREADS ? tid / items : 0;
             const int e = items < THREADS ? tid - way * items : e0 + tid;
@@ -441,7 +444,7 @@ __device__ __forceinline__ void join_pieces(const Fp4Params &fp, const Share &sh
             }
         }
     };
-    if (pieces <= kOneJoin) {
+    if (pieces <= kOneJoin * ways) {
         if (last_of(p.counters + s, pieces)) join(c_first, 1, pieces, true);
         return;
     }

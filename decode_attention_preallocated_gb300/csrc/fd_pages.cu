@@ -599,7 +599,12 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     }
 }
 
-int cluster_for(const Books &k) { return k.num_pages > 32768 ? kMaxCluster : 1; }
+// One block or eight, in us (half the pages in use):
+//   pages      8,000        16,000       32,000       130,000      400,000
+//   reserve    7.1 / 8.5    7.6 / 8.4    10.4 / 9.4   20 / 11      43 / 20
+//   compact    9.3 / 10.5   13.8 / 11.5  22 / 11      80 / 20      233 / 47
+constexpr int kReserveAlone = 24576, kCompactAlone = 12288;
+int cluster_for(const Books &k, int alone) { return k.num_pages > alone ? kMaxCluster : 1; }
 
 template <typename Args>
 int launch_cluster(void (*kernel)(const Args), const Args &a, int size, cudaStream_t st) {
@@ -639,14 +644,14 @@ int launch_pages_reserve(const Books &k, const int32_t *n_new, int n_each, int32
                          int32_t *count, int32_t *scratch, cudaStream_t st) {
     ReserveArgs a{k, n_new, n_each, pairs, count, scratch, scratch + k.num_pages,
                   scratch + 2 * (int64_t)k.num_pages};
-    return launch_cluster(reserve_kernel, a, cluster_for(k), st);
+    return launch_cluster(reserve_kernel, a, cluster_for(k, kReserveAlone), st);
 }
 
 int launch_pages_compact(const Books &k, int32_t *pairs, int32_t *count, int32_t *scratch,
                          cudaStream_t st) {
     const int64_t P = k.num_pages;
     CompactArgs a{k, pairs, count, scratch + 32, scratch + 32 + P, scratch + 32 + 2 * P, scratch};
-    const int rc = launch_cluster(compact_kernel, a, cluster_for(k), st);
+    const int rc = launch_cluster(compact_kernel, a, cluster_for(k, kCompactAlone), st);
     if (rc != 0) return rc;
     const int64_t n = (int64_t)k.B * k.max_pages;
     const int64_t blocks = ceil_div(n, 256) < 1024 ? ceil_div(n, 256) : 1024;
