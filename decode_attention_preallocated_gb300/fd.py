@@ -1,9 +1,10 @@
-"""ctypes binding of libfd.so (the C ABI in include/fd.h).
+"""Python binding of libfd.so (the C ABI in include/fd.h): ctypes, and for the
+4-bit cache and page calls the extension in csrc/fd_torch.cpp.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels inside libfd.so.  PyTorch supplies device memory and the current
-stream.  There is no fallback: if libfd.so is missing or cannot be loaded,
-every call raises.
+stream.  There is no fallback: if libfd.so (or
+the extension) is missing or cannot be loaded, every call raises.
 
 Low-level names mirror the C ABI (``fd_decode``, ``fd_decode_int8``,
 ``fd_decode_append``, ``fd_decode_paged``, ``fd_decode_masked``,

@@ -510,8 +510,8 @@ int fd_read_fp4(const fd_tensor *k_cache, const fd_tensor *v_cache, const fd_ten
  *   elements must fill one block of memory, in any order of dimensions.  No
  *   page may be both copied from and copied to, nor be copied to twice.
  *
- * reserve and compact use pages_scratch(num_pages) bytes of the workspace's
- * room for split partials (fd_pages_scratch_bytes; the room is
+ * reserve and compact use fd_pages_scratch_bytes(num_pages) bytes of the
+ * workspace's room for split partials (the room is
  * fd_workspace_bytes(segments, rows, head_dim, ctas) less about 4 * segments
  * bytes).
  */
