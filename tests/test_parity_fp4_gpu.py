@@ -3,6 +3,7 @@ against the 64-bit oracle: both head dims, every row count class, lengths from
 0 and 1 up, split counts, causal windows that leave rows empty, layouts, pages
 of any size, poisoned memory past the lengths, streams and graphs."""
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -581,3 +582,66 @@ def test_a_given_stream_owns_what_the_call_makes():
         assert (a == b).all()
     torch.cuda.synchronize()
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+def test_more_sequences_than_a_grid_is_high():
+    B, d = 66001, 128
+    rng = np.random.default_rng(81)
+    new = bf16(rng, (B, 1, 1, d))
+    lens = torch.arange(B, dtype=torch.int32) % 3          # 2 is the capacity: nothing is written there
+    codes, scales = np.zeros((B, 1, 2, d // 2), np.uint8), np.zeros((B, 1, 2, d // 16), np.uint8)
+    want_c, want_s = fp4.quantise(new[:, 0].float().numpy(), 1.0, np.float32)
+    for at in range(2):
+        rows = np.arange(B) % 3 == at
+        codes[rows, :, at], scales[rows, :, at] = want_c[rows], want_s[rows]
+    (kd, ksd), (vd, vsd) = (to_dev(np.zeros_like(codes), np.zeros_like(scales)) for _ in range(2))
+    after = lens.cuda()
+    ws = fd.Workspace(64, 16, 256, 64)
+    fd.append_fp4(new.cuda(), new.cuda(), kd, vd, ksd, vsd, after, lengths_out=after, workspace=ws)
+    assert (after.cpu() == torch.clamp(lens + 1, max=2)).all()
+    assert ws.device_status() == fd.FD_DEV_BAD_LENGTH
+    for c, s in ((kd, ksd), (vd, vsd)):
+        assert (c.cpu().numpy() == codes).all() and (s.view(torch.uint8).cpu().numpy() == scales).all()
+    k, v = fd.read_fp4(kd, vd, ksd, vsd, after, 2, out_dtype=F32)
+    want = fp4.values(codes, scales).transpose(0, 2, 1, 3)
+    assert (k.cpu().numpy() == want).all() and (v.cpu().numpy() == want).all()
+
+
+def test_a_query_that_is_one_row_for_all():
+    rng = np.random.default_rng(82)
+    k, ks = cache(rng, 3, 2, 90, 256)
+    v, vs = cache(rng, 3, 2, 90, 256)
+    (kd, ksd), (vd, vsd) = to_dev(k, ks), to_dev(v, vs)
+    q = bf16(rng, (1, 1, 1, 256)).cuda().expand(3, 2, 8, 256)
+    lens = ints([90, 41, 2])
+    got = fd.decode_fp4(q, kd, vd, ksd, vsd, lens, causal=True)
+    assert (got == fd.decode_fp4(q.contiguous(), kd, vd, ksd, vsd, lens, causal=True)).all()
+    want, weight, size = fp4.decode(q.cpu().double().numpy(), k, v, ks, vs, [90, 41, 2], True, scale_of(256))
+    check(got, want, decode_bound(want, weight, size, 90, np.abs(fp4.values(v, vs)).max(), BF), "expanded")
+
+
+def test_two_threads_on_two_streams():
+    rng = np.random.default_rng(83)
+    jobs = []
+    for i in range(2):
+        (kd, ksd), (vd, vsd) = to_dev(*cache(rng, 2, 2, 3000, 128)), to_dev(*cache(rng, 2, 2, 3000, 128))
+        q, lens = bf16(rng, (2, 1 + 2 * i, 8, 128)).cuda(), ints([3000, 1234 + i])
+        jobs.append((q, kd, vd, ksd, vsd, lens, fd.decode_fp4(q, kd, vd, ksd, vsd, lens)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(q, kd, vd, ksd, vsd, lens, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got = [fd.decode_fp4(q, kd, vd, ksd, vsd, lens) for _ in range(50)]
+                torch.cuda.current_stream().synchronize()
+                wrong.extend(i for i, g in enumerate(got) if not (g == want).all())
+        except Exception as e:   # (a thread's own exception ends nothing)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not wrong
