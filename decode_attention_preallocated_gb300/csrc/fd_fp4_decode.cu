@@ -118,7 +118,10 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
     // warp covers positions start + n * TILE ..
     const int t4x16 = t4 * 16 + half * 64;
     const uint32_t to = ring_a + chunk_at(gid, t4);    // rows 8 further lie 512 bytes on
-    const bool runs = PAGED && (p.page_size & 7) == 0, runs16 = PAGED && (p.page_size & 15) == 0;
+    // Pages whose size is a power of two from 8 on are looked up by runs of 8 or
+    // 16 rows, others row by row.  64 sequences of 2,040 positions over pages of
+    // 8: 54.7 us; of 12: 57.0; of 24: 56.2, by runs with a division each 60.5.
+    const bool runs = PAGED && p.page_shift >= 3, runs16 = PAGED && p.page_shift >= 4;
     int start = 0, steps = 0, len = 0, seq = 0;
     const uint8_t *kb = nullptr, *vb = nullptr, *ksb = nullptr, *vsb = nullptr;
     // Pages of the runs of 8 rows of eight steps: lane 4 * (n % 8) + i has run i
@@ -184,14 +187,14 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                             v0 += 8 * p.vs[2];
                         } else {
                             const int pg = __shfl_sync(0xffffffffu, pages, at + i);
-                            const uint32_t first = pg >= 0 ? pg : 0, row = page_row(p, pos0 + 8 * i) + gid;
+                            const uint32_t first = pg >= 0 ? pg : 0, row = ((pos0 + 8 * i) & (p.page_size - 1)) + gid;
                             k0 = kb + wide(first, p.ks[0]) + wide(row, p.ks[2]);
                             v0 = vb + wide(first, p.vs[0]) + wide(row, p.vs[2]);
                         }
                         copy16(dst + i * 512, in ? k0 : kb, in);
                         copy16(dst + i * 512 + kCode, in ? v0 : vb, in);
                     }
-                    const uint32_t first = ok ? mine : 0, row = ok ? page_row(p, pos0 + (lane & ~7)) + (lane & 7) : 0;
+                    const uint32_t first = ok ? mine : 0, row = ok ? (pos0 + lane) & (p.page_size - 1) : 0;
                     copy8(sd, ksb + wide(first, fp.kss[0]) + wide(row, fp.kss[2]), ok);
                     copy8(sd + kScale, vsb + wide(first, fp.vss[0]) + wide(row, fp.vss[2]), ok);
                 } else {
