@@ -12,7 +12,7 @@ from decode_attention_preallocated_gb300 import fd
 PTR = 0x100000
 
 
-@pytest.fixture(scope="module")
+@pytest.fixture(scope="module", autouse=True)
 def L():
     fdbuild.build()
     return fd.lib()
