@@ -174,10 +174,13 @@ void run(const char *name, const Device &dev, PyObject *stream, PyObject *worksp
     if (plain) {
         void *const s = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev.index).stream();
         Ref key(Py_BuildValue("(iK)", dev.index, (unsigned long long)(uintptr_t)s));
-        PyObject *ws = PyDict_GetItemWithError(workspaces, key.p);   // borrowed
-        if (!ws && PyErr_Occurred()) throw Raised{};
-        if (ws) {
-            Ref handle(PyObject_GetAttrString(ws, "handle"));
+        PyObject *found = PyDict_GetItemWithError(workspaces, key.p);   // borrowed
+        if (!found && PyErr_Occurred()) throw Raised{};
+        if (found) {
+            // another thread may put a larger one in its place meanwhile; fd.py
+            // destroys neither
+            Ref ws(Py_NewRef(found));
+            Ref handle(PyObject_GetAttrString(ws.p, "handle"));
             Ref value(PyObject_GetAttrString(handle.p, "value"));
             o.stream = s;
             o.ws = static_cast<fd_workspace *>(PyLong_AsVoidPtr(value.p));

@@ -304,27 +304,38 @@ class Workspace:
 
 
 _ws_cache = {}
+_ws_replaced = []
 _ws_lock = threading.Lock()
 
 
 def workspace_for(device, stream_handle, segments, rows, head_dim, ctas) -> Workspace:
-    """Workspace shared by calls on one (device, stream); grown when needed
-    (growth synchronises the device, so size it up front for graph capture)."""
+    """Workspace shared by calls on one (device, stream); a larger one takes its
+    place when needed (making it allocates, so size it up front for graph
+    capture).  The smaller one is never destroyed: another thread's call may
+    hold it, and a graph captured with it may still be replayed.  What was too
+    small at least doubles, so that few of them pile up."""
     key = (torch.device(device).index, int(stream_handle))
+
+    def grown(need, have, most):
+        return have if need <= have else max(need, min(2 * have, most))
+
     with _ws_lock:
         ws = _ws_cache.get(key)
-        if ws is None or not ws.fits(segments, rows, head_dim, ctas):
+        if ws is None:
             want = dict(max_segments=max(segments, 64), max_rows=max(rows, 16),
                         head_dim=max(head_dim, 256), max_ctas=max(ctas, 1024))
-            if ws is not None:
-                want = dict(max_segments=max(want["max_segments"], ws.max_segments),
-                            max_rows=max(want["max_rows"], ws.max_rows),
-                            head_dim=max(want["head_dim"], ws.head_dim),
-                            max_ctas=max(want["max_ctas"], ws.max_ctas))
-                ws.close()
-            ws = Workspace(device=device, **want)
-            _ws_cache[key] = ws
-        return ws
+        elif ws.fits(segments, rows, head_dim, ctas):
+            return ws
+        else:
+            want = dict(max_segments=grown(segments, ws.max_segments, 1 << 62),
+                        max_rows=grown(rows, ws.max_rows, FD_MAX_ROWS),
+                        head_dim=max(head_dim, ws.head_dim),
+                        max_ctas=grown(ctas, ws.max_ctas, (1 << 31) - 1))
+        new = Workspace(device=device, **want)
+        if ws is not None:
+            _ws_replaced.append(ws)
+        _ws_cache[key] = new
+        return new
 
 
 def auto_num_ctas(kernel=FD_KERNEL_AUTO, head_dim=128, kv_dtype=FD_BF16, rows=1,
