@@ -203,7 +203,10 @@ def as_fd_tensor(t: torch.Tensor) -> FdTensor:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_handle(stream: Optional[torch.cuda.Stream], device) -> int:
+def _stream_handle(stream, device) -> int:
+    """Handle of a stream; an int is one already, None the current stream."""
+    if isinstance(stream, int):
+        return stream
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
@@ -331,7 +334,8 @@ def workspace_for(device, stream_handle, segments, rows, head_dim, ctas) -> Work
                         max_rows=grown(rows, ws.max_rows, FD_MAX_ROWS),
                         head_dim=max(head_dim, ws.head_dim),
                         max_ctas=grown(ctas, ws.max_ctas, (1 << 31) - 1))
-        new = Workspace(device=device, **want)
+        # (zeroed on the stream that its calls run on, which may not be the current)
+        new = Workspace(device=device, stream=int(stream_handle), **want)
         if ws is not None:
             _ws_replaced.append(ws)
         _ws_cache[key] = new

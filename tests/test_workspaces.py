@@ -79,6 +79,13 @@ def test_few_workspaces_pile_up(cache, monkeypatch):
     assert fd.workspace_for("cuda:0", 8, 1, 1, 256, 1).max_segments == 64   # another stream's own
 
 
+def test_a_workspace_is_zeroed_on_the_stream_of_its_calls(cache):
+    # a call given a stream that is not the current one
+    assert fd._stream_handle(fd.workspace_for("cuda:0", 7, 10, 4, 128, 100).stream, torch.device("cuda", 0)) == 7
+    assert fd._stream_handle(fd.workspace_for("cuda:0", 7, 5000, 4, 128, 100).stream, torch.device("cuda", 0)) == 7
+    assert fd._stream_handle(fd.workspace_for("cuda:0", 0, 10, 4, 128, 100).stream, torch.device("cuda", 0)) == 0
+
+
 @pytest.mark.gpu
 def test_two_threads_on_one_stream_while_the_workspace_grows():
     from fp4_util import bf16, cache as quantised, to_dev
