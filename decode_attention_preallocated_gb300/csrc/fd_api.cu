@@ -309,6 +309,7 @@ int run(const Call &c) {
     }
 
     cudaStream_t st = static_cast<cudaStream_t>(o.stream);
+    const std::lock_guard<std::mutex> turn(ws->turn);
     rc = kernel == FD_KERNEL_TC ? fd::launch_tc(p, G, st) : fd::launch_simt(p, G, st);
     return rc == 0 ? FD_OK : (rc == -2 ? FD_ERR_UNSUPPORTED : FD_ERR_CUDA);
 }

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "fd.h"
 
 struct fd_workspace {
@@ -18,6 +20,9 @@ struct fd_workspace {
     float *partials;
     size_t partial_floats;
     int device;
+    std::mutex turn;         // held while a call queues its launches: what one of
+                             // them leaves in the partials for the next is not
+                             // overwritten by another thread's call between them
 };
 
 namespace fd {

@@ -213,6 +213,7 @@ int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor 
         G > ws->max_ctas ||
         (size_t)(p.nseg + G) * (size_t)fd::slot_floats(part_rows, c.d) > ws->partial_floats)
         return FD_ERR_WORKSPACE;
+    const std::lock_guard<std::mutex> turn(ws->turn);
     return status_of(fd::launch_fp4_decode(f, G, static_cast<cudaStream_t>(opts->stream)));
 }
 
@@ -300,6 +301,7 @@ int fd_pages_reserve(int32_t *block_table, int32_t B, int32_t max_pages,
     if (rc) return rc;
     if (!pairs || !count || (!n_new && n_each < 0)) return FD_ERR_ARG;
     if ((size_t)fd::pages_scratch_words(num_pages) > opts->ws->partial_floats) return FD_ERR_WORKSPACE;
+    const std::lock_guard<std::mutex> turn(opts->ws->turn);
     return status_of(fd::launch_pages_reserve(k, n_new, n_each, pairs, count,
                                               reinterpret_cast<int32_t *>(opts->ws->partials),
                                               static_cast<cudaStream_t>(opts->stream)));
@@ -337,6 +339,7 @@ int fd_pages_compact(int32_t *block_table, int32_t B, int32_t max_pages, int32_t
     if (rc) return rc;
     if (!pairs || !count) return FD_ERR_ARG;
     if ((size_t)fd::pages_scratch_words(num_pages) > opts->ws->partial_floats) return FD_ERR_WORKSPACE;
+    const std::lock_guard<std::mutex> turn(opts->ws->turn);
     return status_of(fd::launch_pages_compact(k, pairs, count,
                                               reinterpret_cast<int32_t *>(opts->ws->partials),
                                               static_cast<cudaStream_t>(opts->stream)));

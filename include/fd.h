@@ -542,7 +542,9 @@ int fd_pages_copy(const fd_tensor *pools, int32_t n_pools, const int32_t *pairs,
  * scratch of the split combine belongs to one stream-ordered launch at a
  * time, the rule comfy-kitchen #239 adopts for its GEMM workspace (commit
  * list: the workspace is tied to each launch in stream order).  Two streams
- * that may run decode calls at once need two workspaces.  Calls that do
+ * that may run decode calls at once need two workspaces.  Host threads may
+ * share one with the stream: a call's launches follow one another without
+ * another call's between them.  Calls that do
  * overlap on one workspace can leave its counters inconsistent (results of
  * later calls are then wrong: a merge is skipped, or a masked call keeps an
  * older chunk list) until fd_workspace_reset.

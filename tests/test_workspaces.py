@@ -129,3 +129,64 @@ def test_two_threads_on_one_stream_while_the_workspace_grows():
         t.join(120)
     assert not any(t.is_alive() for t in threads) and not errors
     assert counts == {"decode": steps * 5, "grow": steps}
+
+
+@pytest.mark.gpu
+def test_two_threads_share_a_workspace_and_its_scratch():
+    # compaction's second launch reads what its first left in the room of the
+    # split partials, which the other thread's calls write
+    from fp4_util import bf16, cache as quantised, to_dev
+    from oracle.pages import Books
+    fdbuild.build()
+    rng = np.random.default_rng(85)
+    (kd, ksd), (vd, vsd) = (to_dev(*quantised(rng, 2, 2, 3000, 128)) for _ in range(2))
+    q = bf16(rng, (2, 3, 8, 128)).cuda()
+    lens = torch.tensor([3000, 1234], dtype=torch.int32, device="cuda")
+    dense = [torch.from_numpy(rng.standard_normal((2, 2, 3000, 128))).to(torch.bfloat16).cuda() for _ in range(2)]
+    ws = fd.Workspace(1024, 32, 256, 1024)
+    calls = (lambda: fd.decode_fp4(q, kd, vd, ksd, vsd, lens, workspace=ws),
+             lambda: fd.decode(q, *dense, lens, n_q=3, workspace=ws))
+    want = [call() for call in calls]
+    P = 4000
+    table = np.full((8, 300), -1)
+    used = rng.permutation(P)[:8 * 200]
+    table[:, :200] = used.reshape(8, 200)
+    refs = np.zeros(P, dtype=np.int64)
+    refs[used] = 1
+    model = Books(table, np.full(8, 200), refs, 1)
+    model.compact()
+    after = torch.from_numpy(model.table).cuda()
+    books = [torch.from_numpy(x.astype(np.int32)).cuda() for x in (table, refs)]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    errors, counts, steps = [], [0, 0], 300
+
+    def decode():
+        with torch.cuda.stream(stream):
+            got = [(i % 2, calls[i % 2]()) for i in range(2 * steps)]
+            stream.synchronize()
+            counts[0] = sum(bool((x == want[i]).all()) for i, x in got)
+
+    def compact():
+        with torch.cuda.stream(stream):
+            tables = []
+            for _ in range(steps):
+                t, r = (x.clone() for x in books)
+                fd.pages_compact(t, r, workspace=ws)
+                tables.append(t)
+            stream.synchronize()
+            counts[1] = sum(bool((t == after).all()) for t in tables)
+
+    def run(job):
+        try:
+            job()
+        except Exception as e:   # (a thread's own exception ends nothing)
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(job,)) for job in (decode, compact)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not any(t.is_alive() for t in threads) and not errors
+    assert counts == [2 * steps, steps]
