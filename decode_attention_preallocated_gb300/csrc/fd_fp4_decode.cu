@@ -383,22 +383,28 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
                             }
                     }
             }
-            float mul[NT][2];    // rows 8*n + 2*t4 and the next: factor on q.k
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float2 x = NT == 1 ? mul1 : *reinterpret_cast<const float2 *>(qmul + n * 8 + 2 * t4);
-                mul[n][0] = x.x;
-                mul[n][1] = x.y;
-            }
+            // Scores in the log2 domain, each rounded to fp32 before the reference
+            // is taken from them and from it: at 2^27 and more a product that kept
+            // its low bits could lie 2^15 and more above or below a rounded reference.
             float top[NT][2];
             bool grow = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                // rows 8*n + 2*t4 and the next: factor on q.k
+                const float2 mul = NT == 1 ? mul1 : *reinterpret_cast<const float2 *>(qmul + n * 8 + 2 * t4);
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        S[m][n][e] = __fmul_rn(S[m][n][e], mul.x);
+                        S[m][n][e + 1] = __fmul_rn(S[m][n][e + 1], mul.y);
+                    }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     top[n][c] = fmaxf(fmaxf(S[0][n][c], S[0][n][c + 2]), fmaxf(S[1][n][c], S[1][n][c + 2]));
-                    grow |= __fmaf_rn(top[n][c], mul[n][c], -mr[n][c]) > kGrow;
+                    grow |= __fsub_rn(top[n][c], mr[n][c]) > kGrow;
                 }
+            }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -408,7 +414,7 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
                         // (a row that still sees nothing keeps kNone)
-                        const float ref = fmaxf(mr[n][c], x * mul[n][c] - kBelow);
+                        const float ref = fmaxf(mr[n][c], reference_for(x));
                         const float by = fast_exp2(mr[n][c] - ref);
                         mr[n][c] = ref;
                         l[n][c] *= by;
@@ -424,10 +430,10 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const float w0 = fast_exp2(__fmaf_rn(S[m][n][0], mul[n][0], -mr[n][0]));
-                    const float w1 = fast_exp2(__fmaf_rn(S[m][n][1], mul[n][1], -mr[n][1]));
-                    const float w2 = fast_exp2(__fmaf_rn(S[m][n][2], mul[n][0], -mr[n][0]));
-                    const float w3 = fast_exp2(__fmaf_rn(S[m][n][3], mul[n][1], -mr[n][1]));
+                    const float w0 = fast_exp2(__fsub_rn(S[m][n][0], mr[n][0]));
+                    const float w1 = fast_exp2(__fsub_rn(S[m][n][1], mr[n][1]));
+                    const float w2 = fast_exp2(__fsub_rn(S[m][n][2], mr[n][0]));
+                    const float w3 = fast_exp2(__fsub_rn(S[m][n][3], mr[n][1]));
                     l[n][0] += w0 + w2;
                     l[n][1] += w1 + w3;
                     P[m][n][0] = transpose8x8(pack_f16x2(w0, w1));

@@ -16,6 +16,10 @@ namespace fp4 {
 constexpr float kBelow = 4.f, kGrow = 14.f;
 // The reference of a row that has seen nothing yet.
 constexpr float kNone = -3.402823466e38f;
+// The reference of a row whose largest score is x (in the log2 domain).  From
+// 2^26 on x - kBelow is rounded to a multiple of 8 or more, so that its weight
+// is anywhere from 2^0 to 2^8.
+__device__ __forceinline__ float reference_for(float x) { return __fsub_rn(x, kBelow); }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
