@@ -36,6 +36,7 @@ inline int fp4_seg_units(int tile) { return kFp4PiecePositions / tile > 2 ? kFp4
 int fp4_tile_tokens(int d, int rows);
 int fp4_blocks_per_sm(int rows);
 int launch_fp4_decode(const Fp4Params &p, int num_ctas, cudaStream_t stream);
+int launch_fp4_decode_f32(const Fp4Params &p, int num_ctas, cudaStream_t stream);   // its fp32 outputs
 
 // The rows of a 4-bit cache between bf16 (or fp32) and its own format
 // (fd_fp4_rows.cu).  Cache strides in bytes: [sequence or page, kv head, row].

@@ -10,16 +10,23 @@
 namespace fd {
 namespace fp4 {
 
-// The reference of a row is its running maximum less 4 when it was last set;
-// it is set again only when a weight would pass 2^14, which keeps every weight
-// within fp16 and spares most steps the shuffles and the rescaling.
-constexpr float kBelow = 4.f, kGrow = 14.f;
+// The reference of a row is its running maximum less kBelow when it was last
+// set; it is set again only when a weight would pass 2^kGrow, which keeps every
+// weight within fp16 and spares most steps the shuffles and the rescaling.  fp32
+// outputs keep their weights larger, so that small ones stay above fp16's least.
+template <bool F32>
+struct Reference {
+    static constexpr float kBelow = F32 ? 12.f : 4.f, kGrow = F32 ? 15.f : 14.f;
+    // Of a row whose largest score is x (in the log2 domain).  From 2^26 on
+    // x - kBelow is rounded to a multiple of 8 or more; it lies at most 8 below x
+    // where kBelow is 4, and is x itself where it would lie too far below.
+    static __device__ __forceinline__ float of(float x) {
+        const float ref = __fsub_rn(x, kBelow);
+        return F32 && __fsub_rn(x, ref) > kGrow ? x : ref;
+    }
+};
 // The reference of a row that has seen nothing yet.
 constexpr float kNone = -3.402823466e38f;
-// The reference of a row whose largest score is x (in the log2 domain).  From
-// 2^26 on x - kBelow is rounded to a multiple of 8 or more, so that its weight
-// is anywhere from 2^0 to 2^8.
-__device__ __forceinline__ float reference_for(float x) { return __fsub_rn(x, kBelow); }
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -410,7 +410,9 @@ int fd_decode_noalloc(const fd_tensor *q, const fd_tensor *k_cache,
  * The scores and all sums are fp32 over exact products of the codes, the
  * scales and q (an entry of q below 2^-14 of its row's largest is off by up
  * to 2^-25 of that); each softmax weight is rounded to fp16, i.e. by up to
- * 2^-11 of itself or 2^-29 of the row's largest weight.  A NaN scale
+ * 2^-11 of itself or 2^-29 of the row's largest weight, or for an fp32 output
+ * to two fp16 numbers, by up to 2^-22 or 2^-37.  Scores are finite where
+ * |scale| * k_global * sum |code * scale * q| stays within fp32.  A NaN scale
  * (fd_append_fp4 writes one for a row that is not finite) makes NaN of what
  * it stands for in the query rows that see its position, and reaches no
  * other.  Positions at or past the length and pages past it are never read.
