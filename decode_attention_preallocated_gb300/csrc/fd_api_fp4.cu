@@ -314,7 +314,8 @@ int fd_pages_fork(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *k
     const int rc = check_books(&k, block_table, B, max_pages, kv_lengths, page_size, refs,
                                num_pages, opts);
     if (rc) return rc;
-    if (!src || !dst || n < 1) return FD_ERR_ARG;
+    if (n < 0 || (n > 0 && (!src || !dst))) return FD_ERR_ARG;
+    if (n == 0) return FD_OK;
     return status_of(fd::launch_pages_fork(k, src, dst, lengths, n,
                                            static_cast<cudaStream_t>(opts->stream)));
 }
@@ -326,7 +327,8 @@ int fd_pages_free(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *k
     const int rc = check_books(&k, block_table, B, max_pages, kv_lengths, page_size, refs,
                                num_pages, opts);
     if (rc) return rc;
-    if (n < 1 || (!seqs && n != B)) return FD_ERR_ARG;
+    if (n < 0 || (n > 0 && !seqs && n != B)) return FD_ERR_ARG;
+    if (n == 0) return FD_OK;
     return status_of(fd::launch_pages_free(k, seqs, lengths, n,
                                            static_cast<cudaStream_t>(opts->stream)));
 }

@@ -501,6 +501,7 @@ int fd_read_fp4(const fd_tensor *k_cache, const fd_tensor *v_cache, const fd_ten
  *   sequence i, n = B) becomes 0, or lengths[i] where lengths is given and
  *   smaller than the length, and the row's pages past it are released.
  *   A sequence listed twice ends at the smaller length.
+ * n = 0 lists nothing: fork and free then do nothing.
  * fd_pages_compact moves the pages in use to the numbers 0 .. used - 1: the
  *   i-th page in use at or past `used` goes to the i-th free page below it.
  *   block_table and refs are renumbered, pairs (int32 [num_pages / 2, 2])

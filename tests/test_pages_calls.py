@@ -1,0 +1,56 @@
+"""What the page calls take: lists with nothing in them."""
+import ctypes
+
+import pytest
+import torch
+
+from decode_attention_preallocated_gb300 import build as fdbuild
+from decode_attention_preallocated_gb300 import fd
+
+PTR = 0x100000
+
+
+@pytest.fixture(scope="module", autouse=True)
+def L():
+    fdbuild.build()
+    return fd.lib()
+
+
+def with_room():
+    """opts whose workspace is host memory: for calls that return before the
+    first launch."""
+    room = ctypes.create_string_buffer(1024)
+    o = fd.FdOpts()
+    o.ws = ctypes.addressof(room)
+    return room, ctypes.byref(o)
+
+
+def test_a_list_of_nothing_is_no_error(L):
+    room, o = with_room()
+    assert L.fd_pages_free(PTR, 2, 4, PTR, 16, PTR, 10, PTR, None, 0, o) == fd.FD_OK
+    assert L.fd_pages_free(PTR, 2, 4, PTR, 16, PTR, 10, None, None, 0, o) == fd.FD_OK
+    assert L.fd_pages_fork(PTR, 2, 4, PTR, 16, PTR, 10, PTR, PTR, PTR, 0, o) == fd.FD_OK
+    assert L.fd_pages_fork(PTR, 2, 4, PTR, 16, PTR, 10, None, None, None, 0, o) == fd.FD_OK
+    # with everything else as it has to be
+    assert L.fd_pages_free(PTR, 2, 4, PTR, 16, None, 10, PTR, None, 0, o) == fd.FD_ERR_ARG
+    assert L.fd_pages_fork(PTR, 2, 4, PTR, 0, PTR, 10, PTR, PTR, None, 0, o) == fd.FD_ERR_ARG
+    assert L.fd_pages_free(PTR, 2, 4, PTR, 16, PTR, 10, PTR, None, -1, o) == fd.FD_ERR_ARG
+    assert L.fd_pages_free(PTR, 2, 4, PTR, 16, PTR, 10, None, None, 1, o) == fd.FD_ERR_ARG
+    assert L.fd_pages_fork(PTR, 2, 4, PTR, 16, PTR, 10, None, PTR, None, 1, o) == fd.FD_ERR_ARG
+    assert L.fd_pages_fork(PTR, 2, 4, PTR, 16, PTR, 10, PTR, PTR, None, -1, o) == fd.FD_ERR_ARG
+    assert not any(room.raw)
+
+
+@pytest.mark.gpu
+def test_a_step_in_which_nobody_leaves_or_forks():
+    def ints(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    table, lengths, refs, none = ints([[0, 1], [2, -1]]), ints([7, 3]), ints([1, 1, 1, 0]), ints([])
+    fd.pages_free(table, lengths, refs, 4, seqs=none)
+    fd.pages_free(table, lengths, refs, 4, seqs=none, lengths=none)
+    fd.pages_fork(table, lengths, refs, 4, none, none)
+    fd.pages_fork(table, lengths, refs, 4, none, none, none)
+    assert table.tolist() == [[0, 1], [2, -1]] and lengths.tolist() == [7, 3] and refs.tolist() == [1, 1, 1, 0]
+    with pytest.raises(ValueError):
+        fd.pages_fork(table, lengths, refs, 4, none, ints([1]))
