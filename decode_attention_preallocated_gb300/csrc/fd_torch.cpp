@@ -235,6 +235,8 @@ struct Table {
         if (o == Py_None) return;
         p = ints(o, B, kAny, "block_table", dev);
         max_pages = (int32_t)THPVariable_Unpack(o).size(1);
+        // (an empty one has no address, which the C ABI reads as a flat cache)
+        if (!p) raise(PyExc_ValueError, "block_table must have room for a page");
     }
 };
 
