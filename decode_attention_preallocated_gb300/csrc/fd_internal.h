@@ -113,6 +113,17 @@ struct Split {
 
 FD_HD int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The run of `total` items (below 2^31) that the thread-th of `threads` threads
+// takes: [lo, hi), empty past the items.
+struct Run {
+    int32_t lo, hi;
+};
+FD_HD Run run_of(int32_t total, int32_t threads, int32_t thread) {
+    const int32_t per = total / threads + (total % threads != 0);
+    const int64_t lo = (int64_t)thread * per, hi = lo + per;
+    return Run{(int32_t)(lo < total ? lo : total), (int32_t)(hi < total ? hi : total)};
+}
+
 // Floats in one workspace slot: O[rows][d], then m[rows] and l[rows], padded
 // so that every slot starts on a 16-byte boundary.
 FD_HD int64_t slot_floats(int64_t rows, int64_t d) {

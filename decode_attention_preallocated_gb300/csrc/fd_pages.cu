@@ -331,10 +331,9 @@ struct Ranges {
     // for this thread's entries, in order.
     template <typename F>
     __device__ __forceinline__ void each(const Books &k, const Cluster &c, F f) const {
-        const int per = (total + c.threads - 1) / c.threads;
-        const int64_t from = (int64_t)c.thread * per;
-        if (from >= total) return;
-        const int lo = (int)from, hi = min(total, lo + per);
+        const Run run = run_of(total, c.threads, c.thread);
+        const int lo = run.lo, hi = run.hi;
+        if (lo >= hi) return;
         int b = 0, top = n;   // the last sequence that starts at or before lo
         while (top - b > 1) {
             const int mid = (b + top) >> 1;
