@@ -22,6 +22,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfd.so")
 NATIVE_SRC = os.path.join(CSRC, "fd_torch.cpp")
 NATIVE = os.path.join(HERE, "_fd_torch.so")
+NATIVE_FOR = os.path.join(BUILD_DIR, "_fd_torch.for")   # the versions it was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", "--expt-relaxed-constexpr",
@@ -55,10 +56,13 @@ def up_to_date() -> bool:
 
 def build_native(force: bool = False) -> str:
     """The marshalling extension, against the headers and libraries of the
-    installed PyTorch."""
-    if not force and _newer(NATIVE, [NATIVE_SRC, os.path.join(INCLUDE, "fd.h"), __file__]):
-        return NATIVE
+    installed PyTorch; built again where another one, or another Python, is
+    installed than the one it was built for."""
     import torch
+    built_for = "torch %s, %s\n" % (torch.__version__, sysconfig.get_config_var("SOABI"))
+    if not force and _newer(NATIVE, [NATIVE_SRC, os.path.join(INCLUDE, "fd.h"), __file__]) \
+            and os.path.exists(NATIVE_FOR) and open(NATIVE_FOR).read() == built_for:
+        return NATIVE
     home = os.path.dirname(torch.__file__)
     include = os.path.join(home, "include")
     tmp = NATIVE + ".tmp%d" % os.getpid()
@@ -71,7 +75,12 @@ def build_native(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("%s failed on %s:\n%s%s" % (cmd[0], NATIVE_SRC, r.stdout, r.stderr))
+    if os.path.exists(NATIVE_FOR):
+        os.remove(NATIVE_FOR)   # (a build that ends here is seen as none)
     os.replace(tmp, NATIVE)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(NATIVE_FOR, "w") as f:
+        f.write(built_for)
     return NATIVE
 
 
