@@ -194,14 +194,13 @@ __device__ __forceinline__ bool piece_at(const Seg &g, uint32_t t, uint32_t t_en
     return t0 < t1;
 }
 
-// The first piece of units [t, t_end).
+// The first piece of units [t, t_end).  (Where t lies in the price of a segment
+// whose tiles another block has, the block has none: t_end is at most the first
+// of them.)
 template <int TILE>
 __device__ __forceinline__ bool first_piece(Finder<TILE> &f, uint32_t t, uint32_t t_end, Seg &g,
                                             uint32_t &t0, uint32_t &t1) {
     f.find(t, g);
-    if (piece_at(g, t, t_end, t0, t1)) return true;
-    if (g.first + g.tiles >= t_end) return false;
-    f.next(g);   // (t lay in the price of a segment whose tiles another block has)
     return piece_at(g, t, t_end, t0, t1);
 }
 
