@@ -514,9 +514,9 @@ int fd_read_fp4(const fd_tensor *k_cache, const fd_tensor *v_cache, const fd_ten
  *   page may be both copied from and copied to, nor be copied to twice.
  *
  * reserve and compact use fd_pages_scratch_bytes(num_pages) bytes of the
- * workspace's room for split partials (the room is
- * fd_workspace_bytes(segments, rows, head_dim, ctas) less about 4 * segments
- * bytes).
+ * workspace's room for split partials (the room is at least
+ * fd_workspace_bytes(segments, rows, head_dim, ctas) less 8 * segments + 4 *
+ * ctas + 1024 bytes).
  */
 size_t fd_pages_scratch_bytes(int64_t num_pages);
 int fd_pages_reserve(int32_t *block_table, int32_t B, int32_t max_pages,

@@ -1,4 +1,5 @@
-"""What the page calls take: lists with nothing in them."""
+"""What the page calls take: lists with nothing in them, a workspace sized by
+the header."""
 import ctypes
 
 import pytest
@@ -39,6 +40,14 @@ def test_a_list_of_nothing_is_no_error(L):
     assert L.fd_pages_fork(PTR, 2, 4, PTR, 16, PTR, 10, None, PTR, None, 1, o) == fd.FD_ERR_ARG
     assert L.fd_pages_fork(PTR, 2, 4, PTR, 16, PTR, 10, PTR, PTR, None, -1, o) == fd.FD_ERR_ARG
     assert not any(room.raw)
+
+
+@pytest.mark.parametrize("segments,rows,head_dim,ctas", [(1, 1, 1, 1), (1, 1, 128, 1), (64, 16, 256, 1024), (1, 64, 256, 65535),
+                                                         (1000001, 1, 128, 7), (3, 5, 100, 100003)])
+def test_the_room_of_a_workspace_is_what_the_header_says(L, segments, rows, head_dim, ctas):
+    room = (segments + ctas) * fd.slot_floats(rows, head_dim) * 4     # of the split partials
+    said = L.fd_workspace_bytes(segments, rows, head_dim, ctas) - (8 * segments + 4 * ctas + 1024)
+    assert room - 1024 <= said <= room
 
 
 @pytest.mark.gpu
