@@ -361,14 +361,24 @@ int fd_pages_copy(const fd_tensor *pools, int32_t n_pools, const int32_t *pairs,
         const int rc = check_tensor(&t, t.ndim);
         if (rc) return rc;
         if (t.shape[0] != pools[0].shape[0] || t.shape[0] < 1 || t.shape[0] > (1 << 30)) return FD_ERR_ARG;
-        // the page's elements and the memory they span
-        int64_t elems = 1, span = 1;
+        // the page's elements fill [0, elems): taken by increasing stride, each
+        // dimension of more than one steps by what those before it fill
+        int64_t elems = 1;
+        bool left[4] = {true, true, true, true};
         for (int j = 1; j < t.ndim; ++j) {
             if (t.shape[j] < 1) return FD_ERR_ARG;
-            elems *= t.shape[j];
-            span += (t.shape[j] - 1) * t.stride[j];
+            left[j] = t.shape[j] > 1;
         }
-        if (span != elems || (t.shape[0] > 1 && t.stride[0] < span)) return FD_ERR_ARG;
+        for (;;) {
+            int next = 0;
+            for (int j = 1; j < t.ndim; ++j)
+                if (left[j] && (next == 0 || t.stride[j] < t.stride[next])) next = j;
+            if (next == 0) break;
+            if (t.stride[next] != elems) return FD_ERR_ARG;
+            elems *= t.shape[next];
+            left[next] = false;
+        }
+        if (t.shape[0] > 1 && t.stride[0] < elems) return FD_ERR_ARG;
         q.base[i] = static_cast<uint8_t *>(t.data);
         q.step[i] = t.stride[0] * esize(t.dtype);
         q.bytes[i] = elems * esize(t.dtype);

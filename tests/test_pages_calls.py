@@ -1,5 +1,5 @@
-"""What the page calls take: lists with nothing in them, a workspace sized by
-the header."""
+"""What the page calls take: lists with nothing in them, pages of any order
+of dimensions, a workspace sized by the header."""
 import ctypes
 
 import pytest
@@ -40,6 +40,25 @@ def test_a_list_of_nothing_is_no_error(L):
     assert L.fd_pages_fork(PTR, 2, 4, PTR, 16, PTR, 10, None, PTR, None, 1, o) == fd.FD_ERR_ARG
     assert L.fd_pages_fork(PTR, 2, 4, PTR, 16, PTR, 10, PTR, PTR, None, -1, o) == fd.FD_ERR_ARG
     assert not any(room.raw)
+
+
+@pytest.mark.parametrize("shape,strides,dense", [
+    ((10, 2, 3), (6, 3, 1), True), ((10, 2, 3), (6, 1, 2), True), ((10, 2, 3), (7, 3, 1), True),
+    ((10,), (1,), True), ((10,), (3,), True), ((10, 1, 4), (4, 99, 1), True), ((10, 1, 1), (1, 5, 7), True),
+    ((10, 3, 2), (6, 1, 3), True),
+    ((10, 4, 2, 3), (24, 2, 1, 8), True), ((1, 2, 3), (0, 3, 1), True),
+    # as many elements as the memory they span, but some of them the same and
+    # memory of others between
+    ((10, 2, 3), (6, 5, 0), False), ((10, 2, 2, 2), (8, 3, 3, 1), False),
+    ((10, 2, 3), (8, 4, 1), False), ((10, 3), (3, 0), False), ((10, 2, 3), (5, 3, 1), False),
+])
+def test_pages_that_do_not_fill_their_memory_are_refused(L, shape, strides, dense):
+    t = fd.FdTensor()
+    t.data, t.dtype, t.ndim = PTR, fd.FD_U8, len(shape)
+    t.shape[:len(shape)], t.stride[:len(shape)] = shape, strides
+    o = fd.FdOpts()     # (no workspace: what is left to refuse)
+    rc = L.fd_pages_copy(ctypes.byref(t), 1, PTR, PTR, 4, ctypes.byref(o))
+    assert rc == (fd.FD_ERR_WORKSPACE if dense else fd.FD_ERR_ARG)
 
 
 @pytest.mark.parametrize("segments,rows,head_dim,ctas", [(1, 1, 1, 1), (1, 1, 128, 1), (64, 16, 256, 1024), (1, 64, 256, 65535),
