@@ -622,18 +622,21 @@ _OPTS = struct.Struct("PPiifi2i")      # fd_opts
 _PAD = ((), (0, 0, 0), (0, 0), (0,), ())
 
 
-def _pack(t: torch.Tensor, _pack4=_TENSOR.pack, _types=_DTYPES) -> bytes:
-    """fd_tensor of a tensor, as bytes."""
+# what stands for a dtype where only its size matters
+_SIZES = {1: FD_U8, 2: FD_BF16, 4: FD_F32}
+
+
+def _pack(t: torch.Tensor) -> bytes:
+    """fd_tensor of a pool, as bytes."""
     shape = t.shape
-    if len(shape) == 4 and t.dtype in _types:
-        return _pack4(t.data_ptr(), _types[t.dtype], 4, *shape, *t.stride())
-    if t.dtype not in _types:
+    kind = _DTYPES.get(t.dtype, _SIZES.get(t.element_size()))
+    if kind is None:
         raise TypeError("unsupported dtype %s" % t.dtype)
     n = len(shape)
-    if not 1 <= n <= 3:
+    if not 1 <= n <= 4:
         raise ValueError("1 to 4 dimensions")
     pad = _PAD[n]
-    return _pack4(t.data_ptr(), _types[t.dtype], n, *shape, *pad, *t.stride(), *pad)
+    return _TENSOR.pack(t.data_ptr(), kind, n, *shape, *pad, *t.stride(), *pad)
 
 
 def _empty(shape, dtype, index, stream):
@@ -754,9 +757,10 @@ def pages_compact(block_table, refs, pairs=None, count=None, stream=None,
 
 
 class PagePools:
-    """The pools of a paged cache ([num_pages, ...] CUDA tensors of any dtype:
-    codes, scales, of K and V, of every layer) as ``pages_copy`` wants them;
-    made once, kept with the pools, whose memory it holds on to."""
+    """The pools of a paged cache ([num_pages, ...] CUDA tensors of 1 to 4
+    dimensions and of any dtype of 1, 2 or 4 bytes: codes, scales, of K and V, of
+    every layer) as ``pages_copy`` wants them; made once, kept with the pools,
+    whose memory it holds on to."""
 
     def __init__(self, pools):
         self.pools = list(pools)

@@ -82,3 +82,28 @@ def test_a_step_in_which_nobody_leaves_or_forks():
     assert table.tolist() == [[0, 1], [2, -1]] and lengths.tolist() == [7, 3] and refs.tolist() == [1, 1, 1, 0]
     with pytest.raises(ValueError):
         fd.pages_fork(table, lengths, refs, 4, none, ints([1]))
+
+
+def test_a_dtype_is_packed_by_its_size():
+    def kind(dtype):
+        return fd.FdTensor.from_buffer_copy(fd._pack(torch.zeros(3, 2, dtype=dtype))).dtype
+
+    assert [kind(t) for t in (torch.bfloat16, torch.float32, torch.int8, torch.int32, torch.uint8, torch.float8_e4m3fn)] == \
+        [fd.FD_BF16, fd.FD_F32, fd.FD_I8, fd.FD_I32, fd.FD_U8, fd.FD_E4M3]
+    assert kind(torch.float16) == kind(torch.int16) == fd.FD_BF16
+    assert kind(torch.bool) == kind(torch.float8_e5m2) == fd.FD_U8
+    for dtype in (torch.int64, torch.float64, torch.complex64):
+        with pytest.raises(TypeError):
+            kind(dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.int16, torch.bool, torch.float8_e5m2, torch.int32])
+def test_pools_of_any_dtype_are_copied(dtype):
+    raw = torch.randint(0, 2 if dtype == torch.bool else 120, (9, 3, 8, 16), dtype=torch.uint8, device="cuda")
+    pool = raw.view(dtype)
+    want = raw.clone()
+    want[0], want[5] = raw[7], raw[8]
+    pairs = torch.tensor([[7, 0], [8, 5]], dtype=torch.int32, device="cuda")
+    fd.pages_copy([pool], pairs, torch.tensor([2], dtype=torch.int32, device="cuda"))
+    assert torch.equal(raw, want)
