@@ -235,8 +235,9 @@ fp4_decode_kernel(const __grid_constant__ Fp4Params fp) {
     const auto begin_piece = [&](const Seg &g, uint32_t t0, uint32_t t1) {
         len = g.len;
         seq = g.b;
-        start = (int)((t0 - g.first) * C::TILE) + stream * kSub;
-        steps = start >= len ? 0 : min((int)(t1 - t0), (int)(((unsigned)(len - start) + (C::TILE - 1u)) / C::TILE));
+        const uint32_t from = (t0 - g.first) * C::TILE + stream * kSub;
+        start = (int)from;   // (not used where it passes 2^31: there are no steps)
+        steps = steps_from(from, len, t1 - t0, C::TILE);
         kb = static_cast<const uint8_t *>(p.k) + (int64_t)g.hk * p.ks[1] + t4x16;
         vb = static_cast<const uint8_t *>(p.v) + (int64_t)g.hk * p.vs[1] + t4x16;
         ksb = fp.ks + (int64_t)g.hk * fp.kss[1] + half * 8;

@@ -124,6 +124,14 @@ FD_HD Run run_of(int32_t total, int32_t threads, int32_t thread) {
     return Run{(int32_t)(lo < total ? lo : total), (int32_t)(hi < total ? hi : total)};
 }
 
+// Steps of a stream that covers positions start + n * tile of a prefix of `len`
+// (below 2^31), at most `tiles` of them.  start may pass len, and 2^31.
+FD_HD int32_t steps_from(uint32_t start, uint32_t len, uint32_t tiles, uint32_t tile) {
+    if (start >= len) return 0;
+    const uint32_t n = (len - start + (tile - 1)) / tile;
+    return (int32_t)(n < tiles ? n : tiles);
+}
+
 // Floats in one workspace slot: O[rows][d], then m[rows] and l[rows], padded
 // so that every slot starts on a 16-byte boundary.
 FD_HD int64_t slot_floats(int64_t rows, int64_t d) {
