@@ -442,6 +442,7 @@ int fd_workspace_create(int64_t max_segments, int32_t max_rows, int32_t head_dim
     if (!ws) return FD_ERR_ARG;
     void *base = nullptr;
     if (cudaMalloc(&base, L.total) != cudaSuccess) {
+        cudaGetLastError();   // (the next call's launch is not to be blamed for it)
         delete ws;
         return FD_ERR_CUDA;
     }

@@ -190,3 +190,17 @@ def test_two_threads_share_a_workspace_and_its_scratch():
         t.join(120)
     assert not any(t.is_alive() for t in threads) and not errors
     assert counts == [2 * steps, steps]
+
+
+@pytest.mark.gpu
+def test_a_workspace_that_does_not_fit_the_device_fails_no_later_call():
+    from fp4_util import bf16, cache as quantised, to_dev
+    fdbuild.build()
+    rng = np.random.default_rng(86)
+    (kd, ksd), (vd, vsd) = (to_dev(*quantised(rng, 1, 2, 300, 128)) for _ in range(2))
+    q, lens = bf16(rng, (1, 1, 8, 128)).cuda(), torch.tensor([300], dtype=torch.int32, device="cuda")
+    want = fd.decode_fp4(q, kd, vd, ksd, vsd, lens)
+    with pytest.raises(fd.FdError) as e:
+        fd.Workspace(1 << 31, 64, 256, 1 << 30)          # some 200 TB
+    assert e.value.code == fd.FD_ERR_CUDA
+    assert torch.equal(fd.decode_fp4(q, kd, vd, ksd, vsd, lens), want)
