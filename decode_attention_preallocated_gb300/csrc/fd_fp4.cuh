@@ -1,5 +1,5 @@
 // fd_fp4.cuh -- the 4-bit cache format on the device, shared by the kernels
-// that read it (fd_fp4_decode.cu, fd_fp4_rows.cu) and the one that writes it.
+// that read it (fd_fp4_decode.cuh, fd_fp4_rows.cu) and the one that writes it.
 //
 // A row of d values is d/2 bytes of e2m1 codes (value 2j in byte j's low
 // nibble, 2j+1 in its high one) and d/16 e4m3 scales, one per 16 consecutive

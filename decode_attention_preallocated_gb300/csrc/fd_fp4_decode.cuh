@@ -5,7 +5,7 @@
 // What it computes, per query row: s_j = scale * q . k_j over the visible
 // positions, w_j = 2^(s_j log2 e - m), out = sum_j w_j v_j / sum_j w_j, in one
 // pass with a running reference m.  A position costs d/2 + d/16 bytes of K and
-// as many of V, a quarter of a bf16 cache.
+// as many of V, 0.28 of a bf16 cache's.
 //
 // Layout.  A warp walks 32 positions at a time through a private cp.async ring,
 // turns the codes into fp16 operands in registers and feeds mma.sync m16n8k16,
@@ -35,14 +35,17 @@
 // the weight or 2^-37 of the largest, for twice the MMAs on V.  The sums, the
 // reference and both accumulators are fp32.
 //
-// What bounds it.  4 rows at d = 128, 4 sequences of 131,072 positions: 111.6 us,
-// 5.4 TB/s (0.80 of a copy), DRAM and about 10 us of start and end.  24 rows at
-// d = 256, 8 ragged sequences up to 32,768: 76.9 us, of which the MMAs need 43;
-// the rest is latency with 8 warps an SM.  64 ragged sequences up to 4,096 over
-// pages of 16: 60.2 us, with 2.4 pieces a block.  A step of 32 positions is 640
-// instructions (one eight of rows, flat), half of them widening codes.
-//   fp32 outputs: 4 sequences of 131,072 positions 126.6 us against 113.2 for
-// bf16; 24 rows at d = 256, 8 sequences of 16,384, 82.6 against 65.4.
+// What bounds it.  4 rows at d = 128, 4 sequences of 131,072 positions: 113.7 us,
+// 5.3 TB/s (0.78 of a copy), DRAM and about 10 us of start and end.  24 rows at
+// d = 256, 8 ragged sequences up to 32,768: 79.0 us; 8 of 16,384 66.4, in which
+// the tensor pipe is busy for 26 us and the issue slots for 29: the latency of a
+// step with 8 warps an SM.  64 ragged sequences up to 4,096 over pages of 16:
+// 60.4 us, with 2.4 pieces a block.  A step of 32 positions is 640 instructions
+// (one eight of rows, flat), half of them widening codes.  More than 32 rows are
+// two parts, each of which reads and widens the whole prefix: 60 rows at d = 256,
+// 8 sequences of 16,384, 145 us against 87 for 30.
+//   fp32 outputs: 4 sequences of 131,072 positions 126.6 us against 113.4 for
+// bf16; 24 rows at d = 256, 8 sequences of 16,384, 82 against 66.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -7,7 +7,7 @@
 
 namespace fd {
 
-// Decode over a 4-bit cache (fd_fp4_decode.cu).  `p` describes the launch to
+// Decode over a 4-bit cache (fd_fp4_decode.cuh).  `p` describes the launch to
 // the split partitioner: p.k / p.v are the code caches (strides in bytes), a
 // segment is (sequence, kv head, part of the kv head's query rows), p.Hkv
 // counts (kv head, part) pairs and p.rows the rows of a part.

@@ -12,10 +12,10 @@
 // reserve and compact need ranks over the whole pool, hence barriers; they run
 // as one block, or one thread-block cluster for large pools, whose barrier costs
 // far less than another launch, with a thread per table entry and 128 pages per
-// warp step.  64 sequences leave and 64 come in 256 of 512 entries: 15.6 us for
-// the two calls; 3 children of one sequence forked, reserved for and their page
-// copied: 16.3 us for three; 10,192 pages ranked 9 to 12 us, renumbered 4, and 45 MB of
-// them copied 15.7, the rate of a plain copy.
+// warp step.  64 sequences leave and 64 come in 256 of 512 entries: 16.0 us for
+// the two calls; 3 children of one sequence freed, forked, reserved for and their
+// page copied: 15 to 18 us for the four; 10,192 pages ranked 9 to 12 us, renumbered
+// 4, and 45 MB of them copied 15.7, the rate of a plain copy.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

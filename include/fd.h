@@ -435,8 +435,9 @@ int fd_decode_fp4(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor 
  *   16 values x share s = e4m3(max|x| / (6 * global)), rounded to nearest even
  *   and at most 448; their codes are e2m1(x / (s * global)), to nearest, ties
  *   to the even code, at most 6 (with the quotient's sign; s = 0 gives zero
- *   codes).  Where one of them is a NaN or an infinity the scale is NaN and
- *   the codes are 0.
+ *   codes).  6 * global, s * global and both quotients are rounded to fp32
+ *   first.  Where one of the values is a NaN or an infinity the scale is NaN
+ *   and the codes are 0.
  *   lengths_out: device int32[B], gets min(base_b + new_b, cap); may be
  *   kv_lengths itself (but overlap it in no other way), or NULL.
  * FD_DEV_BAD_LENGTH is set where a length, a new length or base_b + new_b is
