@@ -1,4 +1,4 @@
-// fd_pages.cu -- page bookkeeping of a paged cache: freeing, forking,
+// fd_pages.cu -- page bookkeeping of a paged cache: freeing, forking, reordering,
 // reserving (with copy on write), compacting, and the copies of pages that
 // the last two ask for.
 //
@@ -32,6 +32,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024;
+constexpr int kReorderThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr unsigned kAll = 0xffffffffu;
@@ -122,6 +123,60 @@ __global__ void fork_kernel(const Books k, const int32_t *src, const int32_t *ds
         to[j] = e;
     }
     if (threadIdx.x == 0) k.lengths[d] = (int)L;
+}
+
+// Rows change places only within a column, so a block takes some columns of
+// every row into shared memory and writes them back in their new places; the
+// lengths, which every block reads, are written by the last one to finish.
+__global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const Books k, const int32_t *src, int cols,
+                                                                  int32_t *ticket) {
+    extern __shared__ int32_t old[];
+    const int c0 = blockIdx.x * cols, width = min(cols, k.max_pages - c0);
+    const int cells = k.B * cols;
+    for (int e = threadIdx.x; e < cells; e += kReorderThreads) {
+        const int b = e / cols, c = e - b * cols;
+        if (c < width) old[e] = k.table[(int64_t)b * k.max_pages + c0 + c];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < cells; e += kReorderThreads) {
+        const int b = e / cols, c = e - b * cols;
+        if (c >= width) continue;
+        const int s = src[b];
+        if (s == b) continue;
+        if (s >= k.B) {
+            if (c0 + c == 0) flag(k, FD_DEV_BAD_INDEX);
+            continue;
+        }
+        const int j = c0 + c, was = old[e];
+        int to = -1;
+        if (s >= 0 && j < pages_of(held(k, s), k.page_size)) {
+            to = old[s * cols + c];
+            if (to < 0 || to >= k.num_pages) {
+                flag(k, FD_DEV_BAD_INDEX);
+                to = -1;
+            }
+        }
+        if (to == was) continue;
+        if (to >= 0) atomicAdd(k.refs + to, 1);
+        drop(k, was);
+        k.table[(int64_t)b * k.max_pages + j] = to;
+    }
+    __shared__ int last;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
+        if (last) __threadfence();
+    }
+    __syncthreads();
+    if (!last) return;
+    for (int b = threadIdx.x; b < k.B; b += kReorderThreads) {
+        const int s = src[b];
+        old[b] = s == b || s >= k.B ? k.lengths[b] : s < 0 ? 0 : (int)held(k, s);
+    }
+    __syncthreads();
+    for (int b = threadIdx.x; b < k.B; b += kReorderThreads) k.lengths[b] = old[b];
+    if (threadIdx.x == 0) *ticket = 0;
 }
 
 // ------------------------------------------------------------ one cluster
@@ -639,6 +694,18 @@ int launch_pages_free(const Books &k, const int32_t *seqs, const int32_t *length
 int launch_pages_fork(const Books &k, const int32_t *src, const int32_t *dst, const int32_t *lengths,
                       int n, cudaStream_t st) {
     fork_kernel<<<n, 256, 0, st>>>(k, src, dst, lengths, n);
+    return cudaGetLastError() == cudaSuccess ? 0 : -5;
+}
+
+int launch_pages_reorder(const Books &k, const int32_t *src, int32_t *ticket, cudaStream_t st) {
+    int cols = 32;
+    while (cols > 1 && (int64_t)k.B * cols > kReorderRows) cols /= 2;
+    const int bytes = k.B * cols * 4;
+    if (bytes > 48 * 1024 && cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  kReorderRows * 4) != cudaSuccess)
+        return -5;
+    const unsigned blocks = (unsigned)ceil_div(k.max_pages, cols);
+    reorder_kernel<<<blocks, kReorderThreads, bytes, st>>>(k, src, cols, ticket);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 

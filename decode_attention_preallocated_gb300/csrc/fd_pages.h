@@ -37,6 +37,9 @@ int launch_pages_free(const Books &k, const int32_t *seqs, const int32_t *length
                       cudaStream_t st);
 int launch_pages_fork(const Books &k, const int32_t *src, const int32_t *dst,
                       const int32_t *lengths, int n, cudaStream_t st);
+// Rows that one block of the reordering holds a column of.
+constexpr int kReorderRows = 49152;
+int launch_pages_reorder(const Books &k, const int32_t *src, int32_t *ticket, cudaStream_t st);
 int launch_pages_reserve(const Books &k, const int32_t *n_new, int n_each, int32_t *pairs,
                          int32_t *count, int32_t *scratch, cudaStream_t st);
 int launch_pages_compact(const Books &k, int32_t *pairs, int32_t *count, int32_t *scratch,

@@ -1,5 +1,5 @@
-// fd_torch.cpp -- argument marshalling of the 4-bit cache and page calls for
-// fd.py, as a Python extension: torch tensors become fd_tensor descriptors and
+// fd_torch.cpp -- argument marshalling of the 4-bit cache and page calls, of
+// append, prefill and the beam selection for fd.py, as a Python extension: torch tensors become fd_tensor descriptors and
 // addresses, what the C ABI cannot see (devices, and types and shapes of the
 // int32 arrays) is checked, outputs are allocated, and libfd.so is called.  No
 // arithmetic and no kernel of its own.
@@ -31,6 +31,12 @@ struct {
     decltype(&fd_pages_free) free;
     decltype(&fd_pages_compact) compact;
     decltype(&fd_pages_copy) copy;
+    decltype(&fd_pages_reorder) reorder;
+    decltype(&fd_append) append_rows;
+    decltype(&fd_prefill) prefill;
+    decltype(&fd_prefill_scratch_bytes) prefill_scratch;
+    decltype(&fd_beam_select) beam;
+    decltype(&fd_beam_scratch_bytes) beam_scratch;
 } fd;
 PyObject *workspaces;   // {(device, stream): Workspace}
 PyObject *opts_for;     // (workspace, device, stream, segments, rows, ctas, num_ctas) -> fd_opts as bytes
@@ -335,12 +341,13 @@ struct Books {
 };
 
 // Segments of a default workspace (16 rows of head_dim 256 and two numbers each,
-// for every segment and for 1024 blocks) whose room holds the scratch of reserve
-// and compact.
-int64_t scratch_slots(int64_t num_pages) {
-    const int64_t n = 3 * num_pages / (16 * (256 + 2)) - 1000;
+// for every segment and for 1024 blocks) whose room holds so many words.
+int64_t word_slots(int64_t words) {
+    const int64_t n = words / (16 * (256 + 2)) - 1000;
     return n > 1 ? n : 1;
 }
+// ... the scratch of reserve and compact
+int64_t scratch_slots(int64_t num_pages) { return word_slots(3 * num_pages); }
 
 // table, lengths, refs, page_size, n_new, pairs, count, stream, workspace
 PyObject *reserve(PyObject *const *a) {
@@ -423,11 +430,138 @@ PyObject *copy(PyObject *const *a) {
     return none();
 }
 
-// addresses of the eight calls, the workspaces, opts_for, empty_on, FdError
+// table, lengths, refs, page_size, src, stream, workspace
+PyObject *reorder(PyObject *const *a) {
+    Device dev;
+    const Books k(a[0], a[1], a[2], dev);
+    const int32_t page = whole(a[3]);
+    const int32_t *src = ints(a[4], k.B, kNone, "src", dev);
+    run("fd_pages_reorder", dev, a[5], a[6], 1, 1, 1, 0, [&](const fd_opts *o) {
+        return fd.reorder(k.table, k.B, k.max_pages, k.lens, page, k.refs, k.num_pages, src, o);
+    });
+    return none();
+}
+
+// A tensor that may be None.
+struct Maybe {
+    fd_tensor t{};
+    const fd_tensor *p = nullptr;
+    Maybe(PyObject *o, const char *name, Device &dev) {
+        if (o == Py_None) return;
+        t = describe(tensor(o, name), dev);
+        p = &t;
+    }
+    Maybe(const Maybe &) = delete;
+};
+
+// k_new, v_new, k, v, lengths, new_lengths, lengths_out, q, q_out, rope, interleaved, k_scale, v_scale, table, stream,
+// workspace
+PyObject *append_rows(PyObject *const *a) {
+    Device dev;
+    const at::Tensor &tk = tensor(a[0], "k_new");
+    if (tk.dim() != 4) raise(PyExc_ValueError, "k_new must have four dimensions");
+    const fd_tensor kn = describe(tk, dev), vn = describe(tensor(a[1], "v_new"), dev);
+    const fd_tensor k = describe(tensor(a[2], "k_cache"), dev), v = describe(tensor(a[3], "v_cache"), dev);
+    const int64_t B = kn.shape[0];
+    const int32_t *lens = ints(a[4], B, kNone, "kv_lengths", dev);
+    const int32_t *fresh = ints(a[5], B, kNone, "new_lengths", dev, true);
+    int32_t *after = ints(a[6], B, kNone, "lengths_out", dev, true);
+    if (a[7] == Py_None && a[8] != Py_None) raise(PyExc_ValueError, "q_out without q");
+    const Maybe q(a[7], "q", dev);
+    Ref to(a[7] == Py_None || a[8] != Py_None
+               ? Py_NewRef(a[8])
+               : THPVariable_Wrap(make(THPVariable_Unpack(a[7]).sizes(), at::kBFloat16,
+                                       reinterpret_cast<PyObject *>(torch::getTHPDtype(at::kBFloat16)), dev, a[14])));
+    const Maybe q_out(to.p, "q_out", dev), rope(a[9], "rope", dev);
+    const bool interleaved = truth(a[10]);
+    const Maybe ks(a[11], "k_scale", dev), vs(a[12], "v_scale", dev);
+    const Table t(a[13], B, dev);
+    run("fd_append", dev, a[14], a[15], 1, 1, 1, 0, [&](const fd_opts *o) {
+        return fd.append_rows(&kn, &vn, fresh, q.p, q_out.p, rope.p, interleaved, &k, &v, ks.p, vs.p, t.p, t.max_pages, lens,
+                              after, o);
+    });
+    return Py_NewRef(to.p);
+}
+
+// q, k, v, lengths, new_lengths, causal, scale, k_scale, v_scale, table, out, num_ctas, kernel, stream, workspace
+PyObject *prefill(PyObject *const *a) {
+    Device dev;
+    const at::Tensor &tq = tensor(a[0], "q");
+    if (tq.dim() != 4) raise(PyExc_ValueError, "q must have four dimensions");
+    const fd_tensor q = describe(tq, dev);
+    const fd_tensor k = describe(tensor(a[1], "k_cache"), dev), v = describe(tensor(a[2], "v_cache"), dev);
+    const int64_t B = q.shape[0];
+    const int32_t *lens = ints(a[3], B, kNone, "kv_lengths", dev);
+    const int32_t *fresh = ints(a[4], B, kNone, "new_lengths", dev, true);
+    const bool causal = truth(a[5]);
+    const float scale = a[6] == Py_None ? (float)(1.0 / std::sqrt((double)q.shape[3])) : number(a[6]);
+    const Maybe ks(a[7], "k_scale", dev), vs(a[8], "v_scale", dev);
+    const Table t(a[9], B, dev);
+    const int32_t num_ctas = whole(a[11]), kernel = whole(a[12]);
+    const at::Tensor made = a[10] == Py_None
+                                ? make(tq.sizes(), at::kBFloat16, reinterpret_cast<PyObject *>(torch::getTHPDtype(at::kBFloat16)), dev, a[13])
+                                : tensor(a[10], "out");
+    const fd_tensor out = describe(made, dev);
+    const int64_t room = [&] {
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev.index);
+        return (int64_t)fd.prefill_scratch(num_ctas, (int32_t)q.shape[3]);
+    }();
+    run("fd_prefill", dev, a[13], a[14], word_slots(room / 4), 1, 1, num_ctas, [&](const fd_opts *o) {
+        fd_opts with = *o;
+        with.kernel = kernel;
+        return fd.prefill(&q, &k, &v, ks.p, vs.p, t.p, t.max_pages, lens, fresh, causal, scale, &out, &with);
+    });
+    return a[10] == Py_None ? THPVariable_Wrap(made) : Py_NewRef(a[10]);
+}
+
+// logits, scores, n_out, finished, end_token, out, stream, workspace
+PyObject *beam(PyObject *const *a) {
+    Device dev;
+    const at::Tensor &tl = tensor(a[0], "logits");
+    if (tl.dim() != 3) raise(PyExc_ValueError, "logits must have three dimensions");
+    const fd_tensor logits = describe(tl, dev);
+    const int64_t B = logits.shape[0], K = logits.shape[1];
+    const at::Tensor &ts = tensor(a[1], "scores");
+    dev.on(ts);
+    if (ts.scalar_type() != at::kFloat || ts.dim() != 2 || ts.size(0) != B || ts.size(1) != K || !ts.is_contiguous())
+        raise(PyExc_ValueError, "scores must be a contiguous float32 [B, K] tensor");
+    const int32_t n = whole(a[2]);
+    const int32_t *finished = ints(a[3], B, K, "finished", dev, true);
+    const int32_t end = a[4] == Py_None ? -1 : whole(a[4]);
+    if (n < 1) raise(PyExc_ValueError, "n_out must be positive");
+    at::Tensor out[3];
+    if (a[5] == Py_None) {
+        for (int i = 0; i < 3; ++i) {
+            const at::ScalarType type = i == 0 ? at::kFloat : at::kInt;
+            out[i] = make({B, n}, type, reinterpret_cast<PyObject *>(torch::getTHPDtype(type)), dev, a[6]);
+        }
+    } else {
+        Ref three(PySequence_Fast(a[5], "out must be three tensors"));
+        if (PySequence_Fast_GET_SIZE(three.p) != 3) raise(PyExc_ValueError, "out must be three tensors");
+        for (int i = 0; i < 3; ++i) {
+            out[i] = tensor(PySequence_Fast_GET_ITEM(three.p, i), "out");
+            dev.on(out[i]);
+            if (out[i].scalar_type() != (i == 0 ? at::kFloat : at::kInt) || out[i].dim() != 2 || out[i].size(0) != B ||
+                out[i].size(1) != n || !out[i].is_contiguous())
+                raise(PyExc_ValueError, "out must be contiguous [B, n_out] tensors: float32, int32, int32");
+        }
+    }
+    const int64_t room = K <= INT32_MAX ? (int64_t)fd.beam_scratch(B, (int32_t)K, logits.shape[2], n) : 0;
+    const int64_t slots = word_slots(room / 4);
+    run("fd_beam_select", dev, a[6], a[7], slots > B ? slots : B, 1, 1, 0, [&](const fd_opts *o) {
+        return fd.beam(&logits, static_cast<const float *>(ts.data_ptr()), finished, end, n, static_cast<float *>(out[0].data_ptr()),
+                       static_cast<int32_t *>(out[1].data_ptr()), static_cast<int32_t *>(out[2].data_ptr()), o);
+    });
+    Ref s(THPVariable_Wrap(out[0])), b(THPVariable_Wrap(out[1])), t(THPVariable_Wrap(out[2]));
+    return PyTuple_Pack(3, s.p, b.p, t.p);
+}
+
+// addresses of the calls, the workspaces, opts_for, empty_on, FdError
 PyObject *bind(PyObject *const *a) {
     void **const to = reinterpret_cast<void **>(&fd);
-    if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != 8 || !PyDict_Check(a[1])) raise(PyExc_TypeError, "bind");
-    for (Py_ssize_t i = 0; i < 8; ++i) to[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
+    constexpr Py_ssize_t kCalls = sizeof fd / sizeof(void *);
+    if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != kCalls || !PyDict_Check(a[1])) raise(PyExc_TypeError, "bind");
+    for (Py_ssize_t i = 0; i < kCalls; ++i) to[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
     if (PyErr_Occurred()) throw Raised{};
     Py_XSETREF(workspaces, Py_NewRef(a[1]));
     Py_XSETREF(opts_for, Py_NewRef(a[2]));
@@ -444,7 +578,9 @@ PyMethodDef entry(const char *name) {
 PyMethodDef methods[] = {entry<17, decode>("decode_fp4"), entry<14, append>("append_fp4"), entry<14, read>("read_fp4"),
                          entry<9, reserve>("pages_reserve"), entry<9, fork>("pages_fork"),
                          entry<8, release>("pages_free"), entry<6, compact>("pages_compact"),
-                         entry<6, copy>("pages_copy"), entry<5, bind>("bind"), {nullptr, nullptr, 0, nullptr}};
+                         entry<6, copy>("pages_copy"), entry<7, reorder>("pages_reorder"), entry<16, append_rows>("append"),
+                         entry<15, prefill>("prefill"), entry<8, beam>("beam_select"), entry<5, bind>("bind"),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_fd_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

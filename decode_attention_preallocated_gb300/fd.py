@@ -1,5 +1,6 @@
 """Python binding of libfd.so (the C ABI in include/fd.h): ctypes, and for the
-4-bit cache and page calls the extension in csrc/fd_torch.cpp.
+4-bit cache and page calls, append, prefill and the beam selection the extension
+in csrc/fd_torch.cpp.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels inside libfd.so.  PyTorch supplies device memory and the current
@@ -10,11 +11,13 @@ Low-level names mirror the C ABI (``fd_decode``, ``fd_decode_int8``,
 ``fd_decode_append``, ``fd_decode_paged``, ``fd_decode_masked``,
 ``fd_decode_gather``, ``fd_decode_gather_int8``, ``fd_decode_gather_bias``,
 ``fd_topk_blocks``, ``fd_decode_fp4``, ``fd_append_fp4``, ``fd_read_fp4``,
-``fd_pages_reserve`` / ``_fork`` / ``_free`` / ``_compact`` / ``_copy``,
+``fd_append``, ``fd_prefill``, ``fd_beam_select``,
+``fd_pages_reserve`` / ``_fork`` / ``_reorder`` / ``_free`` / ``_compact`` / ``_copy``,
 ``fd_workspace_create`` ...) and take ``FdTensor`` / ``FdOpts`` structures;
 ``decode``, ``decode_int8``, ``decode_append``, ``decode_paged``,
 ``decode_masked``, ``decode_gather``, ``topk_blocks``, ``decode_fp4``,
-``append_fp4``, ``read_fp4``, ``pages_reserve``, ``pages_fork``,
+``append_fp4``, ``read_fp4``, ``append``, ``prefill``, ``beam_select``,
+``pages_reserve``, ``pages_fork``, ``pages_reorder``,
 ``pages_free``, ``pages_compact`` and ``pages_copy`` take
 torch tensors, allocate ``out`` with torch when it is not given, and keep one
 workspace per (device, stream).
@@ -106,8 +109,9 @@ _SIGNATURES = [
     ("fd_decode_noalloc", ctypes.c_int,
      [_P(FdTensor), _P(FdTensor), _P(FdTensor), ctypes.c_void_p, ctypes.c_int32,
       ctypes.c_int32, ctypes.c_float, _P(FdTensor), ctypes.c_void_p, ctypes.c_int32]),
-    # the 4-bit cache and the page calls are called through the marshalling
-    # extension; here they take descriptors as bytes or any pointer
+    # the 4-bit cache and the page calls, append, prefill and the beam selection
+    # are called through the marshalling extension; here they take descriptors
+    # as bytes or any pointer
     ("fd_decode_fp4", ctypes.c_int,
      [ctypes.c_void_p] * 5 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_int32,
                               ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
@@ -118,7 +122,22 @@ _SIGNATURES = [
     ("fd_read_fp4", ctypes.c_int,
      [ctypes.c_void_p] * 4 + [ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_int32]
      + [ctypes.c_void_p] * 5),
+    ("fd_append", ctypes.c_int,
+     [ctypes.c_void_p] * 6 + [ctypes.c_int32] + [ctypes.c_void_p] * 5 + [ctypes.c_int32]
+     + [ctypes.c_void_p] * 3),
+    ("fd_prefill_scratch_bytes", ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    ("fd_prefill", ctypes.c_int,
+     [ctypes.c_void_p] * 6 + [ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                              ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
+    ("fd_beam_scratch_bytes", ctypes.c_size_t,
+     [ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32]),
+    ("fd_beam_select", ctypes.c_int,
+     [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32]
+     + [ctypes.c_void_p] * 4),
     ("fd_pages_scratch_bytes", ctypes.c_size_t, [ctypes.c_int64]),
+    ("fd_pages_reorder", ctypes.c_int,
+     [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+      ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
     ("fd_pages_reserve", ctypes.c_int,
      [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
       ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
@@ -616,7 +635,7 @@ def decode_gather(q, k_cache, v_cache, idx, scale=None, out=None,
     return out
 
 
-# ------------------------------------------- 4-bit caches and their pages
+# ------- calls through the extension: 4-bit caches, pages, prompts and beams
 _TENSOR = struct.Struct("Pii4q4q")     # fd_tensor
 _OPTS = struct.Struct("PPiifi2i")      # fd_opts
 _PAD = ((), (0, 0, 0), (0, 0), (0,), ())
@@ -674,7 +693,8 @@ class _Unloaded:
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fd_torch", loader))
         loader.exec_module(m)
         calls = ("fd_decode_fp4", "fd_append_fp4", "fd_read_fp4", "fd_pages_reserve", "fd_pages_fork",
-                 "fd_pages_free", "fd_pages_compact", "fd_pages_copy")
+                 "fd_pages_free", "fd_pages_compact", "fd_pages_copy", "fd_pages_reorder", "fd_append",
+                 "fd_prefill", "fd_prefill_scratch_bytes", "fd_beam_select", "fd_beam_scratch_bytes")
         m.bind(tuple(ctypes.cast(getattr(lib(), c), ctypes.c_void_p).value for c in calls),
                _ws_cache, _opts_for, _empty, FdError)
         return m
@@ -721,6 +741,48 @@ def read_fp4(k_cache, v_cache, k_scale, v_scale, kv_lengths, n, start=None, k_gl
                             v_global, block_table, out, out_dtype, stream, workspace)
 
 
+def append(k_new, v_new, k_cache, v_cache, kv_lengths, new_lengths=None, lengths_out=None, q=None,
+           q_out=None, rope=None, interleaved=False, k_scale=None, v_scale=None, block_table=None,
+           stream=None, workspace: Optional[Workspace] = None):
+    """Writes new rows k_new / v_new [B, n, Hkv, d] (bf16) into a bf16 or int8
+    cache [B, Hkv, cap, d] (int8: with fp32 scales [B, Hkv, cap]), or pools of
+    pages with block_table as in ``decode_paged``, at positions kv_lengths[b] ..
+    kv_lengths[b] + new_lengths[b] - 1 (int32 [B]; None: n for every sequence;
+    rows past it are padding).  rope (fp32 [positions, r]: r/2 cosines, then r/2
+    sines of each position's angles) turns the first r values of the keys, and of
+    q [B, n, Hq, d] where given, to their positions: pairs (j, j + r/2), or
+    interleaved (2j, 2j + 1).  lengths_out (int32 [B], may be kv_lengths) receives
+    the lengths with the new rows.  Returns q_out (made when not given, may be q
+    itself; padding rows are left as they were), or None without q."""
+    return _native.append(k_new, v_new, k_cache, v_cache, kv_lengths, new_lengths, lengths_out, q, q_out,
+                          rope, interleaved, k_scale, v_scale, block_table, stream, workspace)
+
+
+def prefill(q, k_cache, v_cache, kv_lengths, new_lengths=None, causal=True, scale=None, k_scale=None,
+            v_scale=None, block_table=None, out=None, num_ctas=0, kernel=FD_KERNEL_AUTO, stream=None,
+            workspace: Optional[Workspace] = None):
+    """Attention of a chunk of new tokens q [B, n, Hq, d] over a bf16 or int8
+    cache (as in ``append``) that holds them already: the newest new_lengths[b]
+    (int32 [B]; None: n) of sequence b's kv_lengths[b] positions are its rows.
+    Row i sees positions 0 .. kv_lengths[b] - new_lengths[b] + i when causal, else
+    all of them.  Returns out [B, n, Hq, d] (bf16); rows past new_lengths[b] keep
+    what out held."""
+    return _native.prefill(q, k_cache, v_cache, kv_lengths, new_lengths, causal, scale, k_scale, v_scale,
+                           block_table, out, num_ctas, kernel, stream, workspace)
+
+
+def beam_select(logits, scores, n_out, finished=None, end_token=None, out=None, stream=None,
+                workspace: Optional[Workspace] = None):
+    """The n_out best continuations of each request of a beam search: logits
+    [B, K, V] (bf16 or fp32) of its K beams, whose log-probabilities so far are
+    scores (fp32 [B, K]; -inf: no beam).  A beam whose entry in finished (int32
+    [B, K]) is not 0 goes on by end_token alone, at no cost.  Returns (or fills
+    out =) scores fp32, rows b*K + k of the winners' beams (for
+    ``pages_reorder``) and tokens, int32, [B, n_out] each, best first; -inf, -1,
+    -1 where too few are left."""
+    return _native.beam_select(logits, scores, n_out, finished, end_token, out, stream, workspace)
+
+
 def pages_reserve(block_table, kv_lengths, refs, page_size, n_new, pairs=None, count=None,
                   stream=None, workspace: Optional[Workspace] = None):
     """Pages of its own for each sequence's next n_new positions (an int for
@@ -739,6 +801,13 @@ def pages_fork(block_table, kv_lengths, refs, page_size, src, dst, lengths=None,
     row src[i] (int32 [n]), the first lengths[i] positions of them where
     lengths is given; kv_lengths[dst[i]] follows."""
     _native.pages_fork(block_table, kv_lengths, refs, page_size, src, dst, lengths, stream, workspace)
+
+
+def pages_reorder(block_table, kv_lengths, refs, page_size, src, stream=None,
+                  workspace: Optional[Workspace] = None):
+    """Every row b of the block table takes the pages of row src[b] (int32 [B]),
+    and its length, all at once; a negative src[b] empties the row."""
+    _native.pages_reorder(block_table, kv_lengths, refs, page_size, src, stream, workspace)
 
 
 def pages_free(block_table, kv_lengths, refs, page_size, seqs=None, lengths=None, stream=None,

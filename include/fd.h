@@ -29,7 +29,12 @@
  *   - fd_decode_fp4: the dense prefix over a cache held in 4 bits, flat or
  *     paged; fd_append_fp4 writes such a cache and fd_read_fp4 reads rows of
  *     it back.
+ *   - fd_append writes new rows into a bf16 or int8 cache, flat or paged, and
+ *     rotates keys and queries to their positions; fd_prefill attends a chunk
+ *     of many new tokens over such a cache.
  *   - fd_pages_*: who holds which page of a paged cache, and copies of pages.
+ *   - fd_beam_select: the best continuations of a beam search, whose rows of
+ *     the block table fd_pages_reorder then puts in place.
  * The prefix is split across thread blocks and the last block to finish a
  * (sequence, kv head) combines the splits inside the same launch
  * (comfy-kitchen #239, "GQA decode"); the query heads of one GQA group share
@@ -468,6 +473,119 @@ int fd_read_fp4(const fd_tensor *k_cache, const fd_tensor *v_cache, const fd_ten
                 const fd_opts *opts);
 
 /*
+ * Rows of a bf16 or int8 cache.  These arguments are the same in fd_append and
+ * fd_prefill:
+ *   k_cache, v_cache: [B, Hkv, cap, d], or with a block_table pools
+ *     [num_pages, Hkv, page_size, d]; both bf16 or both int8 and of one shape;
+ *     16-byte aligned base, strides that are multiples of 16 bytes, innermost
+ *     stride 1.
+ *   k_scale, v_scale: NULL for bf16; for int8 fp32 [B, Hkv, cap] or
+ *     [num_pages, Hkv, page_size], any strides: one scale a row, as in
+ *     fd_decode_int8 and fd_decode_paged.
+ *   block_table: NULL for flat caches, else device int32 [B, max_pages],
+ *     contiguous, as in fd_decode_paged; max_pages is 0 for flat caches.
+ *   d is 128 or 256; cap (max_pages * page_size) below 2^31.
+ *
+ * fd_append writes new rows.  For sequence b with base_b = kv_lengths[b]
+ * (clamped to [0, cap]), row i of k_new / v_new [B, n, Hkv, d] (bf16; 16-byte
+ * aligned base and strides, innermost stride 1) goes to position base_b + i,
+ * for i below new_lengths[b] (device int32[B], clamped to [0, n]; NULL: n).
+ * Rows past that are padding and are not read; positions at or past cap are
+ * not written.
+ *   rope: NULL, or fp32 [positions, r], 16-byte aligned base and row stride,
+ *     innermost stride 1, r a multiple of 16 up to d: the first r/2 numbers of
+ *     row p are the cosines of position p's angles, the others their sines.
+ *     The first r values of a key are then turned in pairs (a, b) ->
+ *     (a cos - b sin, b cos + a sin), where pair j is values j and j + r/2, or
+ *     with interleaved != 0 values 2j and 2j+1; the rest stay.  fp32, each
+ *     product rounded, then their sum, then once to bf16.  A position past the
+ *     table sets FD_DEV_BAD_INDEX, and its row is neither written nor turned.
+ *   q, q_out: NULL, or the queries of the same tokens [B, n, Hq, d] (bf16,
+ *     aligned as k_new) and where they go, turned the same way (copied without
+ *     rope).  q_out may be q itself (then of the same strides), but may
+ *     overlap q, k_new or v_new in no other way.  Padding rows of q_out are left as
+ *     they were.
+ *   int8: s = max|x| / 127 over the d values of a row in fp32, code =
+ *     x / s rounded to nearest even (both quotients correctly rounded), at
+ *     most 127 in magnitude; s = 0 gives zero codes.  Where a value is a NaN
+ *     or an infinity the scale is NaN and the codes are 0.
+ *   lengths_out: device int32[B], gets min(base_b + new_b, cap); may be
+ *     kv_lengths itself (but overlap it in no other way), or NULL.
+ * FD_DEV_BAD_LENGTH is set where a length, a new length or base_b + new_b is
+ * out of range, FD_DEV_BAD_INDEX where a page's table entry names no page (its
+ * rows are not written).  A page must not be reached through two sequences'
+ * write ranges (fd_pages_reserve sees to that).  opts supplies the stream and
+ * the workspace; opts->kernel must be FD_KERNEL_AUTO, and opts->num_ctas is not
+ * used.
+ */
+int fd_append(const fd_tensor *k_new, const fd_tensor *v_new, const int32_t *new_lengths,
+              const fd_tensor *q, const fd_tensor *q_out, const fd_tensor *rope,
+              int32_t interleaved, const fd_tensor *k_cache, const fd_tensor *v_cache,
+              const fd_tensor *k_scale, const fd_tensor *v_scale, const int32_t *block_table,
+              int32_t max_pages, const int32_t *kv_lengths, int32_t *lengths_out,
+              const fd_opts *opts);
+/*
+ * Attention of a chunk of new tokens over a bf16 or int8 cache that holds
+ * them already (fd_append, then this).  q [B, n, Hq, d] (bf16, 16-byte aligned
+ * base and strides, innermost stride 1); sequence b has L_b = kv_lengths[b]
+ * positions (clamped to [0, cap]), the newest new_b of which are its query
+ * rows: new_b = new_lengths[b] (device int32[B], clamped to [0, n]; NULL: n).
+ * Row i < new_b sees positions 0 .. L_b - 1, with causal != 0 positions 0 ..
+ * L_b - new_b + i; a row that sees none gives zeros.  Rows past new_b are
+ * padding: they are not used, and out keeps what it held there.
+ *   out [B, n, Hq, d] bf16, 16-byte aligned base and strides, innermost
+ *     stride 1; overlaps nothing else.
+ *   n >= 1, Hq / Hkv up to 128; any number of rows.
+ *   Scores and sums are fp32; a softmax weight (for int8 times its position's v
+ *     scale) is rounded to bf16, i.e. by up to 2^-9 of itself.  Positions below
+ *     L_b must hold finite values where some row does not see them; those at
+ *     or past L_b and pages past it are never read.
+ * FD_DEV_BAD_LENGTH is set where a length or new length is out of range;
+ * FD_DEV_BAD_INDEX where the entry of a page below L_b names none, whose
+ * positions nobody sees.
+ *   opts->kernel: FD_KERNEL_AUTO, FD_KERNEL_TC (the tcgen05 kernel: flat
+ *     caches, and pools whose three outer strides are multiples of the
+ *     smallest, itself at least d, and the same for K and V; else
+ *     FD_ERR_UNSUPPORTED) or FD_KERNEL_SIMT (warp-level matrix instructions,
+ *     every layout).  opts->num_ctas: 0, or the number of thread blocks that
+ *     share the work of the tcgen05 kernel.
+ * Long contexts of few rows are split over thread blocks, which takes
+ * fd_prefill_scratch_bytes(num_ctas, d) bytes of the workspace's room for split
+ * partials (num_ctas 0: of an automatic launch on the current device; see
+ * fd_pages_scratch_bytes' room below).
+ */
+size_t fd_prefill_scratch_bytes(int32_t num_ctas, int32_t head_dim);
+int fd_prefill(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_cache,
+               const fd_tensor *k_scale, const fd_tensor *v_scale, const int32_t *block_table,
+               int32_t max_pages, const int32_t *kv_lengths, const int32_t *new_lengths,
+               int32_t causal, float scale, const fd_tensor *out, const fd_opts *opts);
+
+/*
+ * One step of a beam search: the n_out best of a request's K beams times V
+ * words.  logits [B, K, V] (bf16 or fp32, innermost stride 1), scores fp32
+ * [B, K] (contiguous; the beams' sums of log-probabilities so far; -inf: no
+ * beam).  With lse = log sum exp of a beam's logits, rounded to fp32, word v of
+ * beam k scores scores[b,k] + (logit - lse), compared exactly; higher scores
+ * win, equal ones go to the lower beam, then the lower word.
+ *   finished: NULL, or device int32 [B, K]: a beam whose entry is not 0 has
+ *     ended, and goes on only by the word end_token (0 .. V-1; not used
+ *     without finished), at a log-probability of 0; its logits are not used.
+ *   scores_out (fp32), beams_out, tokens_out (int32), [B, n_out] each: the
+ *     winners by falling score; beams_out holds the row b*K + k of the winner's
+ *     beam, as fd_pages_reorder's src takes it.  Candidates of -inf or NaN
+ *     score are none; where too few are left, the rest are -inf, -1 and -1.
+ *     They overlap none of the inputs.
+ *   K <= 128, n_out <= 64, V < 2^24 (FD_ERR_UNSUPPORTED beyond).
+ * opts supplies the stream and the workspace, whose room for split partials
+ * holds fd_beam_scratch_bytes(B, K, V, n_out) bytes; opts->kernel must be
+ * FD_KERNEL_AUTO, and opts->num_ctas is not used.
+ */
+size_t fd_beam_scratch_bytes(int64_t B, int32_t K, int64_t V, int32_t n_out);
+int fd_beam_select(const fd_tensor *logits, const float *scores, const int32_t *finished,
+                   int32_t end_token, int32_t n_out, float *scores_out, int32_t *beams_out,
+                   int32_t *tokens_out, const fd_opts *opts);
+
+/*
  * Pages of a paged cache, shared between sequences by reference counts.  The
  * books are caller-owned device memory:
  *   block_table int32 [B, max_pages], contiguous; -1 where a row holds no
@@ -498,6 +616,12 @@ int fd_read_fp4(const fd_tensor *k_cache, const fd_tensor *v_cache, const fd_ten
  *   lengths[i] where that is given and smaller; kv_lengths[dst[i]] = L.  An
  *   entry whose dst is an earlier entry's dst, or another entry's src, is
  *   skipped and flagged as above; src[i] = dst[i] changes nothing.
+ * fd_pages_reorder: every row b of the block table takes, all at once, the
+ *   pages that hold the first L positions of the row that was src[b] (int32
+ *   [B]), L that row's length, and kv_lengths[b] = L; a row that is its own
+ *   source stays as it is, and a negative src[b] empties the row.  A source
+ *   past the last row leaves row b as it is and is flagged as above.  B up to
+ *   49152 (FD_ERR_UNSUPPORTED beyond).
  * fd_pages_free: for each i < n, the length of sequence seqs[i] (seqs NULL:
  *   sequence i, n = B) becomes 0, or lengths[i] where lengths is given and
  *   smaller than the length, and the row's pages past it are released.
@@ -527,6 +651,9 @@ int fd_pages_reserve(int32_t *block_table, int32_t B, int32_t max_pages,
 int fd_pages_fork(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *kv_lengths,
                   int32_t page_size, int32_t *refs, int32_t num_pages, const int32_t *src,
                   const int32_t *dst, const int32_t *lengths, int32_t n, const fd_opts *opts);
+int fd_pages_reorder(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *kv_lengths,
+                     int32_t page_size, int32_t *refs, int32_t num_pages, const int32_t *src,
+                     const fd_opts *opts);
 int fd_pages_free(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *kv_lengths,
                   int32_t page_size, int32_t *refs, int32_t num_pages, const int32_t *seqs,
                   const int32_t *lengths, int32_t n, const fd_opts *opts);

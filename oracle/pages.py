@@ -57,6 +57,28 @@ class Books:
             self.table[d, :self._pages(L)] = rows[s, :self._pages(L)]
             self.lengths[d] = L
 
+    def reorder(self, src):
+        B = len(self.table)
+        rows, lens, P = self.table.copy(), [self._len(b) for b in range(B)], len(self.refs)
+        taken = []
+        for b in range(B):
+            s = int(src[b])
+            if s == b or s >= B:
+                taken.append((list(rows[b]), int(self.lengths[b])))
+                continue
+            L = lens[s] if s >= 0 else 0
+            held = [int(e) if 0 <= e < P else -1 for e in rows[max(s, 0), :self._pages(L)]]
+            taken.append((held + [-1] * (rows.shape[1] - len(held)), L))
+        for b, (row, L) in enumerate(taken):
+            for old, new in zip(rows[b], row):
+                if old != new:
+                    if 0 <= old < P:
+                        self.refs[old] -= 1
+                    if 0 <= new < P:
+                        self.refs[new] += 1
+            self.table[b] = row
+            self.lengths[b] = L
+
     def reserve(self, n_new):
         """Returns the pairs (old, new) to copy, or minus the missing pages."""
         B = len(self.table)
