@@ -323,12 +323,12 @@ int fd_pages_fork(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *k
 int fd_pages_reorder(int32_t *block_table, int32_t B, int32_t max_pages, int32_t *kv_lengths,
                      int32_t page_size, int32_t *refs, int32_t num_pages, const int32_t *src,
                      const fd_opts *opts) {
+    if (!src) return FD_ERR_ARG;
+    if (B > fd::kReorderRows) return FD_ERR_UNSUPPORTED;
     fd::Books k;
     const int rc = check_books(&k, block_table, B, max_pages, kv_lengths, page_size, refs,
                                num_pages, opts);
     if (rc) return rc;
-    if (!src) return FD_ERR_ARG;
-    if (B > fd::kReorderRows) return FD_ERR_UNSUPPORTED;
     return status_of(fd::launch_pages_reorder(k, src, opts->ws->status + 34,
                                               static_cast<cudaStream_t>(opts->stream)));
 }

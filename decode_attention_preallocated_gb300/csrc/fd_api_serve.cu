@@ -11,6 +11,7 @@
 
 #include "fd.h"
 #include "fd_api.h"
+#include "fd_prefill.h"
 #include "fd_serve.h"
 
 namespace {
@@ -159,8 +160,9 @@ int fd_append(const fd_tensor *k_new, const fd_tensor *v_new, const int32_t *new
 }
 
 size_t fd_prefill_scratch_bytes(int32_t num_ctas, int32_t head_dim) {
-    (void)num_ctas; (void)head_dim;
-    return 0;
+    if (num_ctas < 0 || num_ctas > 65535 || (head_dim != 128 && head_dim != 256)) return 0;
+    if (num_ctas == 0) num_ctas = fd::sm_count_current();
+    return (size_t)num_ctas * 2 * (size_t)fd::prefill_slot_floats(head_dim) * 4;
 }
 
 int fd_prefill(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_cache,
@@ -188,8 +190,18 @@ int fd_prefill(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_
     p.lengths = kv_lengths; p.new_lengths = new_lengths;
     p.status = opts->ws->status; p.partials = opts->ws->partials;
     p.wait_ns = opts->wait_limit_us > 0 ? (uint64_t)opts->wait_limit_us * 1000u : fd::kDefaultWaitNs;
+    const cudaStream_t st = static_cast<cudaStream_t>(opts->stream);
+    if (opts->kernel != FD_KERNEL_SIMT && fd::prefill_tc_supports(p)) {
+        int32_t G = opts->num_ctas < 65535 ? opts->num_ctas : 65535;
+        if (G == 0) G = fd::sm_count_current();
+        if (G <= 0) return FD_ERR_CUDA;
+        if (fd_prefill_scratch_bytes(G, p.c.d) > opts->ws->partial_floats * 4) return FD_ERR_WORKSPACE;
+        const std::lock_guard<std::mutex> turn(opts->ws->turn);
+        rc = fd::launch_prefill_tc(p, G, st);
+        if (rc != -2) return status_of(rc);
+    }
     if (opts->kernel == FD_KERNEL_TC) return FD_ERR_UNSUPPORTED;
-    return status_of(fd::launch_prefill_simple(p, static_cast<cudaStream_t>(opts->stream)));
+    return status_of(fd::launch_prefill_simple(p, st));
 }
 
 size_t fd_beam_scratch_bytes(int64_t B, int32_t K, int64_t V, int32_t n_out) {

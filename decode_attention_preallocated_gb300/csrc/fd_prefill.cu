@@ -10,7 +10,7 @@
 
 #include "fd_device.cuh"
 #include "fd_ptx.cuh"
-#include "fd_serve.h"
+#include "fd_prefill.h"
 
 namespace fd {
 

@@ -1,0 +1,980 @@
+// fd_prefill_tc.cu -- attention of a chunk of new tokens over a cache on the
+// tensor cores (tcgen05, TMEM accumulators, TMA loads).
+//
+// Rows.  The query heads of a kv head share its K and V, so a tile holds T =
+// 128 / g tokens of all g heads: row r is token r / g, head r % g.  A segment is
+// one tile, or two where a chunk has more rows than one holds (head_dim 128):
+// each position's K and V then serve 256 rows.
+//
+// Work.  Segments (sequence, kv head, tiles) follow one another in units of
+// positions: a charge for its start and end, then the positions that its last
+// row sees.  The grid's blocks, one an SM, take equal consecutive shares of the
+// units, and in each segment the blocks of 128 positions that start in their
+// share.  A segment that is cut leaves partial sums in the workspace, which a
+// second launch joins in the order of the pieces.
+//
+// Roles in a block:
+//   warp 8   TMA producer: Q of a segment, then K and V tiles of 128 positions
+//            in halves of 128 dimensions, into a ring of shared-memory slots.
+//   warp 9   MMA issuer (one thread): S = Q K^T (128 x 128) into TMEM, O += P V
+//            with P from TMEM.
+//   (warps 10, 11 are idle.)
+//   warps 0-7  softmax: a thread owns a row (two tiles: of its group's tile) or
+//            half the columns of one (one tile, S then double buffered).  P
+//            overwrites S in TMEM in bf16.  A row's reference is its running
+//            maximum, refreshed, and O rescaled, only where a score passes it
+//            by 2^8.
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "fd_api.h"
+#include "fd_device.cuh"
+#include "fd_prefill.h"
+#include "fd_ptx.cuh"
+#include "fd_tensor_map.h"
+
+namespace fd {
+
+namespace {
+
+constexpr int TT = 128;
+// Three warpgroups: softmax takes registers that the third gives up.
+constexpr int kThreads = 384, kSoftmaxRegs = 200, kOtherRegs = 104;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kDevTimeout = 4;          // mirrors FD_DEV_INTERNAL
+constexpr uint64_t kDrainNs = 2000000000ull;
+constexpr float kSlack = 8.f;           // log2: how far a score may pass the reference
+constexpr unsigned kAll = 0xffffffffu;
+
+struct PfArgs {
+    CUtensorMap tq, tk, tv;   // tk, tv: boxes of prow rows (flat: 128)
+    CUtensorMap gk, gv;       // paged: single rows, gathered four at a time
+    PrefillParams p;
+    int32_t T, R;             // tokens and rows a tile
+    int32_t prow;             // rows a box; 0: every tile is gathered
+    int64_t gs[3];            // pool row of (page, kv head, row) in gk, gv
+    float *slots;             // partial sums, two a block
+};
+
+struct Bars {
+    uint64_t slot_full[8], slot_empty[8];
+    uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
+    uint64_t cross, pv_done, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+template <int D, bool TWO>
+struct Cfg {
+    static_assert(!TWO || D == 128, "two tiles' O and S fill TMEM at head_dim 128");
+    static constexpr int NH = D / 128, QT = TWO ? 2 : 1;
+    static constexpr uint32_t BOX = TT * 128;        // 128 rows x 64 numbers
+    static constexpr uint32_t SLOT = 2 * BOX;        // 128 rows x 128 numbers
+    static constexpr uint32_t QTILE = NH * SLOT;
+    static constexpr uint32_t OFF_RED = 512;         // [2][2][128] floats
+    static constexpr uint32_t OFF_BAD = OFF_RED + 2048;   // [8][8] words
+    static constexpr uint32_t OFF_Q = (OFF_BAD + 256 + 1023) / 1024 * 1024;
+    static constexpr uint32_t BUDGET = 232448;
+    static constexpr int NS = (int)((BUDGET - OFF_Q - QT * QTILE) / SLOT);
+    static_assert(NS >= 4 && NS <= 8, "ring");
+    static constexpr uint32_t OFF_SLOTS = OFF_Q + QT * QTILE;
+    static constexpr uint32_t SMEM = OFF_SLOTS + NS * SLOT;
+    static constexpr int NC = TWO ? 128 : 64;        // score columns a softmax thread
+    static constexpr int OC = TWO ? D : D / 2;       // output columns a softmax thread
+    static constexpr uint32_t TMEM_O = 256;          // S: columns 0 .. 255
+    static constexpr int ROWS = QT * TT;             // rows a partial slot
+    static constexpr int64_t SLOT_FLOATS = (int64_t)ROWS * (D + 2);
+    static constexpr uint32_t IDESC_QK = ptx::idesc_bf16(128, 128, 0, 0);
+    static constexpr uint32_t IDESC_PV = ptx::idesc_bf16(128, 128, 0, 1);
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// ------------------------------------------------------------------ work
+// Positions that a segment's start and end are charged as.
+constexpr int64_t kCharge = 256;
+
+struct Seq {
+    int64_t L, fresh, base;
+    int nq;                  // segments a kv head
+};
+
+__device__ __forceinline__ Seq seq_of(const PrefillParams &p, int b, int S, bool flag = false) {
+    const int64_t raw = __ldg(p.lengths + b), L = clamp_len(raw, p.c.cap);
+    const int64_t want = p.new_lengths ? __ldg(p.new_lengths + b) : p.n, fresh = clamp_len(want, p.n);
+    if (flag && (raw != L || want != fresh)) atomicOr(p.status, kDevBadLength);
+    return Seq{L, fresh, L - fresh, (int)((fresh + S - 1) / S)};
+}
+
+// Units of the first q segments of a kv head.
+__device__ __forceinline__ int64_t units_of(const PrefillParams &p, const Seq &s, int S, int64_t q) {
+    if (!p.causal) return q * (kCharge + s.L);
+    return q * (kCharge + (s.base > 0 ? s.base : 0)) + S * (q * (q + 1) / 2);
+}
+
+// A block's walk over the segments of its share.
+struct Walk {
+    int S;                   // tokens a segment
+    int64_t total;
+    int G;                   // blocks that share the units
+    int64_t u0, u1;          // this block's
+    int64_t a, cost;         // first unit and units of the current segment
+    Seq s;
+    int b, hk, q;
+
+    // Every lane of a warp; `c`: the block.  False where it has no work.
+    __device__ __forceinline__ bool find(const PrefillParams &p, int tokens, int c, int grid, bool flag) {
+        S = tokens;
+        const int lane = threadIdx.x & 31;
+        int64_t sum = 0;
+        for (int i = lane; i < p.B; i += 32) {
+            const Seq x = seq_of(p, i, S, flag);
+            sum += units_of(p, x, S, x.nq);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+        total = sum * p.c.Hkv;
+        const int64_t most = total / TT;
+        G = (int)(most < 1 ? 1 : most < grid ? most : grid);
+        if (c >= G || total == 0) return false;
+        u0 = split().start(c);
+        u1 = split().start(c + 1);
+        return seek(p, u0);
+    }
+    __device__ __forceinline__ Split split() const { return Split{total, G}; }
+    // The segment that holds unit u.
+    __device__ __forceinline__ bool seek(const PrefillParams &p, int64_t u) {
+        const int lane = threadIdx.x & 31;
+        int64_t before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int i = b0 + lane;
+            int64_t mine = 0;
+            if (i < p.B) {
+                const Seq x = seq_of(p, i, S);
+                mine = units_of(p, x, S, x.nq) * p.c.Hkv;
+            }
+            int64_t upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(kAll, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const unsigned in = __ballot_sync(kAll, before + upto > u);
+            if (in) {
+                const int at = __ffs(in) - 1;
+                const int64_t first = before + __shfl_sync(kAll, upto - mine, at);
+                b = b0 + at;
+                s = seq_of(p, b, S);
+                const int64_t head = units_of(p, s, S, s.nq);
+                hk = (int)((u - first) / head);
+                const int64_t x = u - first - hk * head;
+                if (p.causal) {
+                    // S/2 q^2 + k q = x
+                    const float k = (float)(kCharge + (s.base > 0 ? s.base : 0)) + 0.5f * S;
+                    q = (int)((sqrtf(k * k + 2.f * S * (float)x) - k) / S);
+                } else {
+                    q = (int)(x / (kCharge + s.L));
+                }
+                q = max(0, min(q, s.nq - 1));
+                while (q > 0 && units_of(p, s, S, q) > x) --q;
+                while (q + 1 < s.nq && units_of(p, s, S, q + 1) <= x) ++q;
+                a = first + hk * head + units_of(p, s, S, q);
+                cost = units_of(p, s, S, q + 1) - units_of(p, s, S, q);
+                return true;
+            }
+            before += __shfl_sync(kAll, upto, 31);
+        }
+        return false;
+    }
+    __device__ __forceinline__ bool next(const PrefillParams &p) {
+        a += cost;
+        if (a >= u1) return false;
+        if (++q == s.nq) {
+            q = 0;
+            if (++hk == p.c.Hkv) {
+                hk = 0;
+                do {
+                    if (++b >= p.B) return false;
+                    s = seq_of(p, b, S);
+                } while (s.nq == 0);
+            }
+        }
+        cost = units_of(p, s, S, q + 1) - units_of(p, s, S, q);
+        return true;
+    }
+    // Positions that the first `tokens` of this segment see.
+    __device__ __forceinline__ int64_t seen(const PrefillParams &p, int tokens) const {
+        if (!p.causal) return s.L;
+        const int64_t last = min(s.fresh, (int64_t)q * S + tokens);
+        return clamp_len(s.base + last, s.L);
+    }
+    __device__ __forceinline__ int blocks(const PrefillParams &p) const { return (int)((seen(p, S) + TT - 1) / TT); }
+    __device__ __forceinline__ int64_t block_unit(int j) const { return a + kCharge + (int64_t)j * TT; }
+};
+
+// The blocks of positions of the current segment that are this block's, and of
+// them those that each tile sees.
+struct Piece {
+    int j0, j1, all;         // of `all`
+    int hi[2];               // tile t works on j0 .. hi[t] - 1
+    __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == all; }
+};
+
+template <int QT>
+__device__ __forceinline__ Piece piece_of(const PfArgs &a, const Walk &w) {
+    const PrefillParams &p = a.p;
+    Piece x;
+    x.all = w.blocks(p);
+    const int64_t from = w.u0 - w.a - kCharge, to = w.u1 - w.a - kCharge;
+    x.j0 = from <= 0 ? 0 : (int)min((int64_t)x.all, (from + TT - 1) / TT);
+    x.j1 = to <= 0 ? 0 : (int)min((int64_t)x.all, (to + TT - 1) / TT);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        x.hi[t] = x.j0;
+        if (t < QT && (int64_t)w.q * w.S + t * a.T < w.s.fresh) {
+            const int n = (int)((w.seen(p, (t + 1) * a.T) + TT - 1) / TT);
+            x.hi[t] = max(x.j0, min(x.j1, n));
+        }
+    }
+    return x;
+}
+
+// ----------------------------------------------------------------- helpers
+__device__ __forceinline__ bool wait_on(Bars *bs, const PrefillParams &p, uint64_t *bar, uint32_t parity, int site) {
+    if (ptx::mbar_wait(bar, parity & 1, &bs->abort_flag, p.wait_ns)) return true;
+    // (the first wait that gave up is recorded, as in the decode kernel)
+    if (!*reinterpret_cast<volatile int *>(&bs->abort_flag) && atomicCAS(p.status + 1, 0, site) == 0) p.status[2] = (int)parity;
+    *reinterpret_cast<volatile int *>(&bs->abort_flag) = 1;
+    atomicOr(p.status, kDevTimeout);
+    return false;
+}
+
+// Waits for a block's own copies or MMAs, which must end even when another role
+// gave up.
+__device__ __forceinline__ void drain_on(uint64_t *bar, uint32_t parity) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity); ++n)
+        if ((n & 63) == 0 && ptx::globaltimer_ns() - t0 > kDrainNs) return;
+}
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void store32(void *dst, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// Row `row` of tile t of the current segment: its token, where it is stored.
+__device__ __forceinline__ bool row_at(const PfArgs &a, const Walk &w, int t, int row, int64_t &token, int64_t &off) {
+    const PrefillParams &p = a.p;
+    token = (int64_t)w.q * w.S + (int64_t)t * a.T + row / p.g;
+    off = w.b * p.os[0] + token * p.os[1] + ((int64_t)w.hk * p.g + row % p.g) * p.os[2];
+    return row < a.R && token < w.s.fresh;
+}
+
+// ------------------------------------------------------------------ kernel
+template <int D, bool TWO>
+__global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_constant__ PfArgs a) {
+    using C = Cfg<D, TWO>;
+    const PrefillParams &p = a.p;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t base = ptx::smem_u32(smem);
+    Bars *bs = reinterpret_cast<Bars *>(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (base & 1023u) {   // the swizzled layouts want aligned buffers
+        if (tid == 0) atomicOr(p.status, kDevTimeout);
+        return;
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        ptx::prefetch_tmap(&a.tq);
+        ptx::prefetch_tmap(&a.tk);
+        ptx::prefetch_tmap(&a.tv);
+        for (int i = 0; i < C::NS; ++i) {
+            ptx::mbar_init(&bs->slot_full[i], 1);
+            ptx::mbar_init(&bs->slot_empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&bs->q_full[t], 1);
+            ptx::mbar_init(&bs->q_free[t], 1);
+            ptx::mbar_init(&bs->s_full[t], 1);
+            ptx::mbar_init(&bs->p_full[t], TWO ? 128 : 256);
+            ptx::mbar_init(&bs->o_full[t], 1);
+        }
+        ptx::mbar_init(&bs->cross, 256);
+        ptx::mbar_init(&bs->pv_done, 1);
+        ptx::mbar_init(&bs->drain, 1);
+        bs->abort_flag = 0;
+        ptx::mbar_fence_init();
+    }
+    if (warp == kMmaWarp) {
+        ptx::tmem_alloc(&bs->tmem_base, 512);
+        ptx::tmem_relinquish();
+    }
+    Walk w;
+    const bool has = w.find(p, C::QT * a.T, blockIdx.x, gridDim.x, warp == kProducerWarp && blockIdx.x == 0);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = bs->tmem_base;
+
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kProducerWarp) {
+        // ------------------------------------------------------- producer
+        uint32_t fills = 0, loads[2] = {0, 0}, seen = 0;   // seen: blocks of positions
+        bool ok = true;
+        // rows of a block of positions: a box's page and first row, or the
+        // pool's rows of positions 4 lane .. 4 lane + 3
+        struct Rows {
+            int y[4];
+        };
+        const bool paged = p.c.block_table != nullptr;
+        for (bool more = has; more && ok; more = w.next(p)) {
+            const Piece x = piece_of<C::QT>(a, w);
+            if (x.j0 >= x.j1) continue;
+#pragma unroll
+            for (int t = 0; t < C::QT; ++t) {
+                if (x.hi[t] <= x.j0 || !ok) continue;
+                if (lane == 0) {
+                    if (loads[t] > 0) ok = wait_on(bs, p, &bs->q_free[t], loads[t] - 1, 1);
+                    if (ok) {
+                        ++loads[t];
+                        ptx::mbar_arrive_expect_tx(&bs->q_full[t], (uint32_t)(a.R * 128 * (D / 64)));
+                        for (int cb = 0; cb < D / 64; ++cb)
+                            ptx::tma_load_4d(smem + C::OFF_Q + t * C::QTILE + cb * C::BOX, &a.tq, &bs->q_full[t], cb * 64,
+                                             w.hk * p.g, w.q * w.S + t * a.T, w.b);
+                    }
+                }
+                ok = __shfl_sync(kAll, ok, 0);
+            }
+            const auto tiled = [&](int j) { return !paged || (a.prow > 0 && (int64_t)(j + 1) * TT <= w.s.L); };
+            const auto look = [&](int j) {
+                Rows r{{-1, -1, -1, -1}};
+                if (!paged || j >= x.j1) return r;
+                const int32_t *table = p.c.block_table + (int64_t)w.b * p.c.max_pages;
+                const bool box = tiled(j);
+                const int n = box ? (lane < TT / a.prow ? 1 : 0) : 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t pos = (int64_t)j * TT + (box ? lane * a.prow : 4 * lane + e);
+                    if (e < n && pos < w.s.L) {
+                        const int32_t at = (int32_t)pos;
+                        const int32_t i = p.c.page_shift >= 0 ? at >> p.c.page_shift : at / p.c.page_size;
+                        const int32_t page = __ldg(table + i), row = at - i * p.c.page_size;
+                        const bool good = page >= 0 && page < p.c.lead;
+                        if (box) {
+                            r.y[0] = good ? page : -1;
+                            r.y[1] = row;
+                        } else {
+                            r.y[e] = good ? (int)(page * a.gs[0] + w.hk * a.gs[1] + row * a.gs[2]) : -1;
+                        }
+                    }
+                }
+                return r;
+            };
+            // one half of K or V of block j
+            const auto fill = [&](int j, int h, bool v, const Rows &r) {
+                const uint32_t slot = fills % C::NS, use = fills / C::NS;
+                if (lane == 0) {
+                    ok = wait_on(bs, p, &bs->slot_empty[slot], use + 1, 2);
+                    if (ok) ptx::mbar_arrive_expect_tx(&bs->slot_full[slot], C::SLOT);
+                }
+                ok = __shfl_sync(kAll, ok, 0);
+                if (!ok) return;
+                ++fills;
+                unsigned char *dst = smem + C::OFF_SLOTS + slot * C::SLOT;
+                if (!paged) {
+                    const int64_t y = min((int64_t)j * TT, w.s.L - TT);   // the last tile ends at the length
+                    if (lane < 2)
+                        ptx::tma_load_4d(dst + lane * C::BOX, v ? &a.tv : &a.tk, &bs->slot_full[slot], h * 128 + lane * 64,
+                                         (int)y, w.hk, w.b);
+                } else if (tiled(j)) {
+                    if (lane < TT / a.prow)
+#pragma unroll
+                        for (int cb = 0; cb < 2; ++cb)
+                            ptx::tma_load_4d(dst + cb * C::BOX + lane * a.prow * 128, v ? &a.tv : &a.tk, &bs->slot_full[slot],
+                                             h * 128 + cb * 64, r.y[1], w.hk, r.y[0]);
+                } else {
+#pragma unroll
+                    for (int cb = 0; cb < 2; ++cb)
+                        ptx::tma_gather4(dst + cb * C::BOX + 4 * lane * 128, v ? &a.gv : &a.gk, &bs->slot_full[slot],
+                                         h * 128 + cb * 64, r.y[0], r.y[1], r.y[2], r.y[3]);
+                }
+            };
+            // which of the block's positions lie on a page that the table does
+            // not name, for the softmax
+            const auto mark = [&](int j, const Rows &r) {
+                if (!paged) return;
+                uint32_t *ring = reinterpret_cast<uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
+                uint32_t bad = 0;   // of positions 4 lane .. 4 lane + 3
+                if (tiled(j)) {
+                    const unsigned runs = __ballot_sync(kAll, lane < TT / a.prow && r.y[0] < 0);
+                    if (runs)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) bad |= ((runs >> ((4 * lane + e) / a.prow)) & 1u) << e;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((int64_t)j * TT + 4 * lane + e < w.s.L && r.y[e] < 0) bad |= 1u << e;
+                }
+                const bool any = __any_sync(kAll, bad != 0);
+                if (any) {
+                    if (bad) atomicOr(p.status, kDevBadIndex);
+                    uint32_t word = bad << (4 * (lane & 7));
+#pragma unroll
+                    for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(kAll, word, o);
+                    if ((lane & 7) == 0) ring[1 + lane / 8] = word;
+                }
+                __syncwarp();
+                if (lane == 0) ring[0] = any;
+                __syncwarp();
+            };
+            Rows now = look(x.j0), after = look(x.j0 + 1);
+            mark(x.j0, now);
+#pragma unroll
+            for (int h = 0; h < C::NH; ++h)
+                if (ok) fill(x.j0, h, false, now);
+            for (int j = x.j0; j < x.j1 && ok; ++j) {
+                const Rows then = look(j + 2);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    // (two tiles: V(j) is wanted before K(j + 1))
+                    const bool v = TWO ? k == 0 : k == 1;
+                    if (!v && j + 1 >= x.j1) continue;
+                    if (!v) mark(j + 1, after);
+#pragma unroll
+                    for (int h = 0; h < C::NH; ++h)
+                        if (ok) fill(v ? j : j + 1, h, v, v ? now : after);
+                }
+                now = after;
+                after = then;
+            }
+            seen += x.j1 - x.j0;
+        }
+        // every copy that was issued lands before the block exits
+        if (lane == 0)
+            for (uint32_t i = fills > C::NS ? fills - C::NS : 0; i < fills; ++i)
+                drain_on(&bs->slot_full[i % C::NS], (i / C::NS) & 1);
+        if (lane == 0)
+            for (int t = 0; t < C::QT; ++t)
+                if (loads[t] > 0) drain_on(&bs->q_full[t], (loads[t] - 1) & 1);
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------- issuer
+        // (two tiles: PV of one tile and its next scores follow the other's, so
+        // that one tile's softmax runs under the other's products; one tile: the
+        // next scores are issued before PV)
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t used = 0;               // slots consumed
+            uint32_t pieces[2] = {0, 0}, ctr[2] = {0, 0};
+            const auto slot_at = [&](uint32_t i) { return base + C::OFF_SLOTS + (i % C::NS) * C::SLOT; };
+            const auto wait_slot = [&](uint32_t i) {
+                ok = ok && wait_on(bs, p, &bs->slot_full[i % C::NS], i / C::NS, 3);
+            };
+            // S[buf] (+)= Q_t K^T over one half of the dimensions
+            const auto qk = [&](int t, uint32_t buf, uint32_t i, int h) {
+                const uint32_t q = base + C::OFF_Q + t * C::QTILE + h * C::SLOT, k = slot_at(i);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    ptx::mma_f16_ss(tmem + buf * 128,
+                                    ptx::smem_desc(q + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024, ptx::kLayoutSwizzle128),
+                                    ptx::smem_desc(k + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024, ptx::kLayoutSwizzle128),
+                                    C::IDESC_QK, h > 0 || kk > 0);
+            };
+            // O_t's dimensions of half h += P[buf] V
+            const auto pv = [&](int t, uint32_t buf, uint32_t i, int h, bool first) {
+                const uint32_t v = slot_at(i);
+#pragma unroll
+                for (int kt = 0; kt < 8; ++kt)
+                    ptx::mma_f16_ts(tmem + C::TMEM_O + t * 128 + h * 128, tmem + buf * 128 + kt * 8,
+                                    ptx::smem_desc(v + kt * 2048, C::BOX, 1024, ptx::kLayoutSwizzle128), C::IDESC_PV,
+                                    !(first && kt == 0));
+            };
+            const auto free_slot = [&](uint32_t i) { ptx::mma_commit(&bs->slot_empty[i % C::NS]); };
+            for (bool more = has; more && ok; more = w.next(p)) {
+                const Piece x = piece_of<C::QT>(a, w);
+                if (x.j0 >= x.j1) continue;
+                for (int t = 0; t < C::QT; ++t)
+                    if (x.hi[t] > x.j0) ok = ok && wait_on(bs, p, &bs->q_full[t], pieces[t]++, 4);
+                if (!ok) break;
+                if (TWO) {
+                    uint32_t k = used++;     // the slot of K(j)
+                    wait_slot(k);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    for (int t = 0; t < 2; ++t)
+                        if (x.j0 < x.hi[t]) {
+                            qk(t, t, k, 0);
+                            ptx::mma_commit(&bs->s_full[t]);
+                            if (x.j0 + 1 == x.hi[t]) ptx::mma_commit(&bs->q_free[t]);
+                        }
+                    free_slot(k);
+                    for (int j = x.j0; j < x.j1 && ok; ++j) {
+                        const bool ahead = j + 1 < x.j1;
+                        const uint32_t v = used++;
+                        if (ahead) k = used++;
+                        const bool second = j < x.hi[1];
+                        wait_slot(v);
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (j >= x.hi[t]) continue;
+                            ok = ok && wait_on(bs, p, &bs->p_full[t], ctr[t]++, 5);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            pv(t, t, v, 0, j == x.j0);
+                            if (t == 1 || !second) free_slot(v);
+                            if (j + 1 == x.hi[t]) ptx::mma_commit(&bs->o_full[t]);
+                            if (j + 1 < x.hi[t]) {
+                                wait_slot(k);
+                                if (!ok) break;
+                                ptx::tc_fence_after();
+                                qk(t, t, k, 0);
+                                ptx::mma_commit(&bs->s_full[t]);
+                                if (j + 2 == x.hi[t]) ptx::mma_commit(&bs->q_free[t]);
+                            }
+                        }
+                        if (!ok) break;
+                        if (ahead) free_slot(k);
+                    }
+                } else {
+                    const auto scores = [&](int j) {
+                        const uint32_t n = ctr[1]++;
+#pragma unroll
+                        for (int h = 0; h < C::NH; ++h) {
+                            const uint32_t k = used++;
+                            wait_slot(k);
+                            if (!ok) return;
+                            ptx::tc_fence_after();
+                            qk(0, n & 1, k, h);
+                            free_slot(k);
+                        }
+                        ptx::mma_commit(&bs->s_full[n & 1]);
+                        if (j + 1 == x.j1) ptx::mma_commit(&bs->q_free[0]);
+                    };
+                    scores(x.j0);
+                    for (int j = x.j0; j < x.j1 && ok; ++j) {
+                        if (j + 1 < x.j1) scores(j + 1);
+                        if (!ok) break;
+                        const uint32_t n = ctr[0]++;
+                        ok = wait_on(bs, p, &bs->p_full[n & 1], n >> 1, 5);
+#pragma unroll
+                        for (int h = 0; h < C::NH && ok; ++h) {
+                            const uint32_t v = used++;
+                            wait_slot(v);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                            pv(0, n & 1, v, h, j == x.j0);
+                            free_slot(v);
+                        }
+                        if (ok) ptx::mma_commit(&bs->pv_done);
+                        if (ok && j + 1 == x.j1) ptx::mma_commit(&bs->o_full[0]);
+                    }
+                }
+            }
+            // every MMA that was issued ends before the block exits
+            ptx::mma_commit(&bs->drain);
+            drain_on(&bs->drain, 0);
+        }
+    }
+    } else {
+        // --------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int group = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int t = TWO ? group : 0;                  // tile
+        const int col0 = TWO ? 0 : group * 64;          // first score column
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // TMEM lane of the warp, << 16
+        const uint32_t o_at = tmem + lanes + C::TMEM_O + (TWO ? t * 128 : group * C::OC);
+        float *red = reinterpret_cast<float *>(smem + C::OFF_RED);
+        uint32_t ctr = 0, pieces = 0, crossed = 0, seen = 0;
+        bool ok = true;
+        // one tile: this thread's number against that of the row's other half
+        const auto other = [&](float mine) {
+            float *room = red + (crossed & 1) * 256;
+            room[group * 128 + row] = mine;
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(&bs->cross);
+            ok = ok && wait_on(bs, p, &bs->cross, crossed, 6);
+            ptx::tc_fence_after();
+            ++crossed;
+            return room[(group ^ 1) * 128 + row];
+        };
+        const float sc = p.scale_log2;
+        for (bool more = has; more && ok; more = w.next(p)) {
+            const Piece x = piece_of<C::QT>(a, w);
+            int64_t token, off;
+            const bool real = row_at(a, w, t, row, token, off);
+            if (x.all == 0) {
+                // nobody sees anything: the block of the segment's first unit
+                if (w.a >= w.u0 && real) {
+                    const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    for (int c = 0; c < C::OC; c += 8)
+                        *reinterpret_cast<uint4 *>(p.out + off + (TWO ? 0 : group * C::OC) + c) =
+                            make_uint4(zero[0], zero[1], zero[2], zero[3]);
+                }
+                continue;
+            }
+            if (x.j0 >= x.j1) continue;
+            const int n = x.hi[t] - x.j0;
+            const int64_t first = (int64_t)w.q * w.S + (int64_t)t * a.T;     // the tile's first token
+            const int last = (int)(p.causal ? min(w.s.base + token, w.s.L - 1) : w.s.L - 1);
+            const int64_t all_see = p.causal ? min(w.s.base + first, w.s.L - 1) : w.s.L - 1;
+            float m = neg_inf(), l = 0.f;
+            uint64_t sum0 = 0, sum1 = 0;
+            for (int j = x.j0; j < x.hi[t] && ok; ++j) {
+                const uint32_t buf = TWO ? t : ctr & 1, use = TWO ? ctr : ctr >> 1;
+                ++ctr;
+                const uint32_t s_at = tmem + lanes + buf * 128;
+                ok = wait_on(bs, p, &bs->s_full[buf], use, 7);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const int pos0 = j * TT;
+                const uint32_t *bad = reinterpret_cast<const uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
+                const bool holes = p.c.block_table && *reinterpret_cast<const volatile uint32_t *>(bad);
+                const bool masked = holes || (int64_t)pos0 + TT - 1 > all_see;
+                const int at = p.c.block_table ? pos0 : (int)min((int64_t)pos0, w.s.L - TT);   // position of column 0
+                const int lo = pos0 - at - col0, hi = last - at - col0;   // columns that the row sees
+                // 32 score columns from c on, hidden ones as -inf
+                const auto hide = [&](float *s, int c) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c + e < lo || c + e > hi) s[e] = neg_inf();
+                    if (holes) {
+                        const uint32_t word = bad[1 + (col0 + c) / 32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if ((word >> e) & 1u) s[e] = neg_inf();
+                    }
+                };
+                const auto most = [&](const float *s, float top) {
+                    float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
+#pragma unroll
+                    for (int e = 4; e < 32; e += 4) {
+                        t0 = fmaxf(t0, fmaxf(s[e], s[e + 1]));
+                        t1 = fmaxf(t1, fmaxf(s[e + 2], s[e + 3]));
+                    }
+                    return fmaxf(top, fmaxf(t0, t1));
+                };
+                // the row's maximum; columns 0 .. 63 stay in registers, 64 .. 127
+                // are read again below
+                float s[64], h[32];
+                float top = neg_inf();
+#pragma unroll
+                for (int c = 64; c < C::NC; c += 32) {
+                    ptx::tmem_ld32(s_at + c, c == 64 ? s : s + 32);
+                    if (c == 96) {
+                        ptx::tmem_wait_ld();
+                        if (masked) {
+                            hide(s, 64);
+                            hide(s + 32, 96);
+                        }
+                        top = most(s, most(s + 32, top));
+                    }
+                }
+                ptx::tmem_ld32(s_at + col0, s);
+                ptx::tmem_ld32(s_at + col0 + 32, s + 32);
+                ptx::tmem_wait_ld();
+                if (masked) {
+                    hide(s, 0);
+                    hide(s + 32, 32);
+                }
+                top = most(s, most(s + 32, top));
+                if (!TWO) top = fmaxf(top, other(top));
+                if (!ok) break;
+                // a new reference where a score passes the old one by 2^8
+                // (rows that are nobody's hold what was left in shared memory)
+                const bool raise = real && ((top - m) * sc > kSlack || m == neg_inf());
+                if (__any_sync(kAll, raise)) {
+                    float f = 1.f;
+                    if (raise) {
+                        f = m == neg_inf() ? 0.f : fast_exp2((m - top) * sc);
+                        m = top;
+                        const float2 u = unpair(sum0), v = unpair(sum1);
+                        sum0 = pair(u.x * f, u.y * f);
+                        sum1 = pair(v.x * f, v.y * f);
+                    }
+                    if (j > x.j0) {
+                        // two tiles: the last PV into O was issued before these
+                        // scores, whose end was waited for; one tile: after
+                        if (!TWO) {
+                            ok = wait_on(bs, p, &bs->pv_done, ctr - 2, 9);
+                            if (!ok) break;
+                            ptx::tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int c = 0; c < C::OC; c += 32) {
+                            ptx::tmem_ld32(o_at + c, h);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) h[e] *= f;
+                            ptx::tmem_st16(o_at + c, h);
+                            ptx::tmem_st16(o_at + c + 16, h + 16);
+                        }
+                    }
+                }
+                const float ref = m == neg_inf() ? 0.f : -m * sc;
+                const uint64_t sc2 = pair(sc, sc), ref2 = pair(ref, ref);
+                // the weights of 32 columns from c on, into P
+                const auto weigh = [&](const float *s, int c) {
+                    uint32_t word[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float2 u = unpair(fma2(pair(s[e], s[e + 1]), sc2, ref2));
+                        const float2 v = unpair(fma2(pair(s[e + 2], s[e + 3]), sc2, ref2));
+                        const float p0 = fast_exp2(u.x), p1 = fast_exp2(u.y), p2 = fast_exp2(v.x), p3 = fast_exp2(v.y);
+                        sum0 = add2(sum0, pair(p0, p1));
+                        sum1 = add2(sum1, pair(p2, p3));
+                        word[e / 2] = pack_bf16x2(p0, p1);
+                        word[e / 2 + 1] = pack_bf16x2(p2, p3);
+                    }
+                    ptx::tmem_st16(s_at + (col0 + c) / 2, word);
+                };
+                weigh(s, 0);
+                if (C::NC == 128) ptx::tmem_ld32(s_at + 64, h);
+                weigh(s + 32, 32);
+                if (C::NC == 128) {
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_ld32(s_at + 96, s);
+                    if (masked) hide(h, 64);
+                    weigh(h, 64);
+                    ptx::tmem_wait_ld();
+                    if (masked) hide(s, 96);
+                    weigh(s, 96);
+                }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bs->p_full[buf]);
+            }
+            if (!ok) break;
+            seen += x.j1 - x.j0;
+            {
+                const float2 u = unpair(sum0), v = unpair(sum1);
+                l = (u.x + u.y) + (v.x + v.y);
+            }
+            if (!TWO) l += other(l);
+            if (!ok) break;
+            if (n > 0) {
+                ok = wait_on(bs, p, &bs->o_full[t], pieces++, 8);
+                if (!ok) break;
+                ptx::tc_fence_after();
+            }
+            const int c0 = TWO ? 0 : group * C::OC;
+            if (x.whole()) {
+                const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+                const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.os[0] * 2) | (uintptr_t)(p.os[1] * 2) |
+                                    (uintptr_t)(p.os[2] * 2)) & 31) == 0;
+#pragma unroll 1
+                for (int c = 0; c < C::OC; c += 32) {
+                    float o[32];
+                    uint32_t word[16];
+                    if (n > 0) {
+                        ptx::tmem_ld32(o_at + c, o);
+                        ptx::tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        word[e] = n > 0 && inv != 0.f ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+                    if (real) {
+                        uint16_t *dst = p.out + off + c0 + c;
+                        if (wide) {
+                            store32(dst, word);
+                            store32(dst + 16, word + 8);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(word[e], word[e + 1], word[e + 2], word[e + 3]);
+                        }
+                    }
+                }
+            } else {
+                float *slot = a.slots + (2 * (int64_t)blockIdx.x + (x.j0 > 0 ? 0 : 1)) * C::SLOT_FLOATS;
+                const int r = t * TT + row;
+                if (TWO || group == 0) {
+                    slot[C::ROWS * D + r] = n > 0 && m != neg_inf() ? m * sc : neg_inf();
+                    slot[C::ROWS * (D + 1) + r] = l;
+                }
+                if (n > 0) {
+                    float *dst = slot + (int64_t)r * D + c0;
+#pragma unroll 1
+                    for (int c = 0; c < C::OC; c += 32) {
+                        float o[32];
+                        ptx::tmem_ld32(o_at + c, o);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) store32(dst + c + e, reinterpret_cast<const uint32_t *>(o + e));
+                    }
+                }
+            }
+            // (the next segment's PV overwrites O once this group's P is there)
+            ptx::tc_fence_before();
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------- join
+// One block for each place between two blocks' shares: if it cuts a segment's
+// blocks of positions, this place's part of the segment's rows is joined from
+// the pieces, in order.
+template <int D, bool TWO>
+__global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PfArgs a, int grid) {
+    using C = Cfg<D, TWO>;
+    const PrefillParams &p = a.p;
+    const int c = blockIdx.x + 1;
+    Walk w;
+    if (!w.find(p, C::QT * a.T, c, grid, false)) return;
+    const int all = w.blocks(p);
+    if (all == 0) return;
+    const Split sp = w.split();
+    const int first = sp.owner(w.block_unit(0)), last = sp.owner(w.block_unit(all - 1));
+    if (c <= first || c > last) return;
+    const int places = last - first, at = c - first - 1;
+    const int r0 = C::ROWS * at / places, r1 = C::ROWS * (at + 1) / places;
+    constexpr int PER = D / 8;
+    for (int e = r0 * PER + (int)threadIdx.x; e < r1 * PER; e += 256) {
+        const int r = e / PER, d = (e % PER) * 8;
+        int64_t token, off;
+        if (!row_at(a, w, r / TT, r % TT, token, off)) continue;
+        const auto slot = [&](int k) { return a.slots + (2 * (int64_t)k + (k == first ? 1 : 0)) * C::SLOT_FLOATS; };
+        float top = neg_inf();
+        for (int k = first; k <= last; ++k) top = fmaxf(top, slot(k)[C::ROWS * D + r]);
+        float l = 0.f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (top > neg_inf()) {
+            for (int k = first; k <= last; ++k) {
+                const float *s = slot(k), m = s[C::ROWS * D + r];
+                if (m == neg_inf()) continue;       // this piece saw nothing and holds no O
+                const float f = fast_exp2(m - top);
+                const float4 u = *reinterpret_cast<const float4 *>(s + (int64_t)r * D + d);
+                const float4 v = *reinterpret_cast<const float4 *>(s + (int64_t)r * D + d + 4);
+                const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+                l = fmaf(f, s[C::ROWS * (D + 1) + r], l);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = fmaf(f, y[i], o[i]);
+            }
+        }
+        const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+        *reinterpret_cast<uint4 *>(p.out + off + d) =
+            make_uint4(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv),
+                       pack_bf16x2(o[4] * inv, o[5] * inv), pack_bf16x2(o[6] * inv, o[7] * inv));
+    }
+}
+
+// ------------------------------------------------------------- host side
+bool encode(CUtensorMap *m, cuuint32_t rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    const EncodeTiledFn fn = encode_fn();
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The pool's rows as one strided 2-D array: the smallest stride, rows, and the
+// three strides in rows.
+bool pool_rows(const KvCache &c, int64_t *rs, int64_t *rows, int64_t g[3]) {
+    int64_t r = c.ks[0];
+    for (int i = 0; i < 3; ++i) {
+        if (c.vs[i] != c.ks[i]) return false;
+        r = c.ks[i] < r ? c.ks[i] : r;
+    }
+    if (r < c.d) return false;
+    for (int i = 0; i < 3; ++i) {
+        if (c.ks[i] % r) return false;
+        g[i] = c.ks[i] / r;
+    }
+    *rs = r;
+    *rows = (c.lead - 1) * g[0] + (int64_t)(c.Hkv - 1) * g[1] + (int64_t)(c.page_size - 1) * g[2] + 1;
+    return *rows < (int64_t)1 << 31;
+}
+
+// Rows of a box: a tile is runs of this many rows that each lie on one page;
+// 0 where there is no such number (every tile is then gathered).
+int box_rows(const KvCache &c) {
+    if (!c.block_table || c.page_size % TT == 0) return TT;
+    return c.page_size >= 8 && c.page_size < TT && TT % c.page_size == 0 ? c.page_size : 0;
+}
+
+template <int D, bool TWO>
+int launch(const PfArgs &a, int grid, cudaStream_t st) {
+    using C = Cfg<D, TWO>;
+    if (cudaFuncSetAttribute(prefill_tc_kernel<D, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
+        return -5;
+    prefill_tc_kernel<D, TWO><<<grid, kThreads, C::SMEM, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return -5;
+    if (grid > 1) prefill_join_kernel<D, TWO><<<grid - 1, 256, 0, st>>>(a, grid);
+    return cudaGetLastError() == cudaSuccess ? 0 : -5;
+}
+
+}  // namespace
+
+// Two tiles hold 256 rows' partial sums at head_dim 128, one 128 at 256.
+int64_t prefill_slot_floats(int d) { return d == 128 ? Cfg<128, true>::SLOT_FLOATS : Cfg<256, false>::SLOT_FLOATS; }
+
+bool prefill_tc_supports(const PrefillParams &p) {
+    int64_t rs, rows, g[3];
+    return !p.c.int8 && p.scale_log2 > 0.f && (!p.c.block_table || pool_rows(p.c, &rs, &rows, g));
+}
+
+int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
+    PfArgs a;
+    memset(&a, 0, sizeof a);
+    a.p = p;
+    a.T = TT / p.g;
+    a.R = a.T * p.g;
+    a.prow = box_rows(p.c);
+    a.slots = p.partials;
+    {
+        const cuuint64_t dims[4] = {(cuuint64_t)p.c.d, (cuuint64_t)p.Hq, (cuuint64_t)p.n, (cuuint64_t)p.B};
+        const cuuint64_t strides[3] = {(cuuint64_t)p.qs[2] * 2, (cuuint64_t)p.qs[1] * 2, (cuuint64_t)p.qs[0] * 2};
+        const cuuint32_t box[4] = {64, (cuuint32_t)p.g, (cuuint32_t)a.T, 1};
+        if (!encode(&a.tq, 4, p.q, dims, strides, box)) return -2;
+    }
+    const void *caches[2] = {p.c.k, p.c.v};
+    const int64_t *strides_of[2] = {p.c.ks, p.c.vs};
+    for (int i = 0; i < 2; ++i) {
+        const int64_t *s = strides_of[i];
+        if (a.prow > 0) {
+            const int64_t rows = p.c.block_table ? p.c.page_size : p.c.cap;
+            const cuuint64_t dims[4] = {(cuuint64_t)p.c.d, (cuuint64_t)rows, (cuuint64_t)p.c.Hkv, (cuuint64_t)p.c.lead};
+            const cuuint64_t strides[3] = {(cuuint64_t)s[2] * 2, (cuuint64_t)s[1] * 2, (cuuint64_t)s[0] * 2};
+            const cuuint32_t box[4] = {64, (cuuint32_t)a.prow, 1, 1};
+            if (!encode(i ? &a.tv : &a.tk, 4, caches[i], dims, strides, box)) return -2;
+        }
+        int64_t rs, rows;
+        if (p.c.block_table) {
+            if (!pool_rows(p.c, &rs, &rows, a.gs)) return -2;
+            const cuuint64_t dims[2] = {(cuuint64_t)p.c.d, (cuuint64_t)rows};
+            const cuuint64_t strides[1] = {(cuuint64_t)rs * 2};
+            const cuuint32_t box[2] = {64, 1};
+            if (!encode(i ? &a.gv : &a.gk, 2, caches[i], dims, strides, box)) return -2;
+        }
+    }
+    if (a.prow == 0) { a.tk = a.gk; a.tv = a.gv; }   // (unused)
+    if (p.c.d == 256) return launch<256, false>(a, grid, st);
+    if ((int64_t)p.n > a.T) return launch<128, true>(a, grid, st);
+    return launch<128, false>(a, grid, st);
+}
+
+}  // namespace fd

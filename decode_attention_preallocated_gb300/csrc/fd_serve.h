@@ -36,7 +36,7 @@ struct RowsParams {
 };
 int launch_append_rows(const RowsParams &p, cudaStream_t st);
 
-// fd_prefill*.cu
+// fd_prefill.cu, fd_prefill_tc.cu (launchers: fd_prefill.h)
 struct PrefillParams {
     KvCache c;
     int32_t B, n, Hq, g, causal;
@@ -48,7 +48,6 @@ struct PrefillParams {
     float *partials;
     uint64_t wait_ns;
 };
-int launch_prefill_simple(const PrefillParams &p, cudaStream_t st);
 
 // fd_beam.cu
 struct BeamParams {
