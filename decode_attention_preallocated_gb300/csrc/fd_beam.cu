@@ -7,14 +7,18 @@
 // of exponentials and its n_out best words (logit, lowest word first), and the
 // last block of a request joins the slices of all its beams.
 //
-// The best n of many: each of W warps finds the ceil(n / W)-th largest of its
-// lanes' maxima; at least n numbers lie at or above the least of these, and
-// few more do, so they are collected in shared memory and ranked by counting.
-// More than the list holds (logits with many equal maxima) go by n rounds of
-// one maximum each.
+// The best n of many: at least n of the threads' largest lie at or above a bound
+// that warp maxima give (bound_of), and few more numbers do.  A block streams its
+// slice, each thread 32 bytes a step, keeping the maximum of each thread's step;
+// the few steps that reach the bound are read again (from L2) for the words that
+// do.  Those are ranked by counting how many are better than each.  The join
+// ranks what the slices left the same way, by scores in single precision widened
+// by what those may be off, and orders the few that remain by their exact scores.
 #include <cuda_runtime.h>
 
 #include <math.h>
+
+#include <initializer_list>
 
 #include "fd_device.cuh"
 #include "fd_serve.h"
@@ -24,7 +28,18 @@ namespace fd {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kList = 1024;        // collected candidates
+// Words a thread, and a block, looks at in one step: 32 bytes a thread.
+template <typename T>
+constexpr int kPer = 32 / (int)sizeof(T);
+template <typename T>
+constexpr int kStep = kPer<T> * kThreads;
+constexpr int kSteps = 16;         // steps of a slice at most
+constexpr int kAgain = 64;         // threads' steps read again at a time
+constexpr int kKeep = 512;         // a longer list is cut before more comes
+constexpr int kList = kKeep + kAgain * kPer<uint16_t>;
+constexpr int kFinals = 512;       // the join's list
+constexpr int kAhead = 2;          // steps whose loads are in flight
+constexpr int kBlocks = 4;         // blocks an SM holds
 constexpr unsigned kAll = 0xffffffffu;
 
 // Unsigned numbers in the order of the floats, both zeros alike; 0 for what is
@@ -38,161 +53,300 @@ __device__ __forceinline__ float float_of(uint32_t k) {
     return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-// What a slice leaves behind: then n_out keys, (order of the logit, ~word)
-// falling, 0 past the last.
+// The order of the lowest finite number.
+constexpr uint32_t kLowest = 0x00800000u;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Two fp32 numbers in one 64-bit register, and operations on both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t scaled(uint64_t a, float f) { return mul2(a, pair(f, f)); }
+
+// What a slice leaves behind: then room for 2 n_out keys (order of the logit,
+// ~word), its n_out best among them, 0 past the last.
 struct Slice {
-    float top, sum;    // of its logits: maximum, and sum of exp(x - top)
+    float top, sum;    // of its logits: maximum, and sum of exp(x - top), NaN with a NaN among them
 };
 
 __device__ __forceinline__ Slice *head_of(char *scratch, int64_t slice, int n_out) {
-    return reinterpret_cast<Slice *>(scratch + slice * (int64_t)(8 + 8 * n_out));
+    return reinterpret_cast<Slice *>(scratch + slice * (int64_t)(8 + 16 * n_out));
 }
 __device__ __forceinline__ uint64_t *keys_of(Slice *h) { return reinterpret_cast<uint64_t *>(h + 1); }
 
-// A bound that at least n of the block's numbers reach, from each thread's
-// largest: 0 where there may be fewer.
-__device__ __forceinline__ uint32_t bound_of(uint32_t mine, int n, uint32_t *warp_bounds) {
-    const int lane = threadIdx.x & 31;
-    uint32_t x = mine, b = 0;
-    for (int k = (n + kWarps - 1) / kWarps; k > 0; --k) {
-        b = __reduce_max_sync(kAll, x);
-        const uint32_t who = __ballot_sync(kAll, x == b);
-        if (lane == __ffs(who) - 1) x = 0;
+// The i-th largest of the warp's keys (1 <= i <= lanes whose key is not 0).
+__device__ __forceinline__ uint64_t warp_largest(uint64_t mine, int i) {
+    uint32_t hi = (uint32_t)(mine >> 32), lo = (uint32_t)mine, top = 0, low = 0;
+    for (; i > 0; --i) {
+        top = __reduce_max_sync(kAll, hi);
+        low = __reduce_max_sync(kAll, hi == top ? lo : 0u);
+        const uint32_t who = __ballot_sync(kAll, hi == top && lo == low);
+        if ((threadIdx.x & 31) == __ffs(who) - 1) hi = lo = 0;
     }
-    if (lane == 0) warp_bounds[threadIdx.x >> 5] = b;
+    return (uint64_t)top << 32 | low;
+}
+
+// A bound that at least n of the block's keys reach, from each thread's largest (0:
+// it has none); 0 where fewer than n threads have one.  Warps with few such
+// lanes give fewer.
+__device__ __forceinline__ uint64_t bound_of(uint64_t mine, int n, int *counts, uint64_t *bounds) {
+    const int warp = threadIdx.x >> 5, have = __popc(__ballot_sync(kAll, mine != 0));
+    int m = (n + kWarps - 1) / kWarps;
+    uint64_t b = have > 0 ? warp_largest(mine, min(have, m)) : ~0ull;
+    if ((threadIdx.x & 31) == 0) {
+        counts[warp] = have;
+        bounds[warp] = b;
+    }
     __syncthreads();
-    b = warp_bounds[0];
+    int got = 0, all = 0;
+    b = ~0ull;
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) b = min(b, warp_bounds[w]);
+    for (int w = 0; w < kWarps; ++w) {
+        got += min(counts[w], m);
+        all += counts[w];
+        b = b < bounds[w] ? b : bounds[w];
+    }
+    if (got >= n) return b;
+    if (all < n) return 0;
+    do {
+        ++m;
+        got = 0;
+        for (int w = 0; w < kWarps; ++w) got += min(counts[w], m);
+    } while (got < n);
+    b = have > 0 ? warp_largest(mine, min(have, m)) : ~0ull;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) bounds[warp] = b;
+    __syncthreads();
+    b = ~0ull;
+    for (int w = 0; w < kWarps; ++w) b = b < bounds[w] ? b : bounds[w];
     return b;
 }
 
-__device__ __forceinline__ uint64_t max64(uint64_t a, uint64_t b) { return a > b ? a : b; }
-
-__device__ __forceinline__ uint64_t block_max(uint64_t x, uint64_t *room) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = max64(x, __shfl_xor_sync(kAll, x, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = room[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) x = max64(x, room[w]);
-    return x;
-}
-
-struct __align__(8) Room {
-    uint64_t list[kList];
-    uint64_t room[kWarps];
-    uint32_t bounds[kWarps];
+struct __align__(16) Room {
+    union {
+        uint64_t list[kList];
+        struct {
+            uint64_t score[kFinals], at[kFinals];
+        } finals;
+    };
+    float lse[128];
+    float tops_of[kSteps][kThreads];   // of each thread's steps
+    uint16_t again[kSteps * kThreads];   // steps to read again: step * kThreads + thread
+    int n_again;
+    uint64_t bounds[kWarps];
+    int counts[kWarps];
     float tops[kWarps], sums[kWarps];
     int count, last;
 };
 
 struct BeamArgs {
     BeamParams p;
-    int32_t slices;
+    int32_t slices, steps;     // a row's slices, of so many steps each
 };
 
-// Values of the final ranking: the score in 64 bits and the candidate's number
-// (beam, word); better: higher, then lower number.
-struct __align__(16) Final {
-    double score;
-    uint64_t at;       // beam << 32 | word
-};
+// A number's bits in the order of the numbers (no NaN).
+__device__ __forceinline__ uint64_t order_of(double x) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x);
+    return u ^ ((u >> 63) ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double double_of(uint64_t k) {
+    return __longlong_as_double((long long)(k ^ ((k >> 63) ? 1ull << 63 : ~0ull)));
+}
+
+// Cuts the list of `count` keys (at most MINE a thread) to its n best, in order;
+// every thread.
+template <int MINE>
+__device__ __forceinline__ void cut(Room &sm, int count, int n) {
+    uint64_t key[MINE], top = 0;
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        const int at = threadIdx.x + i * kThreads;
+        key[i] = at < count ? sm.list[at] : 0;
+        top = key[i] > top ? key[i] : top;
+    }
+    if (count > kThreads / 4) {
+        // first those that can be among them
+        const uint64_t least = bound_of(top, n, sm.counts, sm.bounds);
+        if (threadIdx.x == 0) sm.count = 0;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MINE; ++i)
+            if (key[i] && key[i] >= least) sm.list[atomicAdd(&sm.count, 1)] = key[i];
+        __syncthreads();
+        count = sm.count;
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            const int at = threadIdx.x + i * kThreads;
+            key[i] = at < count ? sm.list[at] : 0;
+        }
+    }
+    int rank[MINE];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        rank[i] = 0;
+        if (i * kThreads >= count) break;
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) rank[i] += sm.list[j] > key[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        if (i * kThreads >= count) break;
+        if (key[i] && rank[i] < n) sm.list[rank[i]] = key[i];
+    }
+    if (threadIdx.x == 0) sm.count = min(count, n);
+    __syncthreads();
+}
+
+// The same for a list of any length, out of line: it is rarely long.
+__device__ __noinline__ void cut_long(Room &sm, int count, int n) {
+    cut<(kList + kThreads - 1) / kThreads>(sm, count, n);
+}
 
 // Joins the slices of request b.
-__device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm, Final *finals, float *lse) {
+__device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm) {
     const BeamParams &p = a.p;
     const int tid = threadIdx.x, K = p.K, S = a.slices, n = p.n_out;
     const int64_t first = (int64_t)b * K * S;
+    const int room = 2 * n, total = K * S * room;
+    // the first of this thread's candidates set out before the sums are joined
+    constexpr int kHeld = 8;
+    uint64_t held[kHeld];
+    const auto key_at = [&](int e) {
+        const int slice = e / room;
+        return __ldcg(keys_of(head_of(p.scratch, first + slice, n)) + (e - slice * room));
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) held[i] = tid + i * kThreads < total ? key_at(tid + i * kThreads) : 0;
     for (int k = tid >> 5; k < K; k += kWarps) {
         const int lane = tid & 31;
-        float top = neg_inf();
+        float top = neg_inf(), sum = 0.f;
         bool nan = false;
         for (int s = lane; s < S; s += 32) {
-            const float t = __ldcg(&head_of(p.scratch, first + (int64_t)k * S + s, n)->top);
-            nan |= t != t;
-            top = fmaxf(top, t);
+            const float2 h = __ldcg(reinterpret_cast<const float2 *>(head_of(p.scratch, first + (int64_t)k * S + s, n)));
+            nan |= h.y != h.y;
+            if (h.x > neg_inf()) {
+                const float now = fmaxf(top, h.x);
+                sum = sum * expf(top - now) + h.y * expf(h.x - now);
+                top = now;
+            }
         }
         nan = __any_sync(kAll, nan);
+        float most = top;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-        double sum = 0;
-        for (int s = lane; s < S; s += 32) {
-            const Slice *h = head_of(p.scratch, first + (int64_t)k * S + s, n);
-            const float t = __ldcg(&h->top);
-            if (t > neg_inf()) sum += (double)(__ldcg(&h->sum) * expf(t - top));
-        }
+        for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
+        sum = top > neg_inf() ? sum * expf(top - most) : 0.f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
         if (lane == 0) {
-            float x = (float)((double)top + log(sum));
+            // sum = 2^e f, f in [0.75, 1.5): the logarithm of f is small, and so
+            // is what it is off by; the three are added in 64 bits
+            const int e = (__float_as_int(sum) - 0x3f400000) >> 23;
+            const float f = __int_as_float(__float_as_int(sum) - (e << 23));
+            float x = (float)((double)most + ((double)e * 0.693147180559945309 + (double)logf(f)));
+            if (!(sum > 0.f && sum < INFINITY)) x = most + logf(sum);   // no word, or no number
             if (nan) x = __uint_as_float(0x7fffffffu);
             if (p.finished && p.finished[(int64_t)b * K + k]) x = 0.f;
-            lse[k] = x;
+            sm.lse[k] = x;
         }
     }
     if (tid == 0) sm.count = 0;
     __syncthreads();
-    // candidates in single precision, widened by what that may be off
-    const int total = K * S * n;
+    // f(beam, key, score in single precision, what that may be off) of this thread's
+    // candidates
     const float *scores = p.scores + (int64_t)b * K;
+    const auto one = [&](int e, uint64_t key, auto f) {
+        if (!key) return;
+        const int k = e / (room * S);
+        const float s = __ldg(scores + k), d = float_of((uint32_t)(key >> 32)) - sm.lse[k], score = s + d;
+        if (score > neg_inf()) f(k, key, score, ldexpf(fabsf(s) + fabsf(d), -22));
+    };
     const auto visit = [&](auto f) {
-        for (int e = tid; e < total; e += kThreads) {
-            const int row = e / n, k = row / S;
-            const uint64_t key = __ldcg(keys_of(head_of(p.scratch, first + row, n)) + (e - row * n));
-            if (!key) continue;
-            const float x = float_of((uint32_t)(key >> 32)), s = __ldg(scores + k), d = x - lse[k];
-            const float score = s + d;
-            if (!(score > neg_inf())) continue;
-            f(k, key, x, s, score, ldexpf(fabsf(s) + fabsf(d), -22));
-        }
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (tid + i * kThreads < total) one(tid + i * kThreads, held[i], f);
+        for (int e = tid + kHeld * kThreads; e < total; e += kThreads) one(e, key_at(e), f);
     };
     float low = neg_inf();
-    visit([&](int, uint64_t, float, float, float score, float off) { low = fmaxf(low, score - off); });
-    const uint32_t least = bound_of(order_of(low), n, sm.bounds);
-    const auto exactly = [&](int k, float x, float s) { return (double)s + ((double)x - (double)lse[k]); };
-    visit([&](int k, uint64_t key, float x, float s, float score, float off) {
+    visit([&](int, uint64_t, float score, float off) { low = fmaxf(low, score - off); });
+    const uint32_t least = (uint32_t)(bound_of((uint64_t)order_of(low) << 32, n, sm.counts, sm.bounds) >> 32);
+    const auto exactly = [&](int k, uint64_t key) {
+        return order_of((double)__ldg(scores + k) + ((double)float_of((uint32_t)(key >> 32)) - (double)sm.lse[k]));
+    };
+    visit([&](int k, uint64_t key, float score, float off) {
         if (order_of(score + off) < least) return;
         const int i = atomicAdd(&sm.count, 1);
-        if (i < kList) finals[i] = Final{exactly(k, x, s), (uint64_t)k << 32 | (uint32_t)~(uint32_t)key};
+        if (i >= kFinals) return;
+        sm.finals.score[i] = key;
+        sm.finals.at[i] = (uint64_t)k << 32 | (uint32_t)~(uint32_t)key;
     });
     __syncthreads();
     const int count = sm.count;
     const int64_t out = (int64_t)b * n;
-    const auto put = [&](int rank, const Final &f) {
-        p.scores_out[out + rank] = (float)f.score;
-        p.beams_out[out + rank] = b * K + (int)(f.at >> 32);
-        p.tokens_out[out + rank] = (int)(uint32_t)f.at;
+    const auto put = [&](int rank, uint64_t score, uint64_t at) {
+        p.scores_out[out + rank] = (float)double_of(score);
+        p.beams_out[out + rank] = b * K + (int)(at >> 32);
+        p.tokens_out[out + rank] = (int)(uint32_t)at;
     };
-    const auto better = [](const Final &x, const Final &y) { return x.score > y.score || (x.score == y.score && x.at < y.at); };
+    // higher scores, then lower numbers
+    const auto better = [](uint64_t s, uint64_t a, uint64_t t, uint64_t b) { return s > t || (s == t && a < b); };
     int found = count;
-    if (count <= kList) {
+    if (count <= kFinals) {
+        for (int i = tid; i < count; i += kThreads) sm.finals.score[i] = exactly((int)(sm.finals.at[i] >> 32), sm.finals.score[i]);
+        __syncthreads();
         for (int i = tid; i < count; i += kThreads) {
-            const Final mine = finals[i];
+            const uint64_t s = sm.finals.score[i], at = sm.finals.at[i];
             int rank = 0;
-            for (int j = 0; j < count; ++j) rank += better(finals[j], mine);
-            if (rank < n) put(rank, mine);
+#pragma unroll 8
+            for (int j = 0; j < count; ++j) {
+                const uint64_t t = sm.finals.score[j], u = sm.finals.at[j];
+                rank += (int)(t > s) | ((int)(t == s) & (int)(u < at));
+            }
+            if (rank < n) put(rank, s, at);
         }
     } else {
-        // the next best, n times
-        Final prev{INFINITY, 0};
+        // more are as good as that: the next best, n times
+        uint64_t ps = 0, pa = 0;
         for (found = 0; found < n; ++found) {
-            Final best{-INFINITY, ~0ull};
-            visit([&](int k, uint64_t key, float x, float s, float, float) {
-                const Final f{exactly(k, x, s), (uint64_t)k << 32 | (uint32_t)~(uint32_t)key};
-                if ((found == 0 || better(prev, f)) && better(f, best)) best = f;
+            uint64_t bs = 0, ba = ~0ull;
+            visit([&](int k, uint64_t key, float, float) {
+                const uint64_t t = exactly(k, key), at = (uint64_t)k << 32 | (uint32_t)~(uint32_t)key;
+                if ((found == 0 || better(ps, pa, t, at)) && better(t, at, bs, ba)) {
+                    bs = t;
+                    ba = at;
+                }
             });
             __syncthreads();
-            finals[tid] = best;
+            sm.finals.score[tid] = bs;
+            sm.finals.at[tid] = ba;
             __syncthreads();
             for (int j = 0; j < kThreads; ++j)
-                if (better(finals[j], best)) best = finals[j];
+                if (better(sm.finals.score[j], sm.finals.at[j], bs, ba)) {
+                    bs = sm.finals.score[j];
+                    ba = sm.finals.at[j];
+                }
             __syncthreads();
-            if (best.at == ~0ull) break;
-            if (tid == 0) put(found, best);
-            prev = best;
+            if (ba == ~0ull) break;
+            if (tid == 0) put(found, bs, ba);
+            ps = bs;
+            pa = ba;
         }
     }
     for (int i = found + tid; i < n; i += kThreads) {
@@ -202,13 +356,69 @@ __device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm, Final *fin
     }
 }
 
-// grid: (slices, beams of all requests).  PER words a thread; VEC: rows are read
-// 16 bytes at a time.
-template <typename T, int PER, bool VEC>
-__global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ BeamArgs a) {
+// This thread's words of one step: neighbours by wide loads, or every 256th.
+template <typename T, bool VEC>
+struct Words {
+    static constexpr int PER = kPer<T>, N = VEC ? PER * (int)sizeof(T) / 16 : 1;
+    uint4 w[N];
+    float x[VEC ? 1 : PER];
+    __device__ __forceinline__ void load(const T *src, int first, int end, int who) {
+        if (VEC) {
+            const int v = first + who * PER;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (v + PER <= end) w[i] = ldg_stream(reinterpret_cast<const uint4 *>(src + v) + i);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int v = first + e * kThreads + who;
+                x[e] = v < end ? number(src + v) : neg_inf();
+            }
+        }
+    }
+    __device__ __forceinline__ static float number(const T *at) {
+        if constexpr (sizeof(T) == 4) return __ldg(at);
+        else return __uint_as_float((uint32_t)__ldg(at) << 16);
+    }
+    // As numbers; the row's last few one by one.
+    __device__ __forceinline__ void get(const T *src, int first, int end, int who, float *to) const {
+        if (!VEC) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) to[e] = x[e];
+            return;
+        }
+        const int v = first + who * PER;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (sizeof(T) == 4) {
+                    to[i * 4 + e] = __uint_as_float(u[e]);
+                } else {
+                    to[i * 8 + 2 * e] = bf16lo(u[e]);
+                    to[i * 8 + 2 * e + 1] = bf16hi(u[e]);
+                }
+            }
+        }
+        if (v + PER > end) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) to[e] = v + e < end ? number(src + v + e) : neg_inf();
+        }
+    }
+    __device__ __forceinline__ static uint32_t word(int first, int who, int e) {
+        return VEC ? first + who * PER + e : first + e * kThreads + who;
+    }
+};
+
+// blockIdx.x: slice of a row (beam of a request).  VEC: rows are read 16 bytes at a
+// time.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_constant__ BeamArgs a) {
+    constexpr int PER = kPer<T>, STEP = kStep<T>;
     __shared__ Room sm;
-    __shared__ Final finals[kList];
-    __shared__ float lse[128];
     const BeamParams &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = p.n_out;
     const int64_t row = blockIdx.x / (unsigned)a.slices;
@@ -218,102 +428,96 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
     uint64_t *keys = keys_of(head);
     if (p.finished && __ldg(p.finished + row)) {
         if (tid == 0) *head = Slice{neg_inf(), 0.f};
-        for (int i = tid; i < n; i += kThreads)
+        for (int i = tid; i < 2 * n; i += kThreads)
             keys[i] = slice == 0 && i == 0 ? (uint64_t)order_of(0.f) << 32 | (uint32_t)~p.end_token : 0ull;
     } else {
-        constexpr int W = VEC ? 16 / (int)sizeof(T) : 1;
         const T *src = static_cast<const T *>(p.logits) + b * p.ls[0] + k * p.ls[1];
-        const int first = slice * (kThreads * PER);
-        float x[PER];
-        bool bad = false;
+        const int first = slice * a.steps * STEP;
+        const int steps = min(a.steps, (p.V - first + STEP - 1) / STEP);
+        if (tid == 0) sm.count = sm.n_again = 0;
+        Words<T, VEC> next[kAhead];
 #pragma unroll
-        for (int j = 0; j < PER / W; ++j) {
-            const int v = first + (j * kThreads + tid) * W;
-            if (VEC && v + W <= p.V) {
-                const uint4 w = ldg_stream(src + v);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < kAhead; ++i)
+            if (i < steps) next[i].load(src, first + i * STEP, p.V, tid);
+        // of this thread's words so far: maximum, and sum of exp(x - top) (two halves)
+        float top = neg_inf();
+        uint64_t sum = 0;
+        for (int i0 = 0; i0 < steps; i0 += kAhead) {
 #pragma unroll
-                for (int e = 0; e < W; ++e)
-                    x[j * W + e] = sizeof(T) == 4 ? __uint_as_float(u[e])
-                                                  : (e & 1) ? bf16hi(u[e / 2]) : bf16lo(u[e / 2]);
-            } else {
+            for (int q = 0; q < kAhead; ++q) {
+                const int i = i0 + q, at = first + i * STEP;
+                if (i >= steps) break;
+                float x[PER];
+                next[q].get(src, at, p.V, tid, x);
+                if (i + kAhead < steps) next[q].load(src, at + kAhead * STEP, p.V, tid);
+                float most = x[0];
 #pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    x[j * W + e] = neg_inf();
-                    if (v + e < p.V) {
-                        if constexpr (sizeof(T) == 4) x[j * W + e] = src[v + e];
-                        else x[j * W + e] = __uint_as_float((uint32_t)src[v + e] << 16);
-                    }
+                for (int e = 1; e < PER; ++e) most = fmaxf(most, x[e]);
+                sm.tops_of[i][tid] = most;
+                if (most > top) {
+                    if (top > neg_inf()) sum = scaled(sum, fast_exp2((top - most) * kLog2e));
+                    top = most;
+                }
+                // (the difference first: a rounded product of the reference would
+                // scale the whole sum; a NaN makes the sum one)
+                const float ref = top > neg_inf() ? -top : 0.f;
+#pragma unroll
+                for (int e = 0; e < PER; e += 2) {
+                    const float2 y = unpair(mul2(add2(pair(x[e], x[e + 1]), pair(ref, ref)), pair(kLog2e, kLog2e)));
+                    sum = add2(sum, pair(fast_exp2(y.x), fast_exp2(y.y)));
                 }
             }
         }
-        float top = neg_inf();
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            bad |= x[e] != x[e];
-            top = fmaxf(top, x[e]);
-        }
-        const uint32_t mine = order_of(top);
+        // the block's maximum and sum, and the steps that reach the bound
         float all = top;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, o));
         if (lane == 0) sm.tops[warp] = all;
-        if (tid == 0) sm.count = 0;
-        const uint32_t least = max(bound_of(mine, n, sm.bounds), 1u);
+        const uint32_t least = max(kLowest, (uint32_t)(bound_of((uint64_t)order_of(top) << 32, n, sm.counts, sm.bounds) >> 32));
+        const float edge = float_of(least);
+        if (top >= edge)
+            for (int i = 0; i < steps; ++i)
+                if (sm.tops_of[i][tid] >= edge) sm.again[atomicAdd(&sm.n_again, 1)] = (uint16_t)(i * kThreads + tid);
         all = sm.tops[0];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) all = fmaxf(all, sm.tops[w]);
-        // sum of exp(x - all), and the candidates
-        // (the difference first: a rounded product of the maximum would scale
-        // the whole sum)
-        const float base = all > neg_inf() ? all : 0.f;
-        float sum = 0.f;
+        const float2 halves = unpair(sum);
+        float mine = halves.x + halves.y;
+        if (top > neg_inf()) mine *= fast_exp2((top - all) * kLog2e);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) sum += fast_exp2((x[e] - base) * 1.4426950408889634f);
-        if (mine >= least) {
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                const uint32_t o = order_of(x[e]);
-                if (o >= least) {
-                    const int i = atomicAdd(&sm.count, 1);
-                    const uint32_t word = first + ((e / W) * kThreads + tid) * W + e % W;
-                    if (i < kList) sm.list[i] = (uint64_t)o << 32 | (uint32_t)~word;
-                }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        if (lane == 0) sm.sums[warp] = sum;
-        bad = __syncthreads_or(bad);
-        const int count = sm.count;
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(kAll, mine, o);
+        if (lane == 0) sm.sums[warp] = mine;
+        __syncthreads();
         if (tid == 0) {
-            sum = 0.f;
-            for (int w = 0; w < kWarps; ++w) sum += sm.sums[w];
-            *head = Slice{bad ? __uint_as_float(0x7fffffffu) : all, sum};
+            mine = 0.f;
+            for (int w = 0; w < kWarps; ++w) mine += sm.sums[w];
+            *head = Slice{all, mine};
         }
-        if (count <= kList) {
-            for (int i = tid; i < count; i += kThreads) {
-                const uint64_t key = sm.list[i];
-                int rank = 0;
-                for (int j = 0; j < count; ++j) rank += sm.list[j] > key;
-                if (rank < n) keys[rank] = key;
-            }
-            for (int i = count + tid; i < n; i += kThreads) keys[i] = 0;
-        } else {
-            uint64_t prev = ~0ull;
-            for (int i = 0; i < n; ++i) {
-                uint64_t best = 0;
+        for (int i0 = 0; i0 < sm.n_again; i0 += kAgain) {
+            bool over = false;
+            if (tid < kAgain && i0 + tid < sm.n_again) {
+                const int e0 = sm.again[i0 + tid], at = first + e0 / kThreads * STEP, who = e0 % kThreads;
+                float x[PER];
+                next[0].load(src, at, p.V, who);
+                next[0].get(src, at, p.V, who, x);
 #pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    const uint32_t o = order_of(x[e]);
-                    const uint32_t word = first + ((e / W) * kThreads + tid) * W + e % W;
-                    const uint64_t key = (uint64_t)o << 32 | (uint32_t)~word;
-                    if (o && key < prev) best = max64(best, key);
-                }
-                prev = block_max(best, sm.room);
-                if (tid == 0) keys[i] = prev;
+                for (int e = 0; e < PER; ++e)
+                    if (x[e] >= edge) {
+                        const int to = atomicAdd(&sm.count, 1);
+                        over |= to >= kKeep;
+                        sm.list[to] = (uint64_t)order_of(x[e]) << 32 | (uint32_t)~Words<T, VEC>::word(at, who, e);
+                    }
             }
+            if (__syncthreads_or(over)) cut_long(sm, sm.count, n);
         }
+        int count = sm.count;
+        if (count > 2 * n) {
+            __syncthreads();
+            if (count <= kThreads) cut<1>(sm, count, n);
+            else cut_long(sm, count, n);
+            count = sm.count;
+        }
+        for (int i = tid; i < 2 * n; i += kThreads) keys[i] = i < count ? sm.list[i] : 0;
     }
     // the last block of a request joins its slices
     __syncthreads();
@@ -324,37 +528,47 @@ __global__ void __launch_bounds__(kThreads) beam_kernel(const __grid_constant__ 
     }
     __syncthreads();
     if (!sm.last) return;
-    join(a, b, sm, finals, lse);
+    join(a, b, sm);
     if (tid == 0) p.tickets[b] = 0;
 }
 
-// Words a thread of the slices of a call: see launch_beam_select.
-int per_thread(int64_t rows, int64_t V) { return rows * ceil_div(V, kThreads * 32) >= 152 ? 32 : 8; }
+// Steps a slice: all rows in one round of the blocks that 152 SMs hold where that
+// gives each row eight slices, else in rounds of twice as many blocks.
+int steps_of(int64_t rows, int64_t V, int step) {
+    const int64_t steps = ceil_div(V, step), room = 152 * kBlocks;
+    const int64_t slices = rows * 8 <= room ? room / rows : ceil_div(2 * room, rows);
+    const int64_t each = ceil_div(steps, slices < steps ? slices : steps);
+    return (int)(each < kSteps ? each : kSteps);
+}
 
-template <typename T, int PER>
+template <typename T>
 void launch(const BeamArgs &a, bool vec, unsigned blocks, cudaStream_t st) {
-    if (vec) beam_kernel<T, PER, true><<<blocks, kThreads, 0, st>>>(a);
-    else beam_kernel<T, PER, false><<<blocks, kThreads, 0, st>>>(a);
+    if (vec) beam_kernel<T, true><<<blocks, kThreads, 0, st>>>(a);
+    else beam_kernel<T, false><<<blocks, kThreads, 0, st>>>(a);
 }
 
 }  // namespace
 
 int64_t beam_scratch_bytes(int64_t B, int K, int64_t V, int n_out) {
-    return B * K * ceil_div(V, kThreads * per_thread(B * K, V)) * (int64_t)(8 + 8 * n_out);
+    // (the more slices of the two types')
+    int64_t slices = 0;
+    for (const int step : {kStep<float>, kStep<uint16_t>}) {
+        const int64_t n = ceil_div(V, (int64_t)steps_of(B * K, V, step) * step);
+        slices = n > slices ? n : slices;
+    }
+    return B * K * slices * (int64_t)(8 + 16 * n_out);
 }
 
 int launch_beam_select(const BeamParams &p, cudaStream_t st) {
     const int64_t rows = (int64_t)p.B * p.K;
-    const int per = per_thread(rows, p.V);
-    BeamArgs a{p, (int32_t)ceil_div(p.V, kThreads * per)};
+    const int step = p.bf16 ? kStep<uint16_t> : kStep<float>, steps = steps_of(rows, p.V, step);
+    BeamArgs a{p, (int32_t)ceil_div(p.V, (int64_t)steps * step), steps};
     const int64_t blocks = rows * a.slices;
     if (blocks >= (int64_t)1 << 31) return -2;
     const int es = p.bf16 ? 2 : 4;
     const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.ls[0] * es % 16 == 0 && p.ls[1] * es % 16 == 0;
-    if (p.bf16 && per == 32) launch<uint16_t, 32>(a, vec, (unsigned)blocks, st);
-    else if (p.bf16) launch<uint16_t, 8>(a, vec, (unsigned)blocks, st);
-    else if (per == 32) launch<float, 32>(a, vec, (unsigned)blocks, st);
-    else launch<float, 8>(a, vec, (unsigned)blocks, st);
+    if (p.bf16) launch<uint16_t>(a, vec, (unsigned)blocks, st);
+    else launch<float>(a, vec, (unsigned)blocks, st);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 

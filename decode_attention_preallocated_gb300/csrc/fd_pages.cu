@@ -32,7 +32,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 1024;
-constexpr int kReorderThreads = 512;
+constexpr int kReorderThreads = 256, kReorderShift = 3;   // 8 columns a block
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr unsigned kAll = 0xffffffffu;
@@ -128,18 +128,20 @@ __global__ void fork_kernel(const Books k, const int32_t *src, const int32_t *ds
 // Rows change places only within a column, so a block takes some columns of
 // every row into shared memory and writes them back in their new places; the
 // lengths, which every block reads, are written by the last one to finish.
-__global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const Books k, const int32_t *src, int cols,
+__global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const Books k, const int32_t *src, int shift,
                                                                   int32_t *ticket) {
     extern __shared__ int32_t old[];
-    const int c0 = blockIdx.x * cols, width = min(cols, k.max_pages - c0);
-    const int cells = k.B * cols;
+    const int cols = 1 << shift, c0 = blockIdx.x << shift, width = min(cols, k.max_pages - c0);
+    const int cells = k.B << shift;
+#pragma unroll 4
     for (int e = threadIdx.x; e < cells; e += kReorderThreads) {
-        const int b = e / cols, c = e - b * cols;
+        const int b = e >> shift, c = e & (cols - 1);
         if (c < width) old[e] = k.table[(int64_t)b * k.max_pages + c0 + c];
     }
     __syncthreads();
+#pragma unroll 2
     for (int e = threadIdx.x; e < cells; e += kReorderThreads) {
-        const int b = e / cols, c = e - b * cols;
+        const int b = e >> shift, c = e & (cols - 1);
         if (c >= width) continue;
         const int s = src[b];
         if (s == b) continue;
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const Books k,
         const int j = c0 + c, was = old[e];
         int to = -1;
         if (s >= 0 && j < pages_of(held(k, s), k.page_size)) {
-            to = old[s * cols + c];
+            to = old[(s << shift) + c];
             if (to < 0 || to >= k.num_pages) {
                 flag(k, FD_DEV_BAD_INDEX);
                 to = -1;
@@ -698,14 +700,14 @@ int launch_pages_fork(const Books &k, const int32_t *src, const int32_t *dst, co
 }
 
 int launch_pages_reorder(const Books &k, const int32_t *src, int32_t *ticket, cudaStream_t st) {
-    int cols = 32;
-    while (cols > 1 && (int64_t)k.B * cols > kReorderRows) cols /= 2;
-    const int bytes = k.B * cols * 4;
+    int shift = kReorderShift;
+    while (shift > 0 && ((int64_t)k.B << shift) > kReorderRows) --shift;
+    const int bytes = (k.B << shift) * 4;
     if (bytes > 48 * 1024 && cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                   kReorderRows * 4) != cudaSuccess)
         return -5;
-    const unsigned blocks = (unsigned)ceil_div(k.max_pages, cols);
-    reorder_kernel<<<blocks, kReorderThreads, bytes, st>>>(k, src, cols, ticket);
+    const unsigned blocks = (unsigned)ceil_div(k.max_pages, 1 << shift);
+    reorder_kernel<<<blocks, kReorderThreads, bytes, st>>>(k, src, shift, ticket);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 

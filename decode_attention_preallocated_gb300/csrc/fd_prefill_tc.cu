@@ -835,11 +835,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------- join
-// One block for each place between two blocks' shares: if it cuts a segment's
-// blocks of positions, this place's part of the segment's rows is joined from
-// the pieces, in order.
+// blockIdx.x: a place between two blocks' shares.  If it cuts a segment's blocks
+// of positions, this place's part of the segment's rows (of kJoinParts) is
+// joined from the pieces, in order.
+constexpr int kJoinParts = 4, kJoinThreads = 256;
+
 template <int D, bool TWO>
-__global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant__ PfArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__ PfArgs a, int grid) {
     using C = Cfg<D, TWO>;
     const PrefillParams &p = a.p;
     const int c = blockIdx.x + 1;
@@ -850,29 +852,34 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(const __grid_constant
     const Split sp = w.split();
     const int first = sp.owner(w.block_unit(0)), last = sp.owner(w.block_unit(all - 1));
     if (c <= first || c > last) return;
-    const int places = last - first, at = c - first - 1;
-    const int r0 = C::ROWS * at / places, r1 = C::ROWS * (at + 1) / places;
+    const int parts = (last - first) * kJoinParts, at = (c - first - 1) * kJoinParts + (int)blockIdx.y;
+    const int r0 = C::ROWS * at / parts, r1 = C::ROWS * (at + 1) / parts;
     constexpr int PER = D / 8;
-    for (int e = r0 * PER + (int)threadIdx.x; e < r1 * PER; e += 256) {
+    for (int e = r0 * PER + (int)threadIdx.x; e < r1 * PER; e += kJoinThreads) {
         const int r = e / PER, d = (e % PER) * 8;
         int64_t token, off;
         if (!row_at(a, w, r / TT, r % TT, token, off)) continue;
-        const auto slot = [&](int k) { return a.slots + (2 * (int64_t)k + (k == first ? 1 : 0)) * C::SLOT_FLOATS; };
-        float top = neg_inf();
-        for (int k = first; k <= last; ++k) top = fmaxf(top, slot(k)[C::ROWS * D + r]);
-        float l = 0.f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (top > neg_inf()) {
-            for (int k = first; k <= last; ++k) {
-                const float *s = slot(k), m = s[C::ROWS * D + r];
-                if (m == neg_inf()) continue;       // this piece saw nothing and holds no O
-                const float f = fast_exp2(m - top);
-                const float4 u = *reinterpret_cast<const float4 *>(s + (int64_t)r * D + d);
-                const float4 v = *reinterpret_cast<const float4 *>(s + (int64_t)r * D + d + 4);
-                const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-                l = fmaf(f, s[C::ROWS * (D + 1) + r], l);
+        // the first piece is its block's second slot, the others their first
+        const float *s = a.slots + (2 * (int64_t)first + 1) * C::SLOT_FLOATS;
+        int64_t step = C::SLOT_FLOATS;
+        float top = neg_inf(), l = 0.f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+        for (int k = first; k <= last; ++k) {
+            // (a piece that saw nothing for the row holds no O)
+            const float m = s[C::ROWS * D + r];
+            const float4 u = *reinterpret_cast<const float4 *>(s + (int64_t)r * D + d);
+            const float4 v = *reinterpret_cast<const float4 *>(s + (int64_t)r * D + d + 4);
+            const float more = s[C::ROWS * (D + 1) + r];
+            s += step;
+            step = 2 * C::SLOT_FLOATS;
+            const float now = fmaxf(top, m), f = now == neg_inf() ? 0.f : fast_exp2(top - now);
+            const bool any = m != neg_inf();
+            const float g = any ? fast_exp2(m - now) : 0.f;
+            const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            top = now;
+            l = l * f + (any ? more * g : 0.f);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = fmaf(f, y[i], o[i]);
-            }
+            for (int i = 0; i < 8; ++i) o[i] = o[i] * f + (any ? y[i] * g : 0.f);
         }
         const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
         *reinterpret_cast<uint4 *>(p.out + off + d) =
@@ -923,7 +930,7 @@ int launch(const PfArgs &a, int grid, cudaStream_t st) {
         return -5;
     prefill_tc_kernel<D, TWO><<<grid, kThreads, C::SMEM, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return -5;
-    if (grid > 1) prefill_join_kernel<D, TWO><<<grid - 1, 256, 0, st>>>(a, grid);
+    if (grid > 1) prefill_join_kernel<D, TWO><<<dim3(grid - 1, kJoinParts), kJoinThreads, 0, st>>>(a, grid);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 

@@ -9,7 +9,8 @@ namespace fd {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kBatch = 3;      // heads whose loads a thread has in flight
 
 __device__ __forceinline__ void write_length(const RowsParams &p, int b) {
     const int64_t raw = p.lengths[b], base = clamp_len(raw, p.c.cap);
@@ -69,8 +70,9 @@ __device__ __forceinline__ uint2 codes_of(const float *x, float s) {
 }
 
 // One block per token: its heads of q, k and v, LANES threads a head.
-template <int LANES>
+template <int LANES, bool INT8>
 __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ RowsParams p) {
+    constexpr int kSlots = kThreads / LANES;   // heads side by side
     const int b = (int)(blockIdx.x / (uint32_t)p.n), i = (int)(blockIdx.x % (uint32_t)p.n);
     const int64_t base = clamp_len(__ldg(p.lengths + b), p.c.cap);
     const int real = p.new_lengths ? (int)clamp_len(__ldg(p.new_lengths + b), p.n) : p.n;
@@ -106,51 +108,74 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_cons
             *reinterpret_cast<float4 *>(sn + 4) = __ldg(s + 1);
         }
         const int Hq = p.q ? p.Hq : 0, heads = Hq + 2 * p.c.Hkv;
-        // (every thread of a head's lanes takes the same turns of this loop)
-        for (int h = (int)threadIdx.x / LANES; h < heads; h += kThreads / LANES) {
-            const bool is_q = h < Hq, is_v = h >= Hq + p.c.Hkv;
-            const int hh = is_q ? h : h - Hq - (is_v ? p.c.Hkv : 0);
-            if (!is_q && !kept) continue;
-            const uint16_t *src = is_q ? p.q + b * p.qs[0] + i * p.qs[1] + hh * p.qs[2]
-                                       : is_v ? p.v_new + b * p.vns[0] + i * p.vns[1] + hh * p.vns[2]
-                                              : p.k_new + b * p.kns[0] + i * p.kns[1] + hh * p.kns[2];
-            const int lo = is_v ? 16 * u : unit.lo, hi = is_v ? 16 * u + 8 : unit.hi;
-            float x[16];
-            widen(*reinterpret_cast<const uint4 *>(src + lo), x);
-            widen(*reinterpret_cast<const uint4 *>(src + hi), x + 8);
-            if (!is_v && unit.turns) {
-                if (unit.across) {
+        // kBatch heads' loads set out together; every thread of a head's lanes
+        // takes the same turns of these loops
+        for (int h0 = (int)threadIdx.x / LANES; h0 < heads; h0 += kBatch * kSlots) {
+            uint4 wl[kBatch], wh[kBatch];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) turn(x[e], x[e + 8], cs[e], sn[e]);
-                } else {
+            for (int e = 0; e < kBatch; ++e) {
+                const int h = h0 + e * kSlots;
+                const bool is_q = h < Hq, is_v = h >= Hq + p.c.Hkv;
+                if (h >= heads || (!is_q && !kept)) continue;
+                const int hh = is_q ? h : h - Hq - (is_v ? p.c.Hkv : 0);
+                const uint16_t *src = is_q ? p.q + b * p.qs[0] + i * p.qs[1] + hh * p.qs[2]
+                                           : is_v ? p.v_new + b * p.vns[0] + i * p.vns[1] + hh * p.vns[2]
+                                                  : p.k_new + b * p.kns[0] + i * p.kns[1] + hh * p.kns[2];
+                wl[e] = *reinterpret_cast<const uint4 *>(src + (is_v ? 16 * u : unit.lo));
+                wh[e] = *reinterpret_cast<const uint4 *>(src + (is_v ? 16 * u + 8 : unit.hi));
+            }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) turn(x[2 * e], x[2 * e + 1], cs[e], sn[e]);
+            for (int e = 0; e < kBatch; ++e) {
+                const int h = h0 + e * kSlots;
+                const bool is_q = h < Hq, is_v = h >= Hq + p.c.Hkv;
+                if (h >= heads || (!is_q && !kept)) continue;
+                const int hh = is_q ? h : h - Hq - (is_v ? p.c.Hkv : 0);
+                const int lo = is_v ? 16 * u : unit.lo, hi = is_v ? 16 * u + 8 : unit.hi;
+                if (!INT8 && (is_v || !unit.turns)) {
+                    // nothing to compute
+                    uint16_t *dst = is_q ? p.q_out + b * p.qos[0] + i * p.qos[1] + hh * p.qos[2]
+                                         : is_v ? static_cast<uint16_t *>(p.c.v) + lead * p.c.vs[0] + hh * p.c.vs[1] + row * p.c.vs[2]
+                                                : static_cast<uint16_t *>(p.c.k) + lead * p.c.ks[0] + hh * p.c.ks[1] + row * p.c.ks[2];
+                    *reinterpret_cast<uint4 *>(dst + lo) = wl[e];
+                    *reinterpret_cast<uint4 *>(dst + hi) = wh[e];
+                    continue;
                 }
-            }
-            if (is_q || !p.c.int8) {
-                uint16_t *dst = is_q ? p.q_out + b * p.qos[0] + i * p.qos[1] + hh * p.qos[2]
-                                     : is_v ? static_cast<uint16_t *>(p.c.v) + lead * p.c.vs[0] + hh * p.c.vs[1] + row * p.c.vs[2]
-                                            : static_cast<uint16_t *>(p.c.k) + lead * p.c.ks[0] + hh * p.c.ks[1] + row * p.c.ks[2];
-                *reinterpret_cast<uint4 *>(dst + lo) = narrow(x);
-                *reinterpret_cast<uint4 *>(dst + hi) = narrow(x + 8);
-                continue;
-            }
-            // the largest magnitude of the row, by its bits (a NaN's are the
-            // largest of all)
-            uint32_t top = 0;
+                float x[16];
+                widen(wl[e], x);
+                widen(wh[e], x + 8);
+                if (!is_v && unit.turns) {
+                    if (unit.across) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-            const uint32_t lanes = LANES == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
-            top = __reduce_max_sync(lanes, top);
-            const float s = top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fffffffu);
-            char *dst = is_v ? static_cast<char *>(p.c.v) + lead * p.c.vs[0] + hh * p.c.vs[1] + row * p.c.vs[2]
-                             : static_cast<char *>(p.c.k) + lead * p.c.ks[0] + hh * p.c.ks[1] + row * p.c.ks[2];
-            *reinterpret_cast<uint2 *>(dst + lo) = codes_of(x, s);
-            *reinterpret_cast<uint2 *>(dst + hi) = codes_of(x + 8, s);
-            if (u == 0) {
-                float *to = is_v ? p.c.v_scale + lead * p.c.vss[0] + hh * p.c.vss[1] + row * p.c.vss[2]
-                                 : p.c.k_scale + lead * p.c.kss[0] + hh * p.c.kss[1] + row * p.c.kss[2];
-                *to = s;
+                        for (int k = 0; k < 8; ++k) turn(x[k], x[k + 8], cs[k], sn[k]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) turn(x[2 * k], x[2 * k + 1], cs[k], sn[k]);
+                    }
+                }
+                if (is_q || !INT8) {
+                    uint16_t *dst = is_q ? p.q_out + b * p.qos[0] + i * p.qos[1] + hh * p.qos[2]
+                                         : static_cast<uint16_t *>(p.c.k) + lead * p.c.ks[0] + hh * p.c.ks[1] + row * p.c.ks[2];
+                    *reinterpret_cast<uint4 *>(dst + lo) = narrow(x);
+                    *reinterpret_cast<uint4 *>(dst + hi) = narrow(x + 8);
+                    continue;
+                }
+                // the largest magnitude of the row, by its bits (a NaN's are the
+                // largest of all)
+                uint32_t top = 0;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
+                const uint32_t lanes = LANES == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
+                top = __reduce_max_sync(lanes, top);
+                const float s = top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 127.f) : __uint_as_float(0x7fffffffu);
+                char *dst = is_v ? static_cast<char *>(p.c.v) + lead * p.c.vs[0] + hh * p.c.vs[1] + row * p.c.vs[2]
+                                 : static_cast<char *>(p.c.k) + lead * p.c.ks[0] + hh * p.c.ks[1] + row * p.c.ks[2];
+                *reinterpret_cast<uint2 *>(dst + lo) = codes_of(x, s);
+                *reinterpret_cast<uint2 *>(dst + hi) = codes_of(x + 8, s);
+                if (u == 0) {
+                    float *to = is_v ? p.c.v_scale + lead * p.c.vss[0] + hh * p.c.vss[1] + row * p.c.vss[2]
+                                     : p.c.k_scale + lead * p.c.kss[0] + hh * p.c.kss[1] + row * p.c.kss[2];
+                    *to = s;
+                }
             }
         }
     }
@@ -177,8 +202,10 @@ __global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_cons
 
 int launch_append_rows(const RowsParams &p, cudaStream_t st) {
     const unsigned blocks = (unsigned)p.B * (unsigned)p.n;
-    if (p.c.d == 128) append_rows_kernel<8><<<blocks, kThreads, 0, st>>>(p);
-    else append_rows_kernel<16><<<blocks, kThreads, 0, st>>>(p);
+    if (p.c.d == 128 && !p.c.int8) append_rows_kernel<8, false><<<blocks, kThreads, 0, st>>>(p);
+    else if (p.c.d == 128) append_rows_kernel<8, true><<<blocks, kThreads, 0, st>>>(p);
+    else if (!p.c.int8) append_rows_kernel<16, false><<<blocks, kThreads, 0, st>>>(p);
+    else append_rows_kernel<16, true><<<blocks, kThreads, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
