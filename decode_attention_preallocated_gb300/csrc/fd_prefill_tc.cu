@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "fd_api.h"
 #include "fd_device.cuh"
@@ -95,56 +96,59 @@ static_assert(sizeof(Bars) <= 512, "barrier block");
 // Positions that a segment's start and end are charged as.
 constexpr int64_t kCharge = 256;
 
+// What a launch's share of the work goes by: B sequences of L_b positions, fresh_b
+// of them new.
 struct Seq {
-    int64_t L, fresh, base;
-    int nq;                  // segments a kv head
+    int L, fresh, nq;        // nq: segments a kv head
+    __device__ __forceinline__ int base() const { return L - fresh; }
 };
 
 __device__ __forceinline__ Seq seq_of(const PrefillParams &p, int b, int S, bool flag = false) {
     const int64_t raw = __ldg(p.lengths + b), L = clamp_len(raw, p.c.cap);
     const int64_t want = p.new_lengths ? __ldg(p.new_lengths + b) : p.n, fresh = clamp_len(want, p.n);
     if (flag && (raw != L || want != fresh)) atomicOr(p.status, kDevBadLength);
-    return Seq{L, fresh, L - fresh, (int)((fresh + S - 1) / S)};
+    return Seq{(int)L, (int)fresh, (int)((fresh + S - 1) / S)};
 }
 
-// Units of the first q segments of a kv head.
+// Units of a segment, and of the first q of a kv head.
+__device__ __forceinline__ int64_t cost_of(const PrefillParams &p, const Seq &s, int S, int q) {
+    return kCharge + (p.causal ? max(s.base(), 0) + (int64_t)S * (q + 1) : (int64_t)s.L);
+}
 __device__ __forceinline__ int64_t units_of(const PrefillParams &p, const Seq &s, int S, int64_t q) {
     if (!p.causal) return q * (kCharge + s.L);
-    return q * (kCharge + (s.base > 0 ? s.base : 0)) + S * (q * (q + 1) / 2);
+    return q * (kCharge + max(s.base(), 0)) + S * (q * (q + 1) / 2);
 }
 
-// A block's walk over the segments of its share.
+// All units, and the blocks that share them.
+struct Total {
+    int64_t units;
+    int G;
+    __device__ __forceinline__ Split split() const { return Split{units, G}; }
+};
+
+// Every lane of a warp.
+__device__ __forceinline__ Total total_of(const PrefillParams &p, int S, int grid, bool flag) {
+    int64_t sum = 0;
+    for (int i = threadIdx.x & 31; i < p.B; i += 32) {
+        const Seq x = seq_of(p, i, S, flag);
+        sum += units_of(p, x, S, x.nq);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    sum *= p.c.Hkv;
+    const int64_t most = sum / TT;
+    return Total{sum, (int)(most < 1 ? 1 : most < grid ? most : grid)};
+}
+
+// A walk over the segments of a share: the current one, and where the share starts
+// and ends, counted from the unit of its first position.
 struct Walk {
-    int S;                   // tokens a segment
-    int64_t total;
-    int G;                   // blocks that share the units
-    int64_t u0, u1;          // this block's
-    int64_t a, cost;         // first unit and units of the current segment
+    int64_t from, to;
     Seq s;
     int b, hk, q;
 
-    // Every lane of a warp; `c`: the block.  False where it has no work.
-    __device__ __forceinline__ bool find(const PrefillParams &p, int tokens, int c, int grid, bool flag) {
-        S = tokens;
-        const int lane = threadIdx.x & 31;
-        int64_t sum = 0;
-        for (int i = lane; i < p.B; i += 32) {
-            const Seq x = seq_of(p, i, S, flag);
-            sum += units_of(p, x, S, x.nq);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-        total = sum * p.c.Hkv;
-        const int64_t most = total / TT;
-        G = (int)(most < 1 ? 1 : most < grid ? most : grid);
-        if (c >= G || total == 0) return false;
-        u0 = split().start(c);
-        u1 = split().start(c + 1);
-        return seek(p, u0);
-    }
-    __device__ __forceinline__ Split split() const { return Split{total, G}; }
-    // The segment that holds unit u.
-    __device__ __forceinline__ bool seek(const PrefillParams &p, int64_t u) {
+    // The segment that holds unit u0 of a share [u0, u1); every lane of a warp.
+    __device__ __forceinline__ void seek(const PrefillParams &p, int S, int64_t u0, int64_t u1) {
         const int lane = threadIdx.x & 31;
         int64_t before = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -160,18 +164,18 @@ struct Walk {
                 const int64_t y = __shfl_up_sync(kAll, upto, o);
                 if (lane >= o) upto += y;
             }
-            const unsigned in = __ballot_sync(kAll, before + upto > u);
+            const unsigned in = __ballot_sync(kAll, before + upto > u0);
             if (in) {
                 const int at = __ffs(in) - 1;
                 const int64_t first = before + __shfl_sync(kAll, upto - mine, at);
                 b = b0 + at;
                 s = seq_of(p, b, S);
                 const int64_t head = units_of(p, s, S, s.nq);
-                hk = (int)((u - first) / head);
-                const int64_t x = u - first - hk * head;
+                hk = (int)((u0 - first) / head);
+                const int64_t x = u0 - first - hk * head;
                 if (p.causal) {
                     // S/2 q^2 + k q = x
-                    const float k = (float)(kCharge + (s.base > 0 ? s.base : 0)) + 0.5f * S;
+                    const float k = (float)(kCharge + max(s.base(), 0)) + 0.5f * S;
                     q = (int)((sqrtf(k * k + 2.f * S * (float)x) - k) / S);
                 } else {
                     q = (int)(x / (kCharge + s.L));
@@ -179,17 +183,19 @@ struct Walk {
                 q = max(0, min(q, s.nq - 1));
                 while (q > 0 && units_of(p, s, S, q) > x) --q;
                 while (q + 1 < s.nq && units_of(p, s, S, q + 1) <= x) ++q;
-                a = first + hk * head + units_of(p, s, S, q);
-                cost = units_of(p, s, S, q + 1) - units_of(p, s, S, q);
-                return true;
+                const int64_t a = first + hk * head + units_of(p, s, S, q) + kCharge;
+                from = u0 - a;
+                to = u1 - a;
+                return;
             }
             before += __shfl_sync(kAll, upto, 31);
         }
-        return false;
     }
-    __device__ __forceinline__ bool next(const PrefillParams &p) {
-        a += cost;
-        if (a >= u1) return false;
+    __device__ __forceinline__ bool next(const PrefillParams &p, int S) {
+        const int64_t cost = cost_of(p, s, S, q);
+        from -= cost;
+        to -= cost;
+        if (to + kCharge <= 0) return false;
         if (++q == s.nq) {
             q = 0;
             if (++hk == p.c.Hkv) {
@@ -200,20 +206,17 @@ struct Walk {
                 } while (s.nq == 0);
             }
         }
-        cost = units_of(p, s, S, q + 1) - units_of(p, s, S, q);
         return true;
     }
     // Positions that the first `tokens` of this segment see.
-    __device__ __forceinline__ int64_t seen(const PrefillParams &p, int tokens) const {
+    __device__ __forceinline__ int seen(const PrefillParams &p, int S, int tokens) const {
         if (!p.causal) return s.L;
-        const int64_t last = min(s.fresh, (int64_t)q * S + tokens);
-        return clamp_len(s.base + last, s.L);
+        return max(0, min(s.L, s.base() + (int)min((int64_t)s.fresh, (int64_t)q * S + tokens)));
     }
-    __device__ __forceinline__ int blocks(const PrefillParams &p) const { return (int)((seen(p, S) + TT - 1) / TT); }
-    __device__ __forceinline__ int64_t block_unit(int j) const { return a + kCharge + (int64_t)j * TT; }
+    __device__ __forceinline__ int blocks(const PrefillParams &p, int S) const { return (seen(p, S, S) + TT - 1) / TT; }
 };
 
-// The blocks of positions of the current segment that are this block's, and of
+// The blocks of positions of the current segment that are this share's, and of
 // them those that each tile sees.
 struct Piece {
     int j0, j1, all;         // of `all`
@@ -224,18 +227,16 @@ struct Piece {
 template <int QT>
 __device__ __forceinline__ Piece piece_of(const PfArgs &a, const Walk &w) {
     const PrefillParams &p = a.p;
+    const int S = QT * a.T;
     Piece x;
-    x.all = w.blocks(p);
-    const int64_t from = w.u0 - w.a - kCharge, to = w.u1 - w.a - kCharge;
-    x.j0 = from <= 0 ? 0 : (int)min((int64_t)x.all, (from + TT - 1) / TT);
-    x.j1 = to <= 0 ? 0 : (int)min((int64_t)x.all, (to + TT - 1) / TT);
+    x.all = w.blocks(p, S);
+    x.j0 = w.from <= 0 ? 0 : (int)min((int64_t)x.all, (w.from + TT - 1) / TT);
+    x.j1 = w.to <= 0 ? 0 : (int)min((int64_t)x.all, (w.to + TT - 1) / TT);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         x.hi[t] = x.j0;
-        if (t < QT && (int64_t)w.q * w.S + t * a.T < w.s.fresh) {
-            const int n = (int)((w.seen(p, (t + 1) * a.T) + TT - 1) / TT);
-            x.hi[t] = max(x.j0, min(x.j1, n));
-        }
+        if (t < QT && (int64_t)w.q * S + t * a.T < w.s.fresh)
+            x.hi[t] = max(x.j0, min(x.j1, (w.seen(p, S, (t + 1) * a.T) + TT - 1) / TT));
     }
     return x;
 }
@@ -285,9 +286,10 @@ __device__ __forceinline__ void store32(void *dst, const uint32_t *w) {
 }
 
 // Row `row` of tile t of the current segment: its token, where it is stored.
-__device__ __forceinline__ bool row_at(const PfArgs &a, const Walk &w, int t, int row, int64_t &token, int64_t &off) {
+template <int QT>
+__device__ __forceinline__ bool row_at(const PfArgs &a, const Walk &w, int t, int row, int &token, int64_t &off) {
     const PrefillParams &p = a.p;
-    token = (int64_t)w.q * w.S + (int64_t)t * a.T + row / p.g;
+    token = (w.q * QT + t) * a.T + row / p.g;
     off = w.b * p.os[0] + token * p.os[1] + ((int64_t)w.hk * p.g + row % p.g) * p.os[2];
     return row < a.R && token < w.s.fresh;
 }
@@ -330,8 +332,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         ptx::tmem_alloc(&bs->tmem_base, 512);
         ptx::tmem_relinquish();
     }
+    const int S = C::QT * a.T;           // tokens a segment
     Walk w;
-    const bool has = w.find(p, C::QT * a.T, blockIdx.x, gridDim.x, warp == kProducerWarp && blockIdx.x == 0);
+    bool has;
+    {
+        const Total total = total_of(p, S, gridDim.x, warp == kProducerWarp && blockIdx.x == 0);
+        has = (int)blockIdx.x < total.G && total.units > 0;
+        if (has) w.seek(p, S, total.split().start(blockIdx.x), total.split().start(blockIdx.x + 1));
+    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             int y[4];
         };
         const bool paged = p.c.block_table != nullptr;
-        for (bool more = has; more && ok; more = w.next(p)) {
+        for (bool more = has; more && ok; more = w.next(p, S)) {
             const Piece x = piece_of<C::QT>(a, w);
             if (x.j0 >= x.j1) continue;
 #pragma unroll
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                         ptx::mbar_arrive_expect_tx(&bs->q_full[t], (uint32_t)(a.R * 128 * (D / 64)));
                         for (int cb = 0; cb < D / 64; ++cb)
                             ptx::tma_load_4d(smem + C::OFF_Q + t * C::QTILE + cb * C::BOX, &a.tq, &bs->q_full[t], cb * 64,
-                                             w.hk * p.g, w.q * w.S + t * a.T, w.b);
+                                             w.hk * p.g, w.q * S + t * a.T, w.b);
                     }
                 }
                 ok = __shfl_sync(kAll, ok, 0);
@@ -404,10 +412,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 ++fills;
                 unsigned char *dst = smem + C::OFF_SLOTS + slot * C::SLOT;
                 if (!paged) {
-                    const int64_t y = min((int64_t)j * TT, w.s.L - TT);   // the last tile ends at the length
+                    const int y = min(j * TT, w.s.L - TT);   // the last tile ends at the length
                     if (lane < 2)
                         ptx::tma_load_4d(dst + lane * C::BOX, v ? &a.tv : &a.tk, &bs->slot_full[slot], h * 128 + lane * 64,
-                                         (int)y, w.hk, w.b);
+                                         y, w.hk, w.b);
                 } else if (tiled(j)) {
                     if (lane < TT / a.prow)
 #pragma unroll
@@ -511,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                                     !(first && kt == 0));
             };
             const auto free_slot = [&](uint32_t i) { ptx::mma_commit(&bs->slot_empty[i % C::NS]); };
-            for (bool more = has; more && ok; more = w.next(p)) {
+            for (bool more = has; more && ok; more = w.next(p, S)) {
                 const Piece x = piece_of<C::QT>(a, w);
                 if (x.j0 >= x.j1) continue;
                 for (int t = 0; t < C::QT; ++t)
@@ -619,51 +627,40 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             return room[(group ^ 1) * 128 + row];
         };
         const float sc = p.scale_log2;
-        for (bool more = has; more && ok; more = w.next(p)) {
+        for (bool more = has; more && ok; more = w.next(p, S)) {
             const Piece x = piece_of<C::QT>(a, w);
-            int64_t token, off;
-            const bool real = row_at(a, w, t, row, token, off);
+            int token;
+            int64_t off;
+            const bool real = row_at<C::QT>(a, w, t, row, token, off);
             if (x.all == 0) {
                 // nobody sees anything: the block of the segment's first unit
-                if (w.a >= w.u0 && real) {
-                    const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (w.from + kCharge <= 0 && real)
                     for (int c = 0; c < C::OC; c += 8)
-                        *reinterpret_cast<uint4 *>(p.out + off + (TWO ? 0 : group * C::OC) + c) =
-                            make_uint4(zero[0], zero[1], zero[2], zero[3]);
-                }
+                        *reinterpret_cast<uint4 *>(p.out + off + (TWO ? 0 : group * C::OC) + c) = make_uint4(0, 0, 0, 0);
                 continue;
             }
             if (x.j0 >= x.j1) continue;
             const int n = x.hi[t] - x.j0;
-            const int64_t first = (int64_t)w.q * w.S + (int64_t)t * a.T;     // the tile's first token
-            const int last = (int)(p.causal ? min(w.s.base + token, w.s.L - 1) : w.s.L - 1);
-            const int64_t all_see = p.causal ? min(w.s.base + first, w.s.L - 1) : w.s.L - 1;
+            const int first = w.q * S + t * a.T;            // the tile's first token
+            const int last = p.causal ? min(w.s.base() + token, w.s.L - 1) : w.s.L - 1;
+            const int all_see = p.causal ? min(w.s.base() + first, w.s.L - 1) : w.s.L - 1;
             float m = neg_inf(), l = 0.f;
             uint64_t sum0 = 0, sum1 = 0;
-            for (int j = x.j0; j < x.hi[t] && ok; ++j) {
-                const uint32_t buf = TWO ? t : ctr & 1, use = TWO ? ctr : ctr >> 1;
-                ++ctr;
+            // one block of positions; with MASK some row does not see all of it
+            const auto block = [&](int j, uint32_t buf, const volatile uint32_t *bad, bool holes, auto mask_tag) {
+                constexpr bool MASK = decltype(mask_tag)::value;
                 const uint32_t s_at = tmem + lanes + buf * 128;
-                ok = wait_on(bs, p, &bs->s_full[buf], use, 7);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const int pos0 = j * TT;
-                const uint32_t *bad = reinterpret_cast<const uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
-                const bool holes = p.c.block_table && *reinterpret_cast<const volatile uint32_t *>(bad);
-                const bool masked = holes || (int64_t)pos0 + TT - 1 > all_see;
-                const int at = p.c.block_table ? pos0 : (int)min((int64_t)pos0, w.s.L - TT);   // position of column 0
-                const int lo = pos0 - at - col0, hi = last - at - col0;   // columns that the row sees
                 // 32 score columns from c on, hidden ones as -inf
                 const auto hide = [&](float *s, int c) {
+                    const int pos0 = j * TT;
+                    const int at = p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
+                    // of these columns the row sees lo .. hi - 1, less those on no page
+                    const int lo = min(max(pos0 - at - col0 - c, 0), 32), hi = min(max(last + 1 - at - col0 - c, 0), 32);
+                    uint32_t sees = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+                    if (holes) sees &= ~bad[1 + (col0 + c) / 32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (c + e < lo || c + e > hi) s[e] = neg_inf();
-                    if (holes) {
-                        const uint32_t word = bad[1 + (col0 + c) / 32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if ((word >> e) & 1u) s[e] = neg_inf();
-                    }
+                        if (!((sees >> e) & 1u)) s[e] = neg_inf();
                 };
                 const auto most = [&](const float *s, float top) {
                     float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
@@ -683,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                     ptx::tmem_ld32(s_at + c, c == 64 ? s : s + 32);
                     if (c == 96) {
                         ptx::tmem_wait_ld();
-                        if (masked) {
+                        if (MASK) {
                             hide(s, 64);
                             hide(s + 32, 96);
                         }
@@ -693,13 +690,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 ptx::tmem_ld32(s_at + col0, s);
                 ptx::tmem_ld32(s_at + col0 + 32, s + 32);
                 ptx::tmem_wait_ld();
-                if (masked) {
+                if (MASK) {
                     hide(s, 0);
                     hide(s + 32, 32);
                 }
                 top = most(s, most(s + 32, top));
                 if (!TWO) top = fmaxf(top, other(top));
-                if (!ok) break;
+                if (!ok) return;
                 // a new reference where a score passes the old one by 2^8
                 // (rows that are nobody's hold what was left in shared memory)
                 const bool raise = real && ((top - m) * sc > kSlack || m == neg_inf());
@@ -717,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                         // scores, whose end was waited for; one tile: after
                         if (!TWO) {
                             ok = wait_on(bs, p, &bs->pv_done, ctr - 2, 9);
-                            if (!ok) break;
+                            if (!ok) return;
                             ptx::tc_fence_after();
                         }
 #pragma unroll 1
@@ -754,15 +751,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 if (C::NC == 128) {
                     ptx::tmem_wait_ld();
                     ptx::tmem_ld32(s_at + 96, s);
-                    if (masked) hide(h, 64);
+                    if (MASK) hide(h, 64);
                     weigh(h, 64);
                     ptx::tmem_wait_ld();
-                    if (masked) hide(s, 96);
+                    if (MASK) hide(s, 96);
                     weigh(s, 96);
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&bs->p_full[buf]);
+            };
+            const int plain = (all_see + 1) / TT;      // blocks that every row sees whole
+            for (int j = x.j0; j < x.hi[t] && ok; ++j) {
+                const uint32_t buf = TWO ? t : ctr & 1, use = TWO ? ctr : ctr >> 1;
+                ++ctr;
+                ok = wait_on(bs, p, &bs->s_full[buf], use, 7);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const volatile uint32_t *bad = reinterpret_cast<const volatile uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
+                const bool holes = p.c.block_table && bad[0] != 0;
+                if (j < plain && !holes) block(j, buf, bad, holes, std::false_type());
+                else block(j, buf, bad, holes, std::true_type());
             }
             if (!ok) break;
             seen += x.j1 - x.j0;
@@ -845,20 +854,26 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
     using C = Cfg<D, TWO>;
     const PrefillParams &p = a.p;
     const int c = blockIdx.x + 1;
+    const int S = C::QT * a.T;
+    const Total total = total_of(p, S, grid, false);
+    if (c >= total.G || total.units == 0) return;
+    const Split sp = total.split();
+    const int64_t u = sp.start(c);
     Walk w;
-    if (!w.find(p, C::QT * a.T, c, grid, false)) return;
-    const int all = w.blocks(p);
+    w.seek(p, S, u, u);
+    const int all = w.blocks(p, S);
     if (all == 0) return;
-    const Split sp = w.split();
-    const int first = sp.owner(w.block_unit(0)), last = sp.owner(w.block_unit(all - 1));
+    const int64_t block0 = u - w.from;                      // unit of the first block
+    const int first = sp.owner(block0), last = sp.owner(block0 + (int64_t)(all - 1) * TT);
     if (c <= first || c > last) return;
     const int parts = (last - first) * kJoinParts, at = (c - first - 1) * kJoinParts + (int)blockIdx.y;
     const int r0 = C::ROWS * at / parts, r1 = C::ROWS * (at + 1) / parts;
     constexpr int PER = D / 8;
     for (int e = r0 * PER + (int)threadIdx.x; e < r1 * PER; e += kJoinThreads) {
         const int r = e / PER, d = (e % PER) * 8;
-        int64_t token, off;
-        if (!row_at(a, w, r / TT, r % TT, token, off)) continue;
+        int token;
+        int64_t off;
+        if (!row_at<C::QT>(a, w, r / TT, r % TT, token, off)) continue;
         // the first piece is its block's second slot, the others their first
         const float *s = a.slots + (2 * (int64_t)first + 1) * C::SLOT_FLOATS;
         int64_t step = C::SLOT_FLOATS;
