@@ -16,9 +16,12 @@
 // Roles in a block:
 //   warp 8   TMA producer: Q of a segment, then K and V tiles of 128 positions
 //            in halves of 128 dimensions, into a ring of shared-memory slots.
-//   warp 9   MMA issuer (one thread): S = Q K^T (128 x 128) into TMEM, O += P V
-//            with P from TMEM.
-//   (warps 10, 11 are idle.)
+//   warps 9, 10  MMA issuers (one thread each): S = Q K^T (128 x 128) into TMEM,
+//            O += P V with P from TMEM.  Two tiles: one issuer a tile; one tile: one
+//            for the scores, one for P V.  The queue of issued MMAs is short, and
+//            what a thread does between them (barriers, commits: half the time with
+//            one issuer) leaves the tensor pipe idle unless the other's are there.
+//   (warp 11 is idle.)
 //   warps 0-7  softmax: a thread owns a row (two tiles: of its group's tile) or
 //            half the columns of one (one tile, S then double buffered).  P
 //            overwrites S in TMEM in bf16.  A row's reference is its running
@@ -43,7 +46,7 @@ constexpr int TT = 128;
 // Three warpgroups: softmax takes registers that the third gives up.
 constexpr int kThreads = 384, kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;   // and 10
 constexpr int kDevTimeout = 4;          // mirrors FD_DEV_INTERNAL
 constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr float kSlack = 8.f;           // log2: how far a score may pass the reference
@@ -62,9 +65,10 @@ struct PfArgs {
 struct Bars {
     uint64_t slot_full[8], slot_empty[8];
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
-    uint64_t cross, pv_done, drain;
+    uint64_t cross, pv_done[2], drain[2];
     uint32_t tmem_base;
     int abort_flag;
+    int turn;                // held by the issuer whose tile's MMAs go out
 };
 
 template <int D, bool TWO>
@@ -259,6 +263,20 @@ __device__ __forceinline__ void drain_on(uint64_t *bar, uint32_t parity) {
         if ((n & 63) == 0 && ptx::globaltimer_ns() - t0 > kDrainNs) return;
 }
 
+// The issuers' turn, taken (within the limit of every wait) and given back.
+__device__ __forceinline__ bool take_turn(Bars *bs, const PrefillParams &p) {
+    if (atomicCAS(&bs->turn, 0, 1) == 0) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t n = 1; atomicCAS(&bs->turn, 0, 1) != 0; ++n)
+        if ((n & 63) == 0 && (*reinterpret_cast<volatile int *>(&bs->abort_flag) || ptx::globaltimer_ns() - t0 > p.wait_ns)) {
+            *reinterpret_cast<volatile int *>(&bs->abort_flag) = 1;
+            atomicOr(p.status, kDevTimeout);
+            return false;
+        }
+    return true;
+}
+__device__ __forceinline__ void give_turn(Bars *bs) { atomicExch(&bs->turn, 0); }
+
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -313,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         ptx::prefetch_tmap(&a.tv);
         for (int i = 0; i < C::NS; ++i) {
             ptx::mbar_init(&bs->slot_full[i], 1);
-            ptx::mbar_init(&bs->slot_empty[i], 1);
+            ptx::mbar_init(&bs->slot_empty[i], C::QT);   // two tiles: by both issuers
         }
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(&bs->q_full[t], 1);
@@ -321,11 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             ptx::mbar_init(&bs->s_full[t], 1);
             ptx::mbar_init(&bs->p_full[t], TWO ? 128 : 256);
             ptx::mbar_init(&bs->o_full[t], 1);
+            ptx::mbar_init(&bs->pv_done[t], 1);
+            ptx::mbar_init(&bs->drain[t], 1);
         }
         ptx::mbar_init(&bs->cross, 256);
-        ptx::mbar_init(&bs->pv_done, 1);
-        ptx::mbar_init(&bs->drain, 1);
         bs->abort_flag = 0;
+        bs->turn = 0;
         ptx::mbar_fence_init();
     }
     if (warp == kMmaWarp) {
@@ -486,122 +505,129 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         if (lane == 0)
             for (int t = 0; t < C::QT; ++t)
                 if (loads[t] > 0) drain_on(&bs->q_full[t], (loads[t] - 1) & 1);
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------- issuer
-        // (two tiles: PV of one tile and its next scores follow the other's, so
-        // that one tile's softmax runs under the other's products; one tile: the
-        // next scores are issued before PV)
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        // --------------------------------------------------------- issuers
         if (lane == 0) {
+            const int me = warp - kMmaWarp;
             bool ok = true;
-            uint32_t used = 0;               // slots consumed
-            uint32_t pieces[2] = {0, 0}, ctr[2] = {0, 0};
+            uint32_t filled = 0;             // slots of the pieces before
+            uint32_t pieces = 0, ctr = 0;
             const auto slot_at = [&](uint32_t i) { return base + C::OFF_SLOTS + (i % C::NS) * C::SLOT; };
             const auto wait_slot = [&](uint32_t i) {
                 ok = ok && wait_on(bs, p, &bs->slot_full[i % C::NS], i / C::NS, 3);
             };
+            const auto free_slot = [&](uint32_t i) { ptx::mma_commit(&bs->slot_empty[i % C::NS]); };
             // S[buf] (+)= Q_t K^T over one half of the dimensions
             const auto qk = [&](int t, uint32_t buf, uint32_t i, int h) {
-                const uint32_t q = base + C::OFF_Q + t * C::QTILE + h * C::SLOT, k = slot_at(i);
+                const uint64_t q = ptx::smem_desc(base + C::OFF_Q + t * C::QTILE + h * C::SLOT, 16, 1024, ptx::kLayoutSwizzle128);
+                const uint64_t k = ptx::smem_desc(slot_at(i), 16, 1024, ptx::kLayoutSwizzle128);
+                ptx::tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk)
-                    ptx::mma_f16_ss(tmem + buf * 128,
-                                    ptx::smem_desc(q + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024, ptx::kLayoutSwizzle128),
-                                    ptx::smem_desc(k + (kk >> 2) * C::BOX + (kk & 3) * 32, 16, 1024, ptx::kLayoutSwizzle128),
-                                    C::IDESC_QK, h > 0 || kk > 0);
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint64_t at = ((kk >> 2) * C::BOX + (kk & 3) * 32) >> 4;
+                    ptx::mma_f16_ss(tmem + buf * 128, q + at, k + at, C::IDESC_QK, h > 0 || kk > 0);
+                }
             };
             // O_t's dimensions of half h += P[buf] V
             const auto pv = [&](int t, uint32_t buf, uint32_t i, int h, bool first) {
-                const uint32_t v = slot_at(i);
+                const uint64_t v = ptx::smem_desc(slot_at(i), C::BOX, 1024, ptx::kLayoutSwizzle128);
+                ptx::tc_fence_after();
 #pragma unroll
                 for (int kt = 0; kt < 8; ++kt)
-                    ptx::mma_f16_ts(tmem + C::TMEM_O + t * 128 + h * 128, tmem + buf * 128 + kt * 8,
-                                    ptx::smem_desc(v + kt * 2048, C::BOX, 1024, ptx::kLayoutSwizzle128), C::IDESC_PV,
-                                    !(first && kt == 0));
+                    ptx::mma_f16_ts(tmem + C::TMEM_O + t * 128 + h * 128, tmem + buf * 128 + kt * 8, v + ((kt * 2048) >> 4),
+                                    C::IDESC_PV, !(first && kt == 0));
             };
-            const auto free_slot = [&](uint32_t i) { ptx::mma_commit(&bs->slot_empty[i % C::NS]); };
             for (bool more = has; more && ok; more = w.next(p, S)) {
                 const Piece x = piece_of<C::QT>(a, w);
-                if (x.j0 >= x.j1) continue;
-                for (int t = 0; t < C::QT; ++t)
-                    if (x.hi[t] > x.j0) ok = ok && wait_on(bs, p, &bs->q_full[t], pieces[t]++, 4);
-                if (!ok) break;
+                const int n = x.j1 - x.j0;
+                if (n <= 0) continue;
                 if (TWO) {
-                    uint32_t k = used++;     // the slot of K(j)
-                    wait_slot(k);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    for (int t = 0; t < 2; ++t)
-                        if (x.j0 < x.hi[t]) {
-                            qk(t, t, k, 0);
-                            ptx::mma_commit(&bs->s_full[t]);
-                            if (x.j0 + 1 == x.hi[t]) ptx::mma_commit(&bs->q_free[t]);
-                        }
-                    free_slot(k);
-                    for (int j = x.j0; j < x.j1 && ok; ++j) {
-                        const bool ahead = j + 1 < x.j1;
-                        const uint32_t v = used++;
-                        if (ahead) k = used++;
-                        const bool second = j < x.hi[1];
-                        wait_slot(v);
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (j >= x.hi[t]) continue;
-                            ok = ok && wait_on(bs, p, &bs->p_full[t], ctr[t]++, 5);
-                            if (!ok) break;
-                            ptx::tc_fence_after();
-                            pv(t, t, v, 0, j == x.j0);
-                            if (t == 1 || !second) free_slot(v);
-                            if (j + 1 == x.hi[t]) ptx::mma_commit(&bs->o_full[t]);
-                            if (j + 1 < x.hi[t]) {
-                                wait_slot(k);
-                                if (!ok) break;
-                                ptx::tc_fence_after();
-                                qk(t, t, k, 0);
-                                ptx::mma_commit(&bs->s_full[t]);
-                                if (j + 2 == x.hi[t]) ptx::mma_commit(&bs->q_free[t]);
-                            }
-                        }
-                        if (!ok) break;
-                        if (ahead) free_slot(k);
-                    }
-                } else {
-                    const auto scores = [&](int j) {
-                        const uint32_t n = ctr[1]++;
-#pragma unroll
-                        for (int h = 0; h < C::NH; ++h) {
-                            const uint32_t k = used++;
-                            wait_slot(k);
-                            if (!ok) return;
-                            ptx::tc_fence_after();
-                            qk(0, n & 1, k, h);
-                            free_slot(k);
-                        }
-                        ptx::mma_commit(&bs->s_full[n & 1]);
-                        if (j + 1 == x.j1) ptx::mma_commit(&bs->q_free[0]);
+                    // tile `me`: scores of the next block follow P V of the last,
+                    // which reads P where they go; fills K(0) V(0) K(1) V(1) ..
+                    const int mine = x.hi[me] - x.j0;
+                    if (mine > 0) ok = wait_on(bs, p, &bs->q_full[me], pieces++, 4);
+                    const auto pass = [&](uint32_t i) {   // a slot that this tile has no use for
+                        wait_slot(i);
+                        if (ok) ptx::mbar_arrive(&bs->slot_empty[i % C::NS]);
                     };
-                    scores(x.j0);
-                    for (int j = x.j0; j < x.j1 && ok; ++j) {
-                        if (j + 1 < x.j1) scores(j + 1);
+                    const auto scores = [&](int i) {
+                        const uint32_t k = filled + 2 * i;
+                        qk(me, me, k, 0);
+                        ptx::mma_commit(&bs->s_full[me]);
+                        free_slot(k);
+                        if (i + 1 == mine) ptx::mma_commit(&bs->q_free[me]);
+                    };
+                    if (ok && mine > 0) {
+                        wait_slot(filled);
+                        if (ok) scores(0);
+                    } else if (ok) {
+                        pass(filled);
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        const uint32_t v = filled + 2 * i + 1;
+                        if (i >= mine) {
+                            pass(v);
+                            if (ok && i + 1 < n) pass(v + 1);
+                            continue;
+                        }
+                        wait_slot(v);
+                        if (i + 1 < mine) wait_slot(v + 1);
+                        ok = ok && wait_on(bs, p, &bs->p_full[me], ctr++, 5);
+                        // one tile's MMAs go out together: mixed with the other's,
+                        // both tiles' softmax would wait for both (883 us of 32 heads
+                        // x 2,048 rows x 32,768 positions became 952)
+                        ok = ok && take_turn(bs, p);
                         if (!ok) break;
-                        const uint32_t n = ctr[0]++;
-                        ok = wait_on(bs, p, &bs->p_full[n & 1], n >> 1, 5);
+                        pv(me, me, v, 0, i == 0);
+                        free_slot(v);
+                        if (i + 1 == mine) ptx::mma_commit(&bs->o_full[me]);
+                        else scores(i + 1);
+                        give_turn(bs);
+                        if (i + 1 == mine && i + 1 < n) pass(v + 1);
+                    }
+                    filled += 2 * n;
+                } else if (me == 0) {
+                    // scores; fills K(0) K(1) V(0) K(2) V(1) .. V(n - 1).  A slot's
+                    // parity tells its next fill from its last only once the last
+                    // one has come.  Each issuer takes half of the fills; what it
+                    // waits for first (P V two blocks back; P of its own block)
+                    // puts the others', up to a ring's length before, behind it.
+                    ok = wait_on(bs, p, &bs->q_full[0], pieces++, 4);
+                    for (int i = 0; i < n && ok; ++i, ++ctr) {
+                        // P of two blocks before, which lies there, has been used
+                        if (ctr >= 2) ok = wait_on(bs, p, &bs->pv_done[ctr & 1], (ctr >> 1) - 1, 10);
 #pragma unroll
                         for (int h = 0; h < C::NH && ok; ++h) {
-                            const uint32_t v = used++;
-                            wait_slot(v);
+                            const uint32_t k = filled + (i == 0 ? 0 : 2 * i - 1) * C::NH + h;
+                            wait_slot(k);
                             if (!ok) break;
-                            ptx::tc_fence_after();
-                            pv(0, n & 1, v, h, j == x.j0);
-                            free_slot(v);
+                            qk(0, ctr & 1, k, h);
+                            if (h == C::NH - 1) ptx::mma_commit(&bs->s_full[ctr & 1]);
+                            free_slot(k);
                         }
-                        if (ok) ptx::mma_commit(&bs->pv_done);
-                        if (ok && j + 1 == x.j1) ptx::mma_commit(&bs->o_full[0]);
                     }
+                    if (ok) ptx::mma_commit(&bs->q_free[0]);
+                    filled += 2 * n * C::NH;
+                } else {
+                    for (int i = 0; i < n && ok; ++i, ++ctr) {
+                        const uint32_t v0 = filled + (i == n - 1 ? 2 * n - 1 : 2 * i + 2) * C::NH;
+                        ok = wait_on(bs, p, &bs->p_full[ctr & 1], ctr >> 1, 5);
+#pragma unroll
+                        for (int h = 0; h < C::NH && ok; ++h) {
+                            wait_slot(v0 + h);
+                            if (!ok) break;
+                            pv(0, ctr & 1, v0 + h, h, i == 0);
+                            if (h == C::NH - 1) ptx::mma_commit(&bs->pv_done[ctr & 1]);
+                            free_slot(v0 + h);
+                        }
+                        if (ok && i == n - 1) ptx::mma_commit(&bs->o_full[0]);
+                    }
+                    filled += 2 * n * C::NH;
                 }
             }
             // every MMA that was issued ends before the block exits
-            ptx::mma_commit(&bs->drain);
-            drain_on(&bs->drain, 0);
+            ptx::mma_commit(&bs->drain[me]);
+            drain_on(&bs->drain[me], 0);
         }
     }
     } else {
@@ -713,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                         // two tiles: the last PV into O was issued before these
                         // scores, whose end was waited for; one tile: after
                         if (!TWO) {
-                            ok = wait_on(bs, p, &bs->pv_done, ctr - 2, 9);
+                            ok = wait_on(bs, p, &bs->pv_done[ctr & 1], (ctr - 2) >> 1, 9);
                             if (!ok) return;
                             ptx::tc_fence_after();
                         }
