@@ -14,14 +14,15 @@
 // second launch joins in the order of the pieces.
 //
 // Roles in a block:
-//   warp 8   TMA producer: Q of a segment, then K and V tiles of 128 positions
-//            in halves of 128 dimensions, into a ring of shared-memory slots.
+//   warps 8, 11  TMA producers: Q of a segment, then K and V tiles of 128 positions
+//            in halves of 128 dimensions, into a ring of shared-memory slots.  Each
+//            brings 64 of the 128 dimensions: small pages take a copy for each run
+//            of rows, and a warp sets out one in some 100 cycles.
 //   warps 9, 10  MMA issuers (one thread each): S = Q K^T (128 x 128) into TMEM,
 //            O += P V with P from TMEM.  Two tiles: one issuer a tile; one tile: one
 //            for the scores, one for P V.  The queue of issued MMAs is short, and
 //            what a thread does between them (barriers, commits: half the time with
 //            one issuer) leaves the tensor pipe idle unless the other's are there.
-//   (warp 11 is idle.)
 //   warps 0-7  softmax: a thread owns a row (two tiles: of its group's tile) or
 //            half the columns of one (one tile, S then double buffered).  P
 //            overwrites S in TMEM in bf16.  A row's reference is its running
@@ -46,7 +47,7 @@ constexpr int TT = 128;
 // Three warpgroups: softmax takes registers that the third gives up.
 constexpr int kThreads = 384, kSoftmaxRegs = 200, kOtherRegs = 104;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
-constexpr int kProducerWarp = 8, kMmaWarp = 9;   // and 10
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kProducer2Warp = 11;   // issuers: 9 and 10
 constexpr int kDevTimeout = 4;          // mirrors FD_DEV_INTERNAL
 constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr float kSlack = 8.f;           // log2: how far a score may pass the reference
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         ptx::prefetch_tmap(&a.tk);
         ptx::prefetch_tmap(&a.tv);
         for (int i = 0; i < C::NS; ++i) {
-            ptx::mbar_init(&bs->slot_full[i], 1);
+            ptx::mbar_init(&bs->slot_full[i], 2);
             ptx::mbar_init(&bs->slot_empty[i], C::QT);   // two tiles: by both issuers
         }
         for (int t = 0; t < 2; ++t) {
@@ -366,8 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
 
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kProducerWarp) {
-        // ------------------------------------------------------- producer
+    if (warp == kProducerWarp || warp == kProducer2Warp) {
+        // ------------------------------------------------------ producers
+        const int part = warp == kProducerWarp ? 0 : 1;
         uint32_t fills = 0, loads[2] = {0, 0}, seen = 0;   // seen: blocks of positions
         bool ok = true;
         // rows of a block of positions: a box's page and first row, or the
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             if (x.j0 >= x.j1) continue;
 #pragma unroll
             for (int t = 0; t < C::QT; ++t) {
-                if (x.hi[t] <= x.j0 || !ok) continue;
+                if (part || x.hi[t] <= x.j0 || !ok) continue;
                 if (lane == 0) {
                     if (loads[t] > 0) ok = wait_on(bs, p, &bs->q_free[t], loads[t] - 1, 1);
                     if (ok) {
@@ -424,34 +426,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 const uint32_t slot = fills % C::NS, use = fills / C::NS;
                 if (lane == 0) {
                     ok = wait_on(bs, p, &bs->slot_empty[slot], use + 1, 2);
-                    if (ok) ptx::mbar_arrive_expect_tx(&bs->slot_full[slot], C::SLOT);
+                    if (ok) ptx::mbar_arrive_expect_tx(&bs->slot_full[slot], C::BOX);
                 }
                 ok = __shfl_sync(kAll, ok, 0);
                 if (!ok) return;
                 ++fills;
-                unsigned char *dst = smem + C::OFF_SLOTS + slot * C::SLOT;
+                unsigned char *dst = smem + C::OFF_SLOTS + slot * C::SLOT + part * C::BOX;
+                const int dim = h * 128 + part * 64;
                 if (!paged) {
                     const int y = min(j * TT, w.s.L - TT);   // the last tile ends at the length
-                    if (lane < 2)
-                        ptx::tma_load_4d(dst + lane * C::BOX, v ? &a.tv : &a.tk, &bs->slot_full[slot], h * 128 + lane * 64,
-                                         y, w.hk, w.b);
+                    if (lane == 0) ptx::tma_load_4d(dst, v ? &a.tv : &a.tk, &bs->slot_full[slot], dim, y, w.hk, w.b);
                 } else if (tiled(j)) {
                     if (lane < TT / a.prow)
-#pragma unroll
-                        for (int cb = 0; cb < 2; ++cb)
-                            ptx::tma_load_4d(dst + cb * C::BOX + lane * a.prow * 128, v ? &a.tv : &a.tk, &bs->slot_full[slot],
-                                             h * 128 + cb * 64, r.y[1], w.hk, r.y[0]);
+                        ptx::tma_load_4d(dst + lane * a.prow * 128, v ? &a.tv : &a.tk, &bs->slot_full[slot], dim, r.y[1],
+                                         w.hk, r.y[0]);
                 } else {
-#pragma unroll
-                    for (int cb = 0; cb < 2; ++cb)
-                        ptx::tma_gather4(dst + cb * C::BOX + 4 * lane * 128, v ? &a.gv : &a.gk, &bs->slot_full[slot],
-                                         h * 128 + cb * 64, r.y[0], r.y[1], r.y[2], r.y[3]);
+                    ptx::tma_gather4(dst + 4 * lane * 128, v ? &a.gv : &a.gk, &bs->slot_full[slot], dim, r.y[0], r.y[1],
+                                     r.y[2], r.y[3]);
                 }
             };
             // which of the block's positions lie on a page that the table does
             // not name, for the softmax
             const auto mark = [&](int j, const Rows &r) {
-                if (!paged) return;
+                if (!paged || part) return;
                 uint32_t *ring = reinterpret_cast<uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
                 uint32_t bad = 0;   // of positions 4 lane .. 4 lane + 3
                 if (tiled(j)) {
