@@ -28,6 +28,10 @@
 //            overwrites S in TMEM in bf16.  A row's reference is its running
 //            maximum, refreshed, and O rescaled, only where a score passes it
 //            by 2^8.
+// int8 caches (one tile): codes come by plain loads instead, through a
+// warpgroup that widens them to bf16 (exactly) in the slots; the position's K
+// scale multiplies its scores, its V scale its weights.  The others' warps 8, 9
+// and 10 are then warps 12, 13 and 14.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -44,10 +48,6 @@ namespace fd {
 namespace {
 
 constexpr int TT = 128;
-// Three warpgroups: softmax takes registers that the third gives up.
-constexpr int kThreads = 384, kSoftmaxRegs = 200, kOtherRegs = 104;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kProducer2Warp = 11;   // issuers: 9 and 10
 constexpr int kDevTimeout = 4;          // mirrors FD_DEV_INTERNAL
 constexpr uint64_t kDrainNs = 2000000000ull;
 constexpr float kSlack = 8.f;           // log2: how far a score may pass the reference
@@ -72,16 +72,27 @@ struct Bars {
     int turn;                // held by the issuer whose tile's MMAs go out
 };
 
-template <int D, bool TWO>
+template <int D, bool TWO, bool I8>
 struct Cfg {
-    static_assert(!TWO || D == 128, "two tiles' O and S fill TMEM at head_dim 128");
+    static_assert(!TWO || (D == 128 && !I8), "two tiles' O and S fill TMEM at head_dim 128");
+    // Warpgroups of softmax (two), of widening where codes are int8, and of the
+    // producers and issuers; softmax takes registers that the others give up.
+    static constexpr int THREADS = I8 ? 512 : 384;
+    static constexpr int LAUNCH_REGS = I8 ? 128 : 168, SOFTMAX_REGS = I8 ? 160 : 200, WIDEN_REGS = I8 ? 112 : 0,
+                         OTHER_REGS = I8 ? 80 : 104;
+    static_assert(256 * SOFTMAX_REGS + 128 * (WIDEN_REGS + OTHER_REGS) <= THREADS * LAUNCH_REGS, "registers of the launch");
+    static constexpr int PRODUCER = I8 ? 12 : 8, PRODUCER2 = I8 ? -1 : 11, ISSUER = PRODUCER + 1;   // warps; issuers: two
     static constexpr int NH = D / 128, QT = TWO ? 2 : 1;
     static constexpr uint32_t BOX = TT * 128;        // 128 rows x 64 numbers
     static constexpr uint32_t SLOT = 2 * BOX;        // 128 rows x 128 numbers
     static constexpr uint32_t QTILE = NH * SLOT;
     static constexpr uint32_t OFF_RED = 512;         // [2][2][128] floats
     static constexpr uint32_t OFF_BAD = OFF_RED + 2048;   // [8][8] words
-    static constexpr uint32_t OFF_Q = (OFF_BAD + 256 + 1023) / 1024 * 1024;
+    // int8: of the last eight blocks of positions, the scales, and of the last four
+    // where their rows of K and V start (elements; -1: nowhere)
+    static constexpr uint32_t OFF_SCALES = OFF_BAD + 256;             // [8][2][128] floats
+    static constexpr uint32_t OFF_ROWS = OFF_SCALES + (I8 ? 8192 : 0);   // [4][2][128] int64
+    static constexpr uint32_t OFF_Q = (OFF_ROWS + (I8 ? 8192 : 0) + 1023) / 1024 * 1024;
     static constexpr uint32_t BUDGET = 232448;
     static constexpr int NS = (int)((BUDGET - OFF_Q - QT * QTILE) / SLOT);
     static_assert(NS >= 4 && NS <= 8, "ring");
@@ -313,10 +324,128 @@ __device__ __forceinline__ bool row_at(const PfArgs &a, const Walk &w, int t, in
     return row < a.R && token < w.s.fresh;
 }
 
+// ---------------------------------------------------------------- widening
+// Four int8 codes (the bytes of w) -> four bf16 numbers, exactly: with c's low
+// seven bits as the mantissa of 128 + (c & 127), less 128, or 256 where c's sign
+// bit is set.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
+    const uint32_t lo = __byte_perm(w, 0x43434343u, 0x4140), hi = __byte_perm(w, 0x43434343u, 0x4342);
+    uint2 r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(lo & 0xff7fff7fu), "r"(lo & 0xff80ff80u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(hi & 0xff7fff7fu), "r"(hi & 0xff80ff80u));
+    return r;
+}
+
+// The widening warpgroup (128 threads): K and V of the share's blocks of positions,
+// in the order of the one-tile issuers, as bf16 in the slots' 128-byte swizzle.  A
+// thread takes 16 of a row's 128 codes, of every 16th row; the next fill's codes
+// are loaded before the last one's are widened.
+template <int D>
+__device__ __forceinline__ void widen_role(const PfArgs &a, Bars *bs, unsigned char *smem, Walk w, bool has) {
+    using C = Cfg<D, false, true>;
+    const PrefillParams &p = a.p;
+    const int tid = (int)threadIdx.x - 256, S = a.T;
+    const int chunk = tid & 7, row0 = tid >> 3;              // rows row0 + 16 i
+    int64_t *rows = reinterpret_cast<int64_t *>(smem + C::OFF_ROWS);
+    uint32_t fills = 0, seen = 0;
+    bool ok = true;
+    uint4 next[8];
+    // the group's threads agree on whether to go on
+    const auto agree = [&]() {
+        int all;
+        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                     : "=r"(all) : "r"((int)ok) : "memory");
+        ok = all != 0;
+    };
+    for (bool more = has; more && ok; more = w.next(p, S)) {
+        const Piece x = piece_of<1>(a, w);
+        const int n = x.j1 - x.j0;
+        if (n <= 0) continue;
+        // where position tid of block i (of the piece) lies, and its scales
+        const auto look = [&](int i) {
+            const int pos = (x.j0 + i) * TT + tid, slot = (seen + i) & 3;
+            int64_t lead = w.b, row = pos;
+            bool there = pos < w.s.L;
+            bool hole = false;
+            if (there && p.c.block_table) {
+                const int32_t at = p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size;
+                lead = __ldg(p.c.block_table + (int64_t)w.b * p.c.max_pages + at);
+                row = pos - at * p.c.page_size;
+                hole = lead < 0 || lead >= p.c.lead;
+                if (hole) atomicOr(p.status, kDevBadIndex);
+                there = !hole;
+            }
+            rows[slot * 256 + tid] = there ? lead * p.c.ks[0] + w.hk * p.c.ks[1] + row * p.c.ks[2] : -1;
+            rows[slot * 256 + 128 + tid] = there ? lead * p.c.vs[0] + w.hk * p.c.vs[1] + row * p.c.vs[2] : -1;
+            float *scales = reinterpret_cast<float *>(smem + C::OFF_SCALES + ((seen + i) & 7) * 1024);
+            scales[tid] = there ? __ldg(p.c.k_scale + lead * p.c.kss[0] + w.hk * p.c.kss[1] + row * p.c.kss[2]) : 0.f;
+            scales[128 + tid] = there ? __ldg(p.c.v_scale + lead * p.c.vss[0] + w.hk * p.c.vss[1] + row * p.c.vss[2]) : 0.f;
+            const unsigned word = __ballot_sync(kAll, hole);
+            if ((tid & 31) == 0) reinterpret_cast<uint32_t *>(smem + C::OFF_BAD)[((seen + i) & 7) * 8 + 1 + (tid >> 5)] = word;
+        };
+        // the codes of one half of K or V of block i
+        const auto load = [&](int i, int h, bool v) {
+            const int64_t *at = rows + ((seen + i) & 3) * 256 + (v ? 128 : 0) + row0;
+            const char *src = static_cast<const char *>(v ? p.c.v : p.c.k) + h * 128 + chunk * 16;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t off = at[16 * e];
+                next[e] = make_uint4(0, 0, 0, 0);
+                if (off >= 0) next[e] = ldg_stream(src + off);
+            }
+        };
+        const auto store = [&](const uint4 *codes) {
+            const uint32_t slot = fills % C::NS, use = fills / C::NS;
+            ok = ok && wait_on(bs, p, &bs->slot_empty[slot], use + 1, 2);
+            ++fills;
+            if (!ok) return;
+            unsigned char *dst = smem + C::OFF_SLOTS + slot * C::SLOT + (chunk >> 2) * C::BOX;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int r = row0 + 16 * e, c0 = (chunk & 3) * 2;
+                const uint2 q0 = widen4(codes[e].x), q1 = widen4(codes[e].y), q2 = widen4(codes[e].z), q3 = widen4(codes[e].w);
+                const uint4 first = make_uint4(q0.x, q0.y, q1.x, q1.y), second = make_uint4(q2.x, q2.y, q3.x, q3.y);
+                // (lanes of the other box take the other chunk first: no bank twice)
+                const bool turn = chunk >= 4;
+                *reinterpret_cast<uint4 *>(dst + r * 128 + (((c0 + turn) ^ (r & 7)) * 16)) = turn ? second : first;
+                *reinterpret_cast<uint4 *>(dst + r * 128 + (((c0 + !turn) ^ (r & 7)) * 16)) = turn ? first : second;
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(&bs->slot_full[slot]);
+        };
+        look(0);
+        agree();
+        if (!ok) break;
+        load(0, 0, false);
+        // fills in order: K(0), K(1), V(0), K(2), V(1) .. V(n - 1), NH halves each
+        for (int f = 0; f < 2 * n; ++f) {
+            const bool v = f == 2 * n - 1 || (f > 0 && (f & 1) == 0);
+            const int i = f == 0 ? 0 : f == 2 * n - 1 ? n - 1 : v ? f / 2 - 1 : (f + 1) / 2;
+            const int g = f + 1;                              // the next
+            const bool gv = g == 2 * n - 1 || (g & 1) == 0;
+            const int gi = g == 2 * n - 1 ? n - 1 : gv ? g / 2 - 1 : (g + 1) / 2;
+            if (g < 2 * n && !gv) look(gi);
+            agree();                                          // (and the rows that were written are there)
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < C::NH; ++h) {
+                uint4 codes[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) codes[e] = next[e];
+                if (h + 1 < C::NH) load(i, h + 1, v);
+                else if (g < 2 * n) load(gi, 0, gv);
+                store(codes);
+            }
+        }
+        agree();
+        seen += n;
+    }
+}
+
 // ------------------------------------------------------------------ kernel
-template <int D, bool TWO>
-__global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_constant__ PfArgs a) {
-    using C = Cfg<D, TWO>;
+template <int D, bool TWO, bool I8>
+__global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel(const __grid_constant__ PfArgs a) {
+    using C = Cfg<D, TWO, I8>;
     const PrefillParams &p = a.p;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = ptx::smem_u32(smem);
@@ -326,12 +455,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         if (tid == 0) atomicOr(p.status, kDevTimeout);
         return;
     }
-    if (warp == kProducerWarp && lane == 0) {
+    if (warp == C::PRODUCER && lane == 0) {
         ptx::prefetch_tmap(&a.tq);
-        ptx::prefetch_tmap(&a.tk);
-        ptx::prefetch_tmap(&a.tv);
+        if (!I8) {
+            ptx::prefetch_tmap(&a.tk);
+            ptx::prefetch_tmap(&a.tv);
+        }
         for (int i = 0; i < C::NS; ++i) {
-            ptx::mbar_init(&bs->slot_full[i], 2);
+            ptx::mbar_init(&bs->slot_full[i], I8 ? 128 : 2);
             ptx::mbar_init(&bs->slot_empty[i], C::QT);   // two tiles: by both issuers
         }
         for (int t = 0; t < 2; ++t) {
@@ -348,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         bs->turn = 0;
         ptx::mbar_fence_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == C::ISSUER) {
         ptx::tmem_alloc(&bs->tmem_base, 512);
         ptx::tmem_relinquish();
     }
@@ -356,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     Walk w;
     bool has;
     {
-        const Total total = total_of(p, S, gridDim.x, warp == kProducerWarp && blockIdx.x == 0);
+        const Total total = total_of(p, S, gridDim.x, warp == C::PRODUCER && blockIdx.x == 0);
         has = (int)blockIdx.x < total.G && total.units > 0;
         if (has) w.seek(p, S, total.split().start(blockIdx.x), total.split().start(blockIdx.x + 1));
     }
@@ -365,11 +496,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     ptx::tc_fence_after();
     const uint32_t tmem = bs->tmem_base;
 
-    if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kProducerWarp || warp == kProducer2Warp) {
+    if (I8 && warp >= 8 && warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(I8 ? C::WIDEN_REGS : 24));
+        if constexpr (I8) widen_role<D>(a, bs, smem, w, has);
+    } else if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
+    if (warp == C::PRODUCER || warp == C::PRODUCER2) {
         // ------------------------------------------------------ producers
-        const int part = warp == kProducerWarp ? 0 : 1;
+        const int part = warp == C::PRODUCER ? 0 : 1;
         uint32_t fills = 0, loads[2] = {0, 0}, seen = 0;   // seen: blocks of positions
         bool ok = true;
         // rows of a block of positions: a box's page and first row, or the
@@ -396,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 }
                 ok = __shfl_sync(kAll, ok, 0);
             }
+            if (I8) continue;      // (Q only)
             const auto tiled = [&](int j) { return !paged || (a.prow > 0 && (int64_t)(j + 1) * TT <= w.s.L); };
             const auto look = [&](int j) {
                 Rows r{{-1, -1, -1, -1}};
@@ -502,10 +637,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         if (lane == 0)
             for (int t = 0; t < C::QT; ++t)
                 if (loads[t] > 0) drain_on(&bs->q_full[t], (loads[t] - 1) & 1);
-    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    } else if (warp == C::ISSUER || warp == C::ISSUER + 1) {
         // --------------------------------------------------------- issuers
         if (lane == 0) {
-            const int me = warp - kMmaWarp;
+            const int me = warp - C::ISSUER;
             bool ok = true;
             uint32_t filled = 0;             // slots of the pieces before
             uint32_t pieces = 0, ctr = 0;
@@ -629,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     }
     } else {
         // --------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
         const int group = warp >> 2, row = (warp & 3) * 32 + lane;
         const int t = TWO ? group : 0;                  // tile
         const int col0 = TWO ? 0 : group * 64;          // first score column
@@ -676,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 // 32 score columns from c on, hidden ones as -inf
                 const auto hide = [&](float *s, int c) {
                     const int pos0 = j * TT;
-                    const int at = p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
+                    const int at = I8 || p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
                     // of these columns the row sees lo .. hi - 1, less those on no page
                     const int lo = min(max(pos0 - at - col0 - c, 0), 32), hi = min(max(last + 1 - at - col0 - c, 0), 32);
                     uint32_t sees = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
@@ -713,6 +848,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 ptx::tmem_ld32(s_at + col0, s);
                 ptx::tmem_ld32(s_at + col0 + 32, s + 32);
                 ptx::tmem_wait_ld();
+                const float4 *scales = reinterpret_cast<const float4 *>(smem + C::OFF_SCALES + ((seen + j - x.j0) & 7) * 1024 + col0 * 4);
+                if (I8) {
+#pragma unroll
+                    for (int e = 0; e < 64; e += 4) {
+                        const float4 k = scales[e / 4];
+                        s[e] *= k.x;
+                        s[e + 1] *= k.y;
+                        s[e + 2] *= k.z;
+                        s[e + 3] *= k.w;
+                    }
+                }
                 if (MASK) {
                     hide(s, 0);
                     hide(s + 32, 32);
@@ -763,8 +909,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                         const float p0 = fast_exp2(u.x), p1 = fast_exp2(u.y), p2 = fast_exp2(v.x), p3 = fast_exp2(v.y);
                         sum0 = add2(sum0, pair(p0, p1));
                         sum1 = add2(sum1, pair(p2, p3));
-                        word[e / 2] = pack_bf16x2(p0, p1);
-                        word[e / 2 + 1] = pack_bf16x2(p2, p3);
+                        if (I8) {
+                            // (the scale of a position that is hidden may be a NaN)
+                            const float4 y = scales[32 + (c + e) / 4];
+                            const auto times = [&](float weight, float by, float score) {
+                                return MASK && score == neg_inf() ? 0.f : weight * by;
+                            };
+                            word[e / 2] = pack_bf16x2(times(p0, y.x, s[e]), times(p1, y.y, s[e + 1]));
+                            word[e / 2 + 1] = pack_bf16x2(times(p2, y.z, s[e + 2]), times(p3, y.w, s[e + 3]));
+                        } else {
+                            word[e / 2] = pack_bf16x2(p0, p1);
+                            word[e / 2 + 1] = pack_bf16x2(p2, p3);
+                        }
                     }
                     ptx::tmem_st16(s_at + (col0 + c) / 2, word);
                 };
@@ -792,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const volatile uint32_t *bad = reinterpret_cast<const volatile uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
-                const bool holes = p.c.block_table && bad[0] != 0;
+                const bool holes = p.c.block_table && (I8 ? (bad[1] | bad[2] | bad[3] | bad[4]) : bad[0]) != 0;
                 if (j < plain && !holes) block(j, buf, bad, holes, std::false_type());
                 else block(j, buf, bad, holes, std::true_type());
             }
@@ -863,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+    if (warp == C::ISSUER) ptx::tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------- join
@@ -874,7 +1030,7 @@ constexpr int kJoinParts = 4, kJoinThreads = 256;
 
 template <int D, bool TWO>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__ PfArgs a, int grid) {
-    using C = Cfg<D, TWO>;
+    using C = Cfg<D, TWO, false>;
     const PrefillParams &p = a.p;
     const int c = blockIdx.x + 1;
     const int S = C::QT * a.T;
@@ -961,12 +1117,12 @@ int box_rows(const KvCache &c) {
     return c.page_size >= 8 && c.page_size < TT && TT % c.page_size == 0 ? c.page_size : 0;
 }
 
-template <int D, bool TWO>
+template <int D, bool TWO, bool I8>
 int launch(const PfArgs &a, int grid, cudaStream_t st) {
-    using C = Cfg<D, TWO>;
-    if (cudaFuncSetAttribute(prefill_tc_kernel<D, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
+    using C = Cfg<D, TWO, I8>;
+    if (cudaFuncSetAttribute(prefill_tc_kernel<D, TWO, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
         return -5;
-    prefill_tc_kernel<D, TWO><<<grid, kThreads, C::SMEM, st>>>(a);
+    prefill_tc_kernel<D, TWO, I8><<<grid, C::THREADS, C::SMEM, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return -5;
     if (grid > 1) prefill_join_kernel<D, TWO><<<dim3(grid - 1, kJoinParts), kJoinThreads, 0, st>>>(a, grid);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
@@ -975,11 +1131,11 @@ int launch(const PfArgs &a, int grid, cudaStream_t st) {
 }  // namespace
 
 // Two tiles hold 256 rows' partial sums at head_dim 128, one 128 at 256.
-int64_t prefill_slot_floats(int d) { return d == 128 ? Cfg<128, true>::SLOT_FLOATS : Cfg<256, false>::SLOT_FLOATS; }
+int64_t prefill_slot_floats(int d) { return d == 128 ? Cfg<128, true, false>::SLOT_FLOATS : Cfg<256, false, false>::SLOT_FLOATS; }
 
 bool prefill_tc_supports(const PrefillParams &p) {
     int64_t rs, rows, g[3];
-    return !p.c.int8 && p.scale_log2 > 0.f && (!p.c.block_table || pool_rows(p.c, &rs, &rows, g));
+    return p.scale_log2 > 0.f && (p.c.int8 || !p.c.block_table || pool_rows(p.c, &rs, &rows, g));
 }
 
 int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
@@ -996,6 +1152,7 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
         const cuuint32_t box[4] = {64, (cuuint32_t)p.g, (cuuint32_t)a.T, 1};
         if (!encode(&a.tq, 4, p.q, dims, strides, box)) return -2;
     }
+    if (p.c.int8) return p.c.d == 128 ? launch<128, false, true>(a, grid, st) : launch<256, false, true>(a, grid, st);
     const void *caches[2] = {p.c.k, p.c.v};
     const int64_t *strides_of[2] = {p.c.ks, p.c.vs};
     for (int i = 0; i < 2; ++i) {
@@ -1017,9 +1174,9 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
         }
     }
     if (a.prow == 0) { a.tk = a.gk; a.tv = a.gv; }   // (unused)
-    if (p.c.d == 256) return launch<256, false>(a, grid, st);
-    if ((int64_t)p.n > a.T) return launch<128, true>(a, grid, st);
-    return launch<128, false>(a, grid, st);
+    if (p.c.d == 256) return launch<256, false, false>(a, grid, st);
+    if ((int64_t)p.n > a.T) return launch<128, true, false>(a, grid, st);
+    return launch<128, false, false>(a, grid, st);
 }
 
 }  // namespace fd
