@@ -28,10 +28,10 @@
 //            overwrites S in TMEM in bf16.  A row's reference is its running
 //            maximum, refreshed, and O rescaled, only where a score passes it
 //            by 2^8.
-// int8 caches (one tile): codes come by plain loads instead, through a
-// warpgroup that widens them to bf16 (exactly) in the slots; the position's K
-// scale multiplies its scores, its V scale its weights.  The others' warps 8, 9
-// and 10 are then warps 12, 13 and 14.
+// int8 caches: codes are copied into the second half of their slot, and
+// warps 8-11 widen them in place to bf16 (exactly); the position's K scale
+// multiplies its scores, its V scale its weights.  The producer is then warp 12,
+// the issuers 13 and 14.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -64,7 +64,7 @@ struct PfArgs {
 };
 
 struct Bars {
-    uint64_t slot_full[8], slot_empty[8];
+    uint64_t slot_full[8], slot_empty[8], raw_full[8];   // raw: int8 codes
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
     uint64_t cross, pv_done[2], drain[2];
     uint32_t tmem_base;
@@ -74,12 +74,12 @@ struct Bars {
 
 template <int D, bool TWO, bool I8>
 struct Cfg {
-    static_assert(!TWO || (D == 128 && !I8), "two tiles' O and S fill TMEM at head_dim 128");
+    static_assert(!TWO || D == 128, "two tiles' O and S fill TMEM at head_dim 128");
     // Warpgroups of softmax (two), of widening where codes are int8, and of the
     // producers and issuers; softmax takes registers that the others give up.
     static constexpr int THREADS = I8 ? 512 : 384;
-    static constexpr int LAUNCH_REGS = I8 ? 128 : 168, SOFTMAX_REGS = I8 ? 160 : 200, WIDEN_REGS = I8 ? 112 : 0,
-                         OTHER_REGS = I8 ? 80 : 104;
+    static constexpr int LAUNCH_REGS = I8 ? 128 : 168, SOFTMAX_REGS = I8 ? 184 : 200, WIDEN_REGS = I8 ? 72 : 0,
+                         OTHER_REGS = I8 ? 72 : 104;
     static_assert(256 * SOFTMAX_REGS + 128 * (WIDEN_REGS + OTHER_REGS) <= THREADS * LAUNCH_REGS, "registers of the launch");
     static constexpr int PRODUCER = I8 ? 12 : 8, PRODUCER2 = I8 ? -1 : 11, ISSUER = PRODUCER + 1;   // warps; issuers: two
     static constexpr int NH = D / 128, QT = TWO ? 2 : 1;
@@ -88,11 +88,8 @@ struct Cfg {
     static constexpr uint32_t QTILE = NH * SLOT;
     static constexpr uint32_t OFF_RED = 512;         // [2][2][128] floats
     static constexpr uint32_t OFF_BAD = OFF_RED + 2048;   // [8][8] words
-    // int8: of the last eight blocks of positions, the scales, and of the last four
-    // where their rows of K and V start (elements; -1: nowhere)
-    static constexpr uint32_t OFF_SCALES = OFF_BAD + 256;             // [8][2][128] floats
-    static constexpr uint32_t OFF_ROWS = OFF_SCALES + (I8 ? 8192 : 0);   // [4][2][128] int64
-    static constexpr uint32_t OFF_Q = (OFF_ROWS + (I8 ? 8192 : 0) + 1023) / 1024 * 1024;
+    static constexpr uint32_t OFF_SCALES = OFF_BAD + 256;   // int8: [8][2][128] floats
+    static constexpr uint32_t OFF_Q = (OFF_SCALES + (I8 ? 8192 : 0) + 1023) / 1024 * 1024;
     static constexpr uint32_t BUDGET = 232448;
     static constexpr int NS = (int)((BUDGET - OFF_Q - QT * QTILE) / SLOT);
     static_assert(NS >= 4 && NS <= 8, "ring");
@@ -304,6 +301,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -336,108 +338,89 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
     return r;
 }
 
-// The widening warpgroup (128 threads): K and V of the share's blocks of positions,
-// in the order of the one-tile issuers, as bf16 in the slots' 128-byte swizzle.  A
-// thread takes 16 of a row's 128 codes, of every 16th row; the next fill's codes
-// are loaded before the last one's are widened.
-template <int D>
+// One warp of the widening warpgroup: its 32 rows of every fill, in place.  A thread
+// takes 16 of a row's 128 codes, of every fourth row, all of them into registers
+// before the warp writes; it also brings the scales of position tid of each block,
+// which are loaded a block before they are wanted.
+template <int D, bool TWO>
 __device__ __forceinline__ void widen_role(const PfArgs &a, Bars *bs, unsigned char *smem, Walk w, bool has) {
-    using C = Cfg<D, false, true>;
+    using C = Cfg<D, TWO, true>;
     const PrefillParams &p = a.p;
-    const int tid = (int)threadIdx.x - 256, S = a.T;
-    const int chunk = tid & 7, row0 = tid >> 3;              // rows row0 + 16 i
-    int64_t *rows = reinterpret_cast<int64_t *>(smem + C::OFF_ROWS);
+    const int tid = (int)threadIdx.x - 256, S = C::QT * a.T;
+    const int chunk = tid & 7, row0 = (tid & ~31) + ((tid & 31) >> 3);   // rows row0 + 4 e
     uint32_t fills = 0, seen = 0;
     bool ok = true;
-    uint4 next[8];
-    // the group's threads agree on whether to go on
-    const auto agree = [&]() {
-        int all;
-        asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                     : "=r"(all) : "r"((int)ok) : "memory");
-        ok = all != 0;
-    };
     for (bool more = has; more && ok; more = w.next(p, S)) {
-        const Piece x = piece_of<1>(a, w);
+        const Piece x = piece_of<C::QT>(a, w);
         const int n = x.j1 - x.j0;
         if (n <= 0) continue;
-        // where position tid of block i (of the piece) lies, and its scales
-        const auto look = [&](int i) {
-            const int pos = (x.j0 + i) * TT + tid, slot = (seen + i) & 3;
-            int64_t lead = w.b, row = pos;
-            bool there = pos < w.s.L;
-            bool hole = false;
-            if (there && p.c.block_table) {
-                const int32_t at = p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size;
-                lead = __ldg(p.c.block_table + (int64_t)w.b * p.c.max_pages + at);
-                row = pos - at * p.c.page_size;
-                hole = lead < 0 || lead >= p.c.lead;
-                if (hole) atomicOr(p.status, kDevBadIndex);
-                there = !hole;
-            }
-            rows[slot * 256 + tid] = there ? lead * p.c.ks[0] + w.hk * p.c.ks[1] + row * p.c.ks[2] : -1;
-            rows[slot * 256 + 128 + tid] = there ? lead * p.c.vs[0] + w.hk * p.c.vs[1] + row * p.c.vs[2] : -1;
-            float *scales = reinterpret_cast<float *>(smem + C::OFF_SCALES + ((seen + i) & 7) * 1024);
-            scales[tid] = there ? __ldg(p.c.k_scale + lead * p.c.kss[0] + w.hk * p.c.kss[1] + row * p.c.kss[2]) : 0.f;
-            scales[128 + tid] = there ? __ldg(p.c.v_scale + lead * p.c.vss[0] + w.hk * p.c.vss[1] + row * p.c.vss[2]) : 0.f;
-            const unsigned word = __ballot_sync(kAll, hole);
-            if ((tid & 31) == 0) reinterpret_cast<uint32_t *>(smem + C::OFF_BAD)[((seen + i) & 7) * 8 + 1 + (tid >> 5)] = word;
+        // what column tid of block i of the piece stands for: its page, and its scales
+        const auto position = [&](int i) {
+            const int pos0 = (x.j0 + i) * TT;
+            return (p.c.block_table ? pos0 : min(pos0, w.s.L - TT)) + tid;
         };
-        // the codes of one half of K or V of block i
-        const auto load = [&](int i, int h, bool v) {
-            const int64_t *at = rows + ((seen + i) & 3) * 256 + (v ? 128 : 0) + row0;
-            const char *src = static_cast<const char *>(v ? p.c.v : p.c.k) + h * 128 + chunk * 16;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int64_t off = at[16 * e];
-                next[e] = make_uint4(0, 0, 0, 0);
-                if (off >= 0) next[e] = ldg_stream(src + off);
-            }
+        const auto lead_of = [&](int i) {
+            const int pos = position(i);
+            if (i >= n || pos < 0 || pos >= w.s.L) return -1;
+            if (!p.c.block_table) return w.b;
+            const int e = __ldg(p.c.block_table + (int64_t)w.b * p.c.max_pages +
+                                (p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size));
+            return e < p.c.lead ? e : -1;
         };
-        const auto store = [&](const uint4 *codes) {
-            const uint32_t slot = fills % C::NS, use = fills / C::NS;
-            ok = ok && wait_on(bs, p, &bs->slot_empty[slot], use + 1, 2);
-            ++fills;
-            if (!ok) return;
-            unsigned char *dst = smem + C::OFF_SLOTS + slot * C::SLOT + (chunk >> 2) * C::BOX;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int r = row0 + 16 * e, c0 = (chunk & 3) * 2;
-                const uint2 q0 = widen4(codes[e].x), q1 = widen4(codes[e].y), q2 = widen4(codes[e].z), q3 = widen4(codes[e].w);
-                const uint4 first = make_uint4(q0.x, q0.y, q1.x, q1.y), second = make_uint4(q2.x, q2.y, q3.x, q3.y);
-                // (lanes of the other box take the other chunk first: no bank twice)
-                const bool turn = chunk >= 4;
-                *reinterpret_cast<uint4 *>(dst + r * 128 + (((c0 + turn) ^ (r & 7)) * 16)) = turn ? second : first;
-                *reinterpret_cast<uint4 *>(dst + r * 128 + (((c0 + !turn) ^ (r & 7)) * 16)) = turn ? first : second;
-            }
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(&bs->slot_full[slot]);
+        float k_scale = 0.f, v_scale = 0.f;
+        const auto bring = [&](int i, int lead) {
+            k_scale = v_scale = 0.f;
+            if (lead < 0) return;
+            const int pos = position(i);
+            const int64_t row = !p.c.block_table ? pos : p.c.page_shift >= 0 ? pos & (p.c.page_size - 1) : pos % p.c.page_size;
+            k_scale = __ldg(p.c.k_scale + lead * p.c.kss[0] + w.hk * p.c.kss[1] + row * p.c.kss[2]);
+            v_scale = __ldg(p.c.v_scale + lead * p.c.vss[0] + w.hk * p.c.vss[1] + row * p.c.vss[2]);
         };
-        look(0);
-        agree();
-        if (!ok) break;
-        load(0, 0, false);
-        // fills in order: K(0), K(1), V(0), K(2), V(1) .. V(n - 1), NH halves each
-        for (int f = 0; f < 2 * n; ++f) {
-            const bool v = f == 2 * n - 1 || (f > 0 && (f & 1) == 0);
-            const int i = f == 0 ? 0 : f == 2 * n - 1 ? n - 1 : v ? f / 2 - 1 : (f + 1) / 2;
-            const int g = f + 1;                              // the next
-            const bool gv = g == 2 * n - 1 || (g & 1) == 0;
-            const int gi = g == 2 * n - 1 ? n - 1 : gv ? g / 2 - 1 : (g + 1) / 2;
-            if (g < 2 * n && !gv) look(gi);
-            agree();                                          // (and the rows that were written are there)
-            if (!ok) break;
-#pragma unroll
+        bring(0, lead_of(0));
+        int lead = lead_of(1);
+        // fills: K(0), K(1), V(0), K(2), V(1) .. V(n - 1), NH halves each; two tiles:
+        // K(0), V(0), K(1), V(1) ..
+        int i = 0;                                             // the next block of K
+        for (int g = 0; g < 2 * n && ok; ++g) {
+            const bool k = TWO ? (g & 1) == 0 : g == 0 || ((g & 1) == 1 && g != 2 * n - 1);
+            if (k) {
+                float *to = reinterpret_cast<float *>(smem + C::OFF_SCALES + ((seen + i) & 7) * 1024);
+                to[tid] = k_scale;
+                to[128 + tid] = v_scale;
+                ++i;
+                bring(i, lead);
+                lead = lead_of(i + 1);
+            }
             for (int h = 0; h < C::NH; ++h) {
+                const uint32_t slot = fills % C::NS, use = fills / C::NS;
+                ok = wait_on(bs, p, &bs->raw_full[slot], use, 11);
+                ok = __all_sync(kAll, ok);
+                if (!ok) break;
+                ++fills;
+                unsigned char *const box = smem + C::OFF_SLOTS + slot * C::SLOT;
                 uint4 codes[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) codes[e] = next[e];
-                if (h + 1 < C::NH) load(i, h + 1, v);
-                else if (g < 2 * n) load(gi, 0, gv);
-                store(codes);
+                for (int e = 0; e < 8; ++e) {
+                    const int r = row0 + 4 * e;
+                    codes[e] = *reinterpret_cast<const uint4 *>(box + C::BOX + r * 128 + ((chunk ^ (r & 7)) * 16));
+                }
+                __syncwarp();
+                unsigned char *const dst = box + (chunk >> 2) * C::BOX;
+                const int c0 = (chunk & 3) * 2;
+                // (lanes of the other box take the other chunk first: no bank twice)
+                const int turn = chunk >> 2;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int r = row0 + 4 * e;
+                    const uint2 q0 = widen4(codes[e].x), q1 = widen4(codes[e].y), q2 = widen4(codes[e].z), q3 = widen4(codes[e].w);
+                    const uint4 first = make_uint4(q0.x, q0.y, q1.x, q1.y), second = make_uint4(q2.x, q2.y, q3.x, q3.y);
+                    *reinterpret_cast<uint4 *>(dst + r * 128 + (((c0 + turn) ^ (r & 7)) * 16)) = turn ? second : first;
+                    *reinterpret_cast<uint4 *>(dst + r * 128 + (((c0 + 1 - turn) ^ (r & 7)) * 16)) = turn ? first : second;
+                }
+                ptx::fence_proxy_async_smem();
+                ptx::mbar_arrive(&bs->slot_full[slot]);
             }
         }
-        agree();
         seen += n;
     }
 }
@@ -457,12 +440,11 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
     }
     if (warp == C::PRODUCER && lane == 0) {
         ptx::prefetch_tmap(&a.tq);
-        if (!I8) {
-            ptx::prefetch_tmap(&a.tk);
-            ptx::prefetch_tmap(&a.tv);
-        }
+        ptx::prefetch_tmap(&a.tk);
+        ptx::prefetch_tmap(&a.tv);
         for (int i = 0; i < C::NS; ++i) {
             ptx::mbar_init(&bs->slot_full[i], I8 ? 128 : 2);
+            ptx::mbar_init(&bs->raw_full[i], 1);
             ptx::mbar_init(&bs->slot_empty[i], C::QT);   // two tiles: by both issuers
         }
         for (int t = 0; t < 2; ++t) {
@@ -498,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
 
     if (I8 && warp >= 8 && warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(I8 ? C::WIDEN_REGS : 24));
-        if constexpr (I8) widen_role<D>(a, bs, smem, w, has);
+        if constexpr (I8) widen_role<D, TWO>(a, bs, smem, w, has);
     } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == C::PRODUCER || warp == C::PRODUCER2) {
@@ -530,7 +512,6 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 }
                 ok = __shfl_sync(kAll, ok, 0);
             }
-            if (I8) continue;      // (Q only)
             const auto tiled = [&](int j) { return !paged || (a.prow > 0 && (int64_t)(j + 1) * TT <= w.s.L); };
             const auto look = [&](int j) {
                 Rows r{{-1, -1, -1, -1}};
@@ -559,24 +540,26 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
             // one half of K or V of block j
             const auto fill = [&](int j, int h, bool v, const Rows &r) {
                 const uint32_t slot = fills % C::NS, use = fills / C::NS;
+                uint64_t *const full = I8 ? &bs->raw_full[slot] : &bs->slot_full[slot];
                 if (lane == 0) {
                     ok = wait_on(bs, p, &bs->slot_empty[slot], use + 1, 2);
-                    if (ok) ptx::mbar_arrive_expect_tx(&bs->slot_full[slot], C::BOX);
+                    if (ok) ptx::mbar_arrive_expect_tx(full, C::BOX);
                 }
                 ok = __shfl_sync(kAll, ok, 0);
                 if (!ok) return;
                 ++fills;
-                unsigned char *dst = smem + C::OFF_SLOTS + slot * C::SLOT + part * C::BOX;
-                const int dim = h * 128 + part * 64;
+                // (codes as pairs, into the second half)
+                unsigned char *dst = smem + C::OFF_SLOTS + slot * C::SLOT + (I8 ? 1 : part) * C::BOX;
+                const int dim = I8 ? h * 64 : h * 128 + part * 64;
                 if (!paged) {
                     const int y = min(j * TT, w.s.L - TT);   // the last tile ends at the length
-                    if (lane == 0) ptx::tma_load_4d(dst, v ? &a.tv : &a.tk, &bs->slot_full[slot], dim, y, w.hk, w.b);
+                    if (lane == 0) ptx::tma_load_4d(dst, v ? &a.tv : &a.tk, full, dim, y, w.hk, w.b);
                 } else if (tiled(j)) {
                     if (lane < TT / a.prow)
-                        ptx::tma_load_4d(dst + lane * a.prow * 128, v ? &a.tv : &a.tk, &bs->slot_full[slot], dim, r.y[1],
+                        ptx::tma_load_4d(dst + lane * a.prow * 128, v ? &a.tv : &a.tk, full, dim, r.y[1],
                                          w.hk, r.y[0]);
                 } else {
-                    ptx::tma_gather4(dst + 4 * lane * 128, v ? &a.gv : &a.gk, &bs->slot_full[slot], dim, r.y[0], r.y[1],
+                    ptx::tma_gather4(dst + 4 * lane * 128, v ? &a.gv : &a.gk, full, dim, r.y[0], r.y[1],
                                      r.y[2], r.y[3]);
                 }
             };
@@ -633,7 +616,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
         // every copy that was issued lands before the block exits
         if (lane == 0)
             for (uint32_t i = fills > C::NS ? fills - C::NS : 0; i < fills; ++i)
-                drain_on(&bs->slot_full[i % C::NS], (i / C::NS) & 1);
+                drain_on(I8 ? &bs->raw_full[i % C::NS] : &bs->slot_full[i % C::NS], (i / C::NS) & 1);
         if (lane == 0)
             for (int t = 0; t < C::QT; ++t)
                 if (loads[t] > 0) drain_on(&bs->q_full[t], (loads[t] - 1) & 1);
@@ -811,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 // 32 score columns from c on, hidden ones as -inf
                 const auto hide = [&](float *s, int c) {
                     const int pos0 = j * TT;
-                    const int at = I8 || p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
+                    const int at = p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
                     // of these columns the row sees lo .. hi - 1, less those on no page
                     const int lo = min(max(pos0 - at - col0 - c, 0), 32), hi = min(max(last + 1 - at - col0 - c, 0), 32);
                     uint32_t sees = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
@@ -829,6 +812,20 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                     }
                     return fmaxf(top, fmaxf(t0, t1));
                 };
+                // int8: the scores of 32 columns from c on, times their scales of K
+                const ulonglong2 *scales = reinterpret_cast<const ulonglong2 *>(smem + C::OFF_SCALES + ((seen + j - x.j0) & 7) * 1024 + col0 * 4);
+                const auto scale = [&](float *s, int c) {
+                    if (!I8) return;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const ulonglong2 k = scales[(c + e) / 4];
+                        const float2 u = unpair(mul2(pair(s[e], s[e + 1]), k.x)), v = unpair(mul2(pair(s[e + 2], s[e + 3]), k.y));
+                        s[e] = u.x;
+                        s[e + 1] = u.y;
+                        s[e + 2] = v.x;
+                        s[e + 3] = v.y;
+                    }
+                };
                 // the row's maximum; columns 0 .. 63 stay in registers, 64 .. 127
                 // are read again below
                 float s[64], h[32];
@@ -838,6 +835,8 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                     ptx::tmem_ld32(s_at + c, c == 64 ? s : s + 32);
                     if (c == 96) {
                         ptx::tmem_wait_ld();
+                        scale(s, 64);
+                        scale(s + 32, 96);
                         if (MASK) {
                             hide(s, 64);
                             hide(s + 32, 96);
@@ -848,17 +847,8 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 ptx::tmem_ld32(s_at + col0, s);
                 ptx::tmem_ld32(s_at + col0 + 32, s + 32);
                 ptx::tmem_wait_ld();
-                const float4 *scales = reinterpret_cast<const float4 *>(smem + C::OFF_SCALES + ((seen + j - x.j0) & 7) * 1024 + col0 * 4);
-                if (I8) {
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
-                        const float4 k = scales[e / 4];
-                        s[e] *= k.x;
-                        s[e + 1] *= k.y;
-                        s[e + 2] *= k.z;
-                        s[e + 3] *= k.w;
-                    }
-                }
+                scale(s, 0);
+                scale(s + 32, 32);
                 if (MASK) {
                     hide(s, 0);
                     hide(s + 32, 32);
@@ -911,12 +901,16 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                         sum1 = add2(sum1, pair(p2, p3));
                         if (I8) {
                             // (the scale of a position that is hidden may be a NaN)
-                            const float4 y = scales[32 + (c + e) / 4];
-                            const auto times = [&](float weight, float by, float score) {
-                                return MASK && score == neg_inf() ? 0.f : weight * by;
-                            };
-                            word[e / 2] = pack_bf16x2(times(p0, y.x, s[e]), times(p1, y.y, s[e + 1]));
-                            word[e / 2 + 1] = pack_bf16x2(times(p2, y.z, s[e + 2]), times(p3, y.w, s[e + 3]));
+                            const ulonglong2 y = scales[32 + (c + e) / 4];
+                            float2 f = unpair(mul2(pair(p0, p1), y.x)), g = unpair(mul2(pair(p2, p3), y.y));
+                            if (MASK) {
+                                f.x = s[e] == neg_inf() ? 0.f : f.x;
+                                f.y = s[e + 1] == neg_inf() ? 0.f : f.y;
+                                g.x = s[e + 2] == neg_inf() ? 0.f : g.x;
+                                g.y = s[e + 3] == neg_inf() ? 0.f : g.y;
+                            }
+                            word[e / 2] = pack_bf16x2(f.x, f.y);
+                            word[e / 2 + 1] = pack_bf16x2(g.x, g.y);
                         } else {
                             word[e / 2] = pack_bf16x2(p0, p1);
                             word[e / 2 + 1] = pack_bf16x2(p2, p3);
@@ -930,9 +924,11 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 if (C::NC == 128) {
                     ptx::tmem_wait_ld();
                     ptx::tmem_ld32(s_at + 96, s);
+                    scale(h, 64);
                     if (MASK) hide(h, 64);
                     weigh(h, 64);
                     ptx::tmem_wait_ld();
+                    scale(s, 96);
                     if (MASK) hide(s, 96);
                     weigh(s, 96);
                 }
@@ -948,7 +944,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const volatile uint32_t *bad = reinterpret_cast<const volatile uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
-                const bool holes = p.c.block_table && (I8 ? (bad[1] | bad[2] | bad[3] | bad[4]) : bad[0]) != 0;
+                const bool holes = p.c.block_table && bad[0] != 0;
                 if (j < plain && !holes) block(j, buf, bad, holes, std::false_type());
                 else block(j, buf, bad, holes, std::true_type());
             }
@@ -1083,11 +1079,12 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
 }
 
 // ------------------------------------------------------------- host side
+// bf16 numbers, or pairs of int8 codes.
 bool encode(CUtensorMap *m, cuuint32_t rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
-            const cuuint32_t *box) {
+            const cuuint32_t *box, bool codes = false) {
     const EncodeTiledFn fn = encode_fn();
     const cuuint32_t one[4] = {1, 1, 1, 1};
-    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
+    return fn && fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1135,7 +1132,7 @@ int64_t prefill_slot_floats(int d) { return d == 128 ? Cfg<128, true, false>::SL
 
 bool prefill_tc_supports(const PrefillParams &p) {
     int64_t rs, rows, g[3];
-    return p.scale_log2 > 0.f && (p.c.int8 || !p.c.block_table || pool_rows(p.c, &rs, &rows, g));
+    return p.scale_log2 > 0.f && (!p.c.block_table || pool_rows(p.c, &rs, &rows, g));
 }
 
 int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
@@ -1152,31 +1149,33 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
         const cuuint32_t box[4] = {64, (cuuint32_t)p.g, (cuuint32_t)a.T, 1};
         if (!encode(&a.tq, 4, p.q, dims, strides, box)) return -2;
     }
-    if (p.c.int8) return p.c.d == 128 ? launch<128, false, true>(a, grid, st) : launch<256, false, true>(a, grid, st);
+    const int es = p.c.int8 ? 1 : 2;                 // bytes a number
+    const cuuint64_t width = (cuuint64_t)p.c.d * es / 2;
     const void *caches[2] = {p.c.k, p.c.v};
     const int64_t *strides_of[2] = {p.c.ks, p.c.vs};
     for (int i = 0; i < 2; ++i) {
         const int64_t *s = strides_of[i];
         if (a.prow > 0) {
             const int64_t rows = p.c.block_table ? p.c.page_size : p.c.cap;
-            const cuuint64_t dims[4] = {(cuuint64_t)p.c.d, (cuuint64_t)rows, (cuuint64_t)p.c.Hkv, (cuuint64_t)p.c.lead};
-            const cuuint64_t strides[3] = {(cuuint64_t)s[2] * 2, (cuuint64_t)s[1] * 2, (cuuint64_t)s[0] * 2};
+            const cuuint64_t dims[4] = {width, (cuuint64_t)rows, (cuuint64_t)p.c.Hkv, (cuuint64_t)p.c.lead};
+            const cuuint64_t strides[3] = {(cuuint64_t)(s[2] * es), (cuuint64_t)(s[1] * es), (cuuint64_t)(s[0] * es)};
             const cuuint32_t box[4] = {64, (cuuint32_t)a.prow, 1, 1};
-            if (!encode(i ? &a.tv : &a.tk, 4, caches[i], dims, strides, box)) return -2;
+            if (!encode(i ? &a.tv : &a.tk, 4, caches[i], dims, strides, box, p.c.int8)) return -2;
         }
         int64_t rs, rows;
         if (p.c.block_table) {
             if (!pool_rows(p.c, &rs, &rows, a.gs)) return -2;
-            const cuuint64_t dims[2] = {(cuuint64_t)p.c.d, (cuuint64_t)rows};
-            const cuuint64_t strides[1] = {(cuuint64_t)rs * 2};
+            const cuuint64_t dims[2] = {width, (cuuint64_t)rows};
+            const cuuint64_t strides[1] = {(cuuint64_t)(rs * es)};
             const cuuint32_t box[2] = {64, 1};
-            if (!encode(i ? &a.gv : &a.gk, 2, caches[i], dims, strides, box)) return -2;
+            if (!encode(i ? &a.gv : &a.gk, 2, caches[i], dims, strides, box, p.c.int8)) return -2;
         }
     }
     if (a.prow == 0) { a.tk = a.gk; a.tv = a.gv; }   // (unused)
-    if (p.c.d == 256) return launch<256, false, false>(a, grid, st);
-    if ((int64_t)p.n > a.T) return launch<128, true, false>(a, grid, st);
-    return launch<128, false, false>(a, grid, st);
+    const bool two = p.n > a.T, i8 = p.c.int8;   // two tiles where the longest chunk fills more than one
+    if (p.c.d == 256) return i8 ? launch<256, false, true>(a, grid, st) : launch<256, false, false>(a, grid, st);
+    if (two) return i8 ? launch<128, true, true>(a, grid, st) : launch<128, true, false>(a, grid, st);
+    return i8 ? launch<128, false, true>(a, grid, st) : launch<128, false, false>(a, grid, st);
 }
 
 }  // namespace fd
