@@ -6,11 +6,10 @@
 // one tile, or two where a chunk has more rows than one holds (head_dim 128):
 // each position's K and V then serve 256 rows.
 //
-// Work.  Segments (sequence, kv head, tiles) follow one another in units of
-// positions: a charge for its start and end, then the positions that its last
-// row sees.  The grid's blocks, one an SM, take equal consecutive shares of the
-// units, and in each segment the blocks of 128 positions that start in their
-// share.  A segment that is cut leaves partial sums in the workspace, which a
+// Work.  Segments (sequence, kv head, tiles) follow one another in units of 128
+// positions: a charge for its start and end, then its blocks of positions (a
+// bound on them that sums in closed form).  The grid's blocks, one an SM, take
+// equal consecutive shares of the units.  A segment that is cut leaves partial sums in the workspace, which a
 // second launch joins in the order of the pieces.
 //
 // Roles in a block:
@@ -35,7 +34,6 @@
 #include <cuda_runtime.h>
 
 #include <cstring>
-#include <type_traits>
 
 #include "fd_api.h"
 #include "fd_device.cuh"
@@ -68,7 +66,7 @@ struct Bars {
     uint64_t q_full[2], q_free[2], s_full[2], p_full[2], o_full[2];
     uint64_t cross, pv_done[2], drain[2];
     uint32_t tmem_base;
-    int abort_flag;
+    int abort_flag;          // the site of the first wait that ran out, else 0
     int turn;                // held by the issuer whose tile's MMAs go out
 };
 
@@ -106,8 +104,8 @@ struct Cfg {
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
 // ------------------------------------------------------------------ work
-// Positions that a segment's start and end are charged as.
-constexpr int64_t kCharge = 256;
+// Blocks of positions that a segment's start and end are charged as.
+constexpr int kCharge = 2;
 
 // What a launch's share of the work goes by: B sequences of L_b positions, fresh_b
 // of them new.
@@ -117,95 +115,111 @@ struct Seq {
 };
 
 __device__ __forceinline__ Seq seq_of(const PrefillParams &p, int b, int S, bool flag = false) {
-    const int64_t raw = __ldg(p.lengths + b), L = clamp_len(raw, p.c.cap);
-    const int64_t want = p.new_lengths ? __ldg(p.new_lengths + b) : p.n, fresh = clamp_len(want, p.n);
+    const int cap = (int)p.c.cap, raw = __ldg(p.lengths + b), L = max(0, min(raw, cap));
+    const int want = p.new_lengths ? __ldg(p.new_lengths + b) : p.n, fresh = max(0, min(want, p.n));
     if (flag && (raw != L || want != fresh)) atomicOr(p.status, kDevBadLength);
-    return Seq{(int)L, (int)fresh, (int)((fresh + S - 1) / S)};
+    return Seq{L, fresh, (fresh + S - 1) / S};
 }
 
-// Units of a segment, and of the first q of a kv head.
-__device__ __forceinline__ int64_t cost_of(const PrefillParams &p, const Seq &s, int S, int q) {
-    return kCharge + (p.causal ? max(s.base(), 0) + (int64_t)S * (q + 1) : (int64_t)s.L);
+// Units of a segment, and of the first q of a kv head.  Causal segments see the
+// positions before the chunk and (q + 1) S new ones, in at most ceil((q + 1) /
+// per) blocks, per = 128 / S (S = 256: 2 (q + 1)).
+__device__ __forceinline__ int cost_of(const PrefillParams &p, const Seq &s, int S, int q) {
+    if (!p.causal) return kCharge + (s.L + TT - 1) / TT;
+    const int per = TT / S;
+    return kCharge + (max(s.base(), 0) + TT - 1) / TT + (S > TT ? 2 * (q + 1) : (q + per) / per);
 }
-__device__ __forceinline__ int64_t units_of(const PrefillParams &p, const Seq &s, int S, int64_t q) {
-    if (!p.causal) return q * (kCharge + s.L);
-    return q * (kCharge + max(s.base(), 0)) + S * (q * (q + 1) / 2);
+__device__ __forceinline__ int units_of(const PrefillParams &p, const Seq &s, int S, int q) {
+    if (!p.causal) return q * (kCharge + (s.L + TT - 1) / TT);
+    const int before = q * (kCharge + (max(s.base(), 0) + TT - 1) / TT);
+    if (S > TT) return before + q * (q + 1);
+    const int per = TT / S, m = q / per;
+    return before + per * (m * (m + 1) / 2) + (q - m * per) * (m + 1);
 }
 
-// All units, and the blocks that share them.
+// All units (below 2^31), and the blocks that share them: the first `rest` take
+// one more.
 struct Total {
-    int64_t units;
-    int G;
-    __device__ __forceinline__ Split split() const { return Split{units, G}; }
+    int units, each, G, rest;
+    int first;               // units of this lane's first sequence, of one kv head
+    __device__ __forceinline__ int start(int c) const { return c * each + min(c, rest); }
+    __device__ __forceinline__ int owner(int u) const {
+        const int more = rest * (each + 1);
+        return u < more ? u / (each + 1) : rest + (u - more) / each;
+    }
 };
 
 // Every lane of a warp.
 __device__ __forceinline__ Total total_of(const PrefillParams &p, int S, int grid, bool flag) {
-    int64_t sum = 0;
+    Total t;
+    t.first = 0;
+    int sum = 0;
+#pragma unroll 1
     for (int i = threadIdx.x & 31; i < p.B; i += 32) {
         const Seq x = seq_of(p, i, S, flag);
-        sum += units_of(p, x, S, x.nq);
+        const int mine = units_of(p, x, S, x.nq);
+        if (i < 32) t.first = mine;
+        sum += mine;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    sum *= p.c.Hkv;
-    const int64_t most = sum / TT;
-    return Total{sum, (int)(most < 1 ? 1 : most < grid ? most : grid)};
+    t.units = __reduce_add_sync(kAll, sum) * p.c.Hkv;
+    t.G = max(1, min(t.units, grid));
+    t.each = t.units / t.G;
+    t.rest = t.units - t.each * t.G;
+    return t;
 }
 
 // A walk over the segments of a share: the current one, and where the share starts
-// and ends, counted from the unit of its first position.
+// and ends, in blocks of it.
 struct Walk {
-    int64_t from, to;
+    int from, to;
     Seq s;
     int b, hk, q;
 
     // The segment that holds unit u0 of a share [u0, u1); every lane of a warp.
-    __device__ __forceinline__ void seek(const PrefillParams &p, int S, int64_t u0, int64_t u1) {
+    __device__ __forceinline__ void seek(const PrefillParams &p, int S, const Total &t, int u0, int u1) {
         const int lane = threadIdx.x & 31;
-        int64_t before = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int i = b0 + lane;
-            int64_t mine = 0;
-            if (i < p.B) {
-                const Seq x = seq_of(p, i, S);
-                mine = units_of(p, x, S, x.nq) * p.c.Hkv;
-            }
-            int64_t upto = mine;
+        int before = 0, mine = t.first * p.c.Hkv;
+#pragma unroll 1
+        for (int b0 = 0;; b0 += 32) {
+            int upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(kAll, upto, o);
+                const int y = __shfl_up_sync(kAll, upto, o);
                 if (lane >= o) upto += y;
             }
             const unsigned in = __ballot_sync(kAll, before + upto > u0);
             if (in) {
                 const int at = __ffs(in) - 1;
-                const int64_t first = before + __shfl_sync(kAll, upto - mine, at);
+                int x = u0 - before - __shfl_sync(kAll, upto - mine, at);
                 b = b0 + at;
                 s = seq_of(p, b, S);
-                const int64_t head = units_of(p, s, S, s.nq);
-                hk = (int)((u0 - first) / head);
-                const int64_t x = u0 - first - hk * head;
+                const int head = units_of(p, s, S, s.nq);
+                hk = x / head;
+                x -= hk * head;
                 if (p.causal) {
-                    // S/2 q^2 + k q = x
-                    const float k = (float)(kCharge + max(s.base(), 0)) + 0.5f * S;
-                    q = (int)((sqrtf(k * k + 2.f * S * (float)x) - k) / S);
+                    // about S / 256 q^2 + k q = x
+                    const float k = (float)cost_of(p, s, S, 0), w = S * (1.f / 128);
+                    q = max(0, min((int)((sqrtf(k * k + 2.f * w * (float)x) - k) / w), s.nq - 1));
+                    while (q > 0 && units_of(p, s, S, q) > x) --q;
+                    while (q + 1 < s.nq && units_of(p, s, S, q + 1) <= x) ++q;
                 } else {
-                    q = (int)(x / (kCharge + s.L));
+                    q = x / cost_of(p, s, S, 0);
                 }
-                q = max(0, min(q, s.nq - 1));
-                while (q > 0 && units_of(p, s, S, q) > x) --q;
-                while (q + 1 < s.nq && units_of(p, s, S, q + 1) <= x) ++q;
-                const int64_t a = first + hk * head + units_of(p, s, S, q) + kCharge;
-                from = u0 - a;
-                to = u1 - a;
+                from = x - units_of(p, s, S, q) - kCharge;
+                to = from + (u1 - u0);
                 return;
             }
             before += __shfl_sync(kAll, upto, 31);
+            const int i = b0 + 32 + lane;
+            mine = 0;
+            if (i < p.B) {
+                const Seq x = seq_of(p, i, S);
+                mine = units_of(p, x, S, x.nq) * p.c.Hkv;
+            }
         }
     }
     __device__ __forceinline__ bool next(const PrefillParams &p, int S) {
-        const int64_t cost = cost_of(p, s, S, q);
+        const int cost = cost_of(p, s, S, q);
         from -= cost;
         to -= cost;
         if (to + kCharge <= 0) return false;
@@ -224,7 +238,7 @@ struct Walk {
     // Positions that the first `tokens` of this segment see.
     __device__ __forceinline__ int seen(const PrefillParams &p, int S, int tokens) const {
         if (!p.causal) return s.L;
-        return max(0, min(s.L, s.base() + (int)min((int64_t)s.fresh, (int64_t)q * S + tokens)));
+        return max(0, min(s.L, s.base() + min(s.fresh, q * S + tokens)));
     }
     __device__ __forceinline__ int blocks(const PrefillParams &p, int S) const { return (seen(p, S, S) + TT - 1) / TT; }
 };
@@ -243,25 +257,32 @@ __device__ __forceinline__ Piece piece_of(const PfArgs &a, const Walk &w) {
     const int S = QT * a.T;
     Piece x;
     x.all = w.blocks(p, S);
-    x.j0 = w.from <= 0 ? 0 : (int)min((int64_t)x.all, (w.from + TT - 1) / TT);
-    x.j1 = w.to <= 0 ? 0 : (int)min((int64_t)x.all, (w.to + TT - 1) / TT);
+    x.j0 = max(0, min(x.all, w.from));
+    x.j1 = max(0, min(x.all, w.to));
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         x.hi[t] = x.j0;
-        if (t < QT && (int64_t)w.q * S + t * a.T < w.s.fresh)
+        if (t < QT && w.q * S + t * a.T < w.s.fresh)
             x.hi[t] = max(x.j0, min(x.j1, (w.seen(p, S, (t + 1) * a.T) + TT - 1) / TT));
     }
     return x;
 }
 
 // ----------------------------------------------------------------- helpers
+// A wait within the launch's limit; one that runs out stops the block's others, and
+// its role reports `site` when it ends.
 __device__ __forceinline__ bool wait_on(Bars *bs, const PrefillParams &p, uint64_t *bar, uint32_t parity, int site) {
-    if (ptx::mbar_wait(bar, parity & 1, &bs->abort_flag, p.wait_ns)) return true;
-    // (the first wait that gave up is recorded, as in the decode kernel)
-    if (!*reinterpret_cast<volatile int *>(&bs->abort_flag) && atomicCAS(p.status + 1, 0, site) == 0) p.status[2] = (int)parity;
-    *reinterpret_cast<volatile int *>(&bs->abort_flag) = 1;
-    atomicOr(p.status, kDevTimeout);
-    return false;
+    if (ptx::mbar_try_wait(bar, parity & 1)) return true;
+    volatile int *abort = &bs->abort_flag;
+    uint64_t t0 = 0;
+    for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity & 1); ++n)
+        if ((n & 63) == 0) {
+            const uint64_t now = ptx::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > p.wait_ns) atomicCAS(&bs->abort_flag, 0, site);
+            if (*abort) return false;
+        }
+    return true;
 }
 
 // Waits for a block's own copies or MMAs, which must end even when another role
@@ -274,13 +295,14 @@ __device__ __forceinline__ void drain_on(uint64_t *bar, uint32_t parity) {
 
 // The issuers' turn, taken (within the limit of every wait) and given back.
 __device__ __forceinline__ bool take_turn(Bars *bs, const PrefillParams &p) {
-    if (atomicCAS(&bs->turn, 0, 1) == 0) return true;
-    const uint64_t t0 = ptx::globaltimer_ns();
+    volatile int *abort = &bs->abort_flag;
+    uint64_t t0 = 0;
     for (uint32_t n = 1; atomicCAS(&bs->turn, 0, 1) != 0; ++n)
-        if ((n & 63) == 0 && (*reinterpret_cast<volatile int *>(&bs->abort_flag) || ptx::globaltimer_ns() - t0 > p.wait_ns)) {
-            *reinterpret_cast<volatile int *>(&bs->abort_flag) = 1;
-            atomicOr(p.status, kDevTimeout);
-            return false;
+        if ((n & 63) == 0) {
+            const uint64_t now = ptx::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > p.wait_ns) atomicCAS(&bs->abort_flag, 0, 12);
+            if (*abort) return false;
         }
     return true;
 }
@@ -471,7 +493,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
     {
         const Total total = total_of(p, S, gridDim.x, warp == C::PRODUCER && blockIdx.x == 0);
         has = (int)blockIdx.x < total.G && total.units > 0;
-        if (has) w.seek(p, S, total.split().start(blockIdx.x), total.split().start(blockIdx.x + 1));
+        if (has) w.seek(p, S, total, total.start(blockIdx.x), total.start(blockIdx.x + 1));
     }
     ptx::tc_fence_before();
     __syncthreads();
@@ -591,25 +613,33 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 if (lane == 0) ring[0] = any;
                 __syncwarp();
             };
-            Rows now = look(x.j0), after = look(x.j0 + 1);
-            mark(x.j0, now);
-#pragma unroll
-            for (int h = 0; h < C::NH; ++h)
-                if (ok) fill(x.j0, h, false, now);
-            for (int j = x.j0; j < x.j1 && ok; ++j) {
-                const Rows then = look(j + 2);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    // (two tiles: V(j) is wanted before K(j + 1))
-                    const bool v = TWO ? k == 0 : k == 1;
-                    if (!v && j + 1 >= x.j1) continue;
-                    if (!v) mark(j + 1, after);
-#pragma unroll
-                    for (int h = 0; h < C::NH; ++h)
-                        if (ok) fill(v ? j : j + 1, h, v, v ? now : after);
+            // K(0), K(1), V(0), K(2), V(1) .. V(n - 1); two tiles: K(0), V(0), K(1), ..
+            const int n = x.j1 - x.j0;
+            Rows of_v{{-1, -1, -1, -1}}, of_k = look(x.j0), then = of_v;
+            int kb = 0, vb = 0;
+#pragma unroll 1
+            for (int f = 0; f < 2 * n && ok; ++f) {
+                const bool v = TWO ? (f & 1) : f == 2 * n - 1 || (f > 0 && (f & 1) == 0);
+                const int j = x.j0 + (v ? vb : kb);
+                if (!v) mark(j, of_k);
+#pragma unroll 1
+                for (int h = 0; h < C::NH && ok; ++h) fill(j, h, v, v ? of_v : of_k);
+                if (!v) {
+                    const Rows r = look(j + 1);
+                    if (TWO || f == 0) {
+                        of_v = of_k;
+                        of_k = r;
+                    } else {
+                        then = r;
+                    }
+                    ++kb;
+                } else {
+                    if (!TWO) {
+                        of_v = of_k;
+                        of_k = then;
+                    }
+                    ++vb;
                 }
-                now = after;
-                after = then;
             }
             seen += x.j1 - x.j0;
         }
@@ -787,22 +817,10 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
             const int all_see = p.causal ? min(w.s.base() + first, w.s.L - 1) : w.s.L - 1;
             float m = neg_inf(), l = 0.f;
             uint64_t sum0 = 0, sum1 = 0;
-            // one block of positions; with MASK some row does not see all of it
-            const auto block = [&](int j, uint32_t buf, const volatile uint32_t *bad, bool holes, auto mask_tag) {
-                constexpr bool MASK = decltype(mask_tag)::value;
+            // one block of positions, whose hidden scores are -inf already where some row
+            // does not see all of it (masked; int8: the others scaled)
+            const auto block = [&](int j, uint32_t buf, bool masked) {
                 const uint32_t s_at = tmem + lanes + buf * 128;
-                // 32 score columns from c on, hidden ones as -inf
-                const auto hide = [&](float *s, int c) {
-                    const int pos0 = j * TT;
-                    const int at = p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
-                    // of these columns the row sees lo .. hi - 1, less those on no page
-                    const int lo = min(max(pos0 - at - col0 - c, 0), 32), hi = min(max(last + 1 - at - col0 - c, 0), 32);
-                    uint32_t sees = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
-                    if (holes) sees &= ~bad[1 + (col0 + c) / 32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (!((sees >> e) & 1u)) s[e] = neg_inf();
-                };
                 const auto most = [&](const float *s, float top) {
                     float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
 #pragma unroll
@@ -815,7 +833,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 // int8: the scores of 32 columns from c on, times their scales of K
                 const ulonglong2 *scales = reinterpret_cast<const ulonglong2 *>(smem + C::OFF_SCALES + ((seen + j - x.j0) & 7) * 1024 + col0 * 4);
                 const auto scale = [&](float *s, int c) {
-                    if (!I8) return;
+                    if (!I8 || masked) return;
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {
                         const ulonglong2 k = scales[(c + e) / 4];
@@ -837,10 +855,6 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                         ptx::tmem_wait_ld();
                         scale(s, 64);
                         scale(s + 32, 96);
-                        if (MASK) {
-                            hide(s, 64);
-                            hide(s + 32, 96);
-                        }
                         top = most(s, most(s + 32, top));
                     }
                 }
@@ -849,10 +863,6 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 ptx::tmem_wait_ld();
                 scale(s, 0);
                 scale(s + 32, 32);
-                if (MASK) {
-                    hide(s, 0);
-                    hide(s + 32, 32);
-                }
                 top = most(s, most(s + 32, top));
                 if (!TWO) top = fmaxf(top, other(top));
                 if (!ok) return;
@@ -903,7 +913,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                             // (the scale of a position that is hidden may be a NaN)
                             const ulonglong2 y = scales[32 + (c + e) / 4];
                             float2 f = unpair(mul2(pair(p0, p1), y.x)), g = unpair(mul2(pair(p2, p3), y.y));
-                            if (MASK) {
+                            if (masked) {
                                 f.x = s[e] == neg_inf() ? 0.f : f.x;
                                 f.y = s[e + 1] == neg_inf() ? 0.f : f.y;
                                 g.x = s[e + 2] == neg_inf() ? 0.f : g.x;
@@ -925,11 +935,9 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                     ptx::tmem_wait_ld();
                     ptx::tmem_ld32(s_at + 96, s);
                     scale(h, 64);
-                    if (MASK) hide(h, 64);
                     weigh(h, 64);
                     ptx::tmem_wait_ld();
                     scale(s, 96);
-                    if (MASK) hide(s, 96);
                     weigh(s, 96);
                 }
                 ptx::tmem_wait_st();
@@ -945,8 +953,36 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 ptx::tc_fence_after();
                 const volatile uint32_t *bad = reinterpret_cast<const volatile uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
                 const bool holes = p.c.block_table && bad[0] != 0;
-                if (j < plain && !holes) block(j, buf, bad, holes, std::false_type());
-                else block(j, buf, bad, holes, std::true_type());
+                const bool masked = j >= plain || holes;
+                if (masked) {
+                    // in place first: blocks that a row does not see whole are few, and
+                    // a second loop body would crowd the instruction caches
+                    const uint32_t s_at = tmem + lanes + buf * 128 + col0;
+                    const int pos0 = j * TT;
+                    const int at = p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
+#pragma unroll 1
+                    for (int c = 0; c < C::NC; c += 32) {
+                        float s[32];
+                        ptx::tmem_ld32(s_at + c, s);
+                        // of these columns the row sees lo .. hi - 1, less those on no page
+                        const int lo = min(max(pos0 - at - col0 - c, 0), 32), hi = min(max(last + 1 - at - col0 - c, 0), 32);
+                        uint32_t sees = hi > lo ? (0xffffffffu >> (32 - (hi - lo))) << lo : 0u;
+                        if (holes) sees &= ~bad[1 + (col0 + c) / 32];
+                        ptx::tmem_wait_ld();
+                        if (I8) {
+                            const float *k = reinterpret_cast<const float *>(smem + C::OFF_SCALES + ((seen + j - x.j0) & 7) * 1024) + col0 + c;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) s[e] *= k[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!((sees >> e) & 1u)) s[e] = neg_inf();
+                        ptx::tmem_st16(s_at + c, s);
+                        ptx::tmem_st16(s_at + c + 16, s + 16);
+                    }
+                    ptx::tmem_wait_st();
+                }
+                block(j, buf, masked);
             }
             if (!ok) break;
             seen += x.j1 - x.j0;
@@ -1015,6 +1051,11 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+    if (tid == 0 && bs->abort_flag) {
+        // (the launch's first is recorded, as in the decode kernel)
+        atomicOr(p.status, kDevTimeout);
+        atomicCAS(p.status + 1, 0, bs->abort_flag);
+    }
     if (warp == C::ISSUER) ptx::tmem_dealloc(tmem, 512);
 }
 
@@ -1032,14 +1073,13 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
     const int S = C::QT * a.T;
     const Total total = total_of(p, S, grid, false);
     if (c >= total.G || total.units == 0) return;
-    const Split sp = total.split();
-    const int64_t u = sp.start(c);
+    const int u = total.start(c);
     Walk w;
-    w.seek(p, S, u, u);
+    w.seek(p, S, total, u, u);
     const int all = w.blocks(p, S);
     if (all == 0) return;
-    const int64_t block0 = u - w.from;                      // unit of the first block
-    const int first = sp.owner(block0), last = sp.owner(block0 + (int64_t)(all - 1) * TT);
+    const int block0 = u - w.from;                          // unit of the first block
+    const int first = total.owner(block0), last = total.owner(block0 + all - 1);
     if (c <= first || c > last) return;
     const int parts = (last - first) * kJoinParts, at = (c - first - 1) * kJoinParts + (int)blockIdx.y;
     const int r0 = C::ROWS * at / parts, r1 = C::ROWS * (at + 1) / parts;
@@ -1140,6 +1180,11 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
     memset(&a, 0, sizeof a);
     a.p = p;
     a.T = TT / p.g;
+    {
+        // units are counted in 32 bits
+        const int64_t S = a.T, nq = ceil_div(p.n, S);
+        if ((int64_t)p.B * p.c.Hkv * nq * (kCharge + ceil_div(p.c.cap + p.n, TT) + 2) >= (int64_t)1 << 31) return -2;
+    }
     a.R = a.T * p.g;
     a.prow = box_rows(p.c);
     a.slots = p.partials;
