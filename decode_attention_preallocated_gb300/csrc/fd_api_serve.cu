@@ -189,7 +189,7 @@ int fd_prefill(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_
     for (int i = 0; i < 3; ++i) { p.qs[i] = q->stride[i]; p.os[i] = out->stride[i]; }
     p.lengths = kv_lengths; p.new_lengths = new_lengths;
     p.status = opts->ws->status; p.partials = opts->ws->partials;
-    p.wait_ns = opts->wait_limit_us > 0 ? (uint64_t)opts->wait_limit_us * 1000u : fd::kDefaultWaitNs;
+    p.wait_rounds = opts->wait_limit_us > 0 ? opts->wait_limit_us : (int32_t)(fd::kDefaultWaitNs / 1000);
     const cudaStream_t st = static_cast<cudaStream_t>(opts->stream);
     if (opts->kernel != FD_KERNEL_SIMT && fd::prefill_tc_supports(p)) {
         int32_t G = opts->num_ctas < 65535 ? opts->num_ctas : 65535;

@@ -123,17 +123,17 @@ __device__ __forceinline__ Seq seq_of(const PrefillParams &p, int b, int S, bool
 
 // Units of a segment, and of the first q of a kv head.  Causal segments see the
 // positions before the chunk and (q + 1) S new ones, in at most ceil((q + 1) /
-// per) blocks, per = 128 / S (S = 256: 2 (q + 1)).
+// per) blocks, per = 128 / S whole segments a block (S = 256: 2 (q + 1) blocks).
 __device__ __forceinline__ int cost_of(const PrefillParams &p, const Seq &s, int S, int q) {
     if (!p.causal) return kCharge + (s.L + TT - 1) / TT;
-    const int per = TT / S;
+    const int per = p.per;
     return kCharge + (max(s.base(), 0) + TT - 1) / TT + (S > TT ? 2 * (q + 1) : (q + per) / per);
 }
 __device__ __forceinline__ int units_of(const PrefillParams &p, const Seq &s, int S, int q) {
     if (!p.causal) return q * (kCharge + (s.L + TT - 1) / TT);
     const int before = q * (kCharge + (max(s.base(), 0) + TT - 1) / TT);
     if (S > TT) return before + q * (q + 1);
-    const int per = TT / S, m = q / per;
+    const int per = p.per, m = q / per;
     return before + per * (m * (m + 1) / 2) + (q - m * per) * (m + 1);
 }
 
@@ -269,19 +269,16 @@ __device__ __forceinline__ Piece piece_of(const PfArgs &a, const Walk &w) {
 }
 
 // ----------------------------------------------------------------- helpers
-// A wait within the launch's limit; one that runs out stops the block's others, and
-// its role reports `site` when it ends.
+// A wait within the launch's limit, counted in rounds of a microsecond's suspension
+// (no clock, no call: some thirty places wait, and instruction caches are
+// small).  One that runs out stops the block's others, and its site is reported
+// when the block ends.
 __device__ __forceinline__ bool wait_on(Bars *bs, const PrefillParams &p, uint64_t *bar, uint32_t parity, int site) {
-    if (ptx::mbar_try_wait(bar, parity & 1)) return true;
     volatile int *abort = &bs->abort_flag;
-    uint64_t t0 = 0;
-    for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity & 1); ++n)
-        if ((n & 63) == 0) {
-            const uint64_t now = ptx::globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > p.wait_ns) atomicCAS(&bs->abort_flag, 0, site);
-            if (*abort) return false;
-        }
+    for (int n = p.wait_rounds; !ptx::mbar_try_wait_for(bar, parity & 1, 1000); --n) {
+        if (n == 0) *abort = site;
+        if (*abort) return false;
+    }
     return true;
 }
 
@@ -293,17 +290,14 @@ __device__ __forceinline__ void drain_on(uint64_t *bar, uint32_t parity) {
         if ((n & 63) == 0 && ptx::globaltimer_ns() - t0 > kDrainNs) return;
 }
 
-// The issuers' turn, taken (within the limit of every wait) and given back.
+// The issuers' turn, taken (the other holds it for a microsecond or so; a thousand
+// tries of some 100 cycles a round) and given back.
 __device__ __forceinline__ bool take_turn(Bars *bs, const PrefillParams &p) {
     volatile int *abort = &bs->abort_flag;
-    uint64_t t0 = 0;
-    for (uint32_t n = 1; atomicCAS(&bs->turn, 0, 1) != 0; ++n)
-        if ((n & 63) == 0) {
-            const uint64_t now = ptx::globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > p.wait_ns) atomicCAS(&bs->abort_flag, 0, 12);
-            if (*abort) return false;
-        }
+    for (int64_t n = 1000 * (int64_t)p.wait_rounds; atomicCAS(&bs->turn, 0, 1) != 0; --n) {
+        if (n == 0) *abort = 12;
+        if (*abort) return false;
+    }
     return true;
 }
 __device__ __forceinline__ void give_turn(Bars *bs) { atomicExch(&bs->turn, 0); }
@@ -540,23 +534,29 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 if (!paged || j >= x.j1) return r;
                 const int32_t *table = p.c.block_table + (int64_t)w.b * p.c.max_pages;
                 const bool box = tiled(j);
-                const int n = box ? (lane < TT / a.prow ? 1 : 0) : 4;
+                const int pos = j * TT + lane * (box ? a.prow : 4);
+                if (box && lane >= TT / a.prow) return r;
+                int i = p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size, row = pos - i * p.c.page_size;
+                if (box) {
+                    const int32_t page = __ldg(table + i);
+                    r.y[0] = page < p.c.lead ? page : -1;
+                    r.y[1] = row;
+                    return r;
+                }
+                // four positions, on one page or more
+                int page[4], at[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int64_t pos = (int64_t)j * TT + (box ? lane * a.prow : 4 * lane + e);
-                    if (e < n && pos < w.s.L) {
-                        const int32_t at = (int32_t)pos;
-                        const int32_t i = p.c.page_shift >= 0 ? at >> p.c.page_shift : at / p.c.page_size;
-                        const int32_t page = __ldg(table + i), row = at - i * p.c.page_size;
-                        const bool good = page >= 0 && page < p.c.lead;
-                        if (box) {
-                            r.y[0] = good ? page : -1;
-                            r.y[1] = row;
-                        } else {
-                            r.y[e] = good ? (int)(page * a.gs[0] + w.hk * a.gs[1] + row * a.gs[2]) : -1;
-                        }
+                    at[e] = row;
+                    page[e] = pos + e < w.s.L ? __ldg(table + i) : -1;
+                    if (++row == p.c.page_size) {
+                        row = 0;
+                        ++i;
                     }
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (page[e] >= 0 && page[e] < p.c.lead) r.y[e] = (int)(page[e] * a.gs[0] + w.hk * a.gs[1] + at[e] * a.gs[2]);
                 return r;
             };
             // one half of K or V of block j
@@ -1093,7 +1093,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
         const float *s = a.slots + (2 * (int64_t)first + 1) * C::SLOT_FLOATS;
         int64_t step = C::SLOT_FLOATS;
         float top = neg_inf(), l = 0.f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
+#pragma unroll 2
         for (int k = first; k <= last; ++k) {
             // (a piece that saw nothing for the row holds no O)
             const float m = s[C::ROWS * D + r];
@@ -1218,6 +1218,7 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
     }
     if (a.prow == 0) { a.tk = a.gk; a.tv = a.gv; }   // (unused)
     const bool two = p.n > a.T, i8 = p.c.int8;   // two tiles where the longest chunk fills more than one
+    a.p.per = max(1, TT / (two && p.c.d == 128 ? 2 * a.T : a.T));
     if (p.c.d == 256) return i8 ? launch<256, false, true>(a, grid, st) : launch<256, false, false>(a, grid, st);
     if (two) return i8 ? launch<128, true, true>(a, grid, st) : launch<128, true, false>(a, grid, st);
     return i8 ? launch<128, false, true>(a, grid, st) : launch<128, false, false>(a, grid, st);

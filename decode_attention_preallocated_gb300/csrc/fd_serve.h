@@ -46,7 +46,8 @@ struct PrefillParams {
     const int32_t *lengths, *new_lengths;
     int32_t *status;
     float *partials;
-    uint64_t wait_ns;
+    int32_t per;                   // tcgen05: set by the launch
+    int32_t wait_rounds;           // tcgen05: bound on each internal wait, in rounds of about 1 us
 };
 
 // fd_beam.cu
