@@ -27,13 +27,16 @@
 //            overwrites S in TMEM in bf16.  A row's reference is its running
 //            maximum, refreshed, and O rescaled, only where a score passes it
 //            by 2^8.
+// Small pages (boxes of fewer than 64 rows) take too many TMA copies: warps 8-11
+// copy K and V by cp.async instead.
 // int8 caches: codes are copied into the second half of their slot, and
 // warps 8-11 widen them in place to bf16 (exactly); the position's K scale
-// multiplies its scores, its V scale its weights.  The producer is then warp 12,
+// multiplies its scores, its V scale its weights.  In both the producer is warp 12,
 // the issuers 13 and 14.
 #include <cuda_runtime.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include "fd_api.h"
 #include "fd_device.cuh"
@@ -70,16 +73,20 @@ struct Bars {
     int turn;                // held by the issuer whose tile's MMAs go out
 };
 
-template <int D, bool TWO, bool I8>
+// How K and V come: whole slots by TMA; int8 codes by TMA, widened; by cp.async.
+enum Load { kTma, kCodes, kCopies };
+
+template <int D, bool TWO, int LOAD>
 struct Cfg {
+    static constexpr bool I8 = LOAD == kCodes, MORE = LOAD != kTma;   // MORE: a warpgroup that widens or copies
     static_assert(!TWO || D == 128, "two tiles' O and S fill TMEM at head_dim 128");
-    // Warpgroups of softmax (two), of widening where codes are int8, and of the
-    // producers and issuers; softmax takes registers that the others give up.
-    static constexpr int THREADS = I8 ? 512 : 384;
-    static constexpr int LAUNCH_REGS = I8 ? 128 : 168, SOFTMAX_REGS = I8 ? 184 : 200, WIDEN_REGS = I8 ? 72 : 0,
-                         OTHER_REGS = I8 ? 72 : 104;
-    static_assert(256 * SOFTMAX_REGS + 128 * (WIDEN_REGS + OTHER_REGS) <= THREADS * LAUNCH_REGS, "registers of the launch");
-    static constexpr int PRODUCER = I8 ? 12 : 8, PRODUCER2 = I8 ? -1 : 11, ISSUER = PRODUCER + 1;   // warps; issuers: two
+    // Warpgroups of softmax (two), of widening or copying, and of the producers and
+    // issuers; softmax takes registers that the others give up.
+    static constexpr int THREADS = MORE ? 512 : 384;
+    static constexpr int LAUNCH_REGS = MORE ? 128 : 168, SOFTMAX_REGS = MORE ? 184 : 200, MORE_REGS = MORE ? 72 : 0,
+                         OTHER_REGS = MORE ? 72 : 104;
+    static_assert(256 * SOFTMAX_REGS + 128 * (MORE_REGS + OTHER_REGS) <= THREADS * LAUNCH_REGS, "registers of the launch");
+    static constexpr int PRODUCER = MORE ? 12 : 8, PRODUCER2 = MORE ? -1 : 11, ISSUER = PRODUCER + 1;   // warps; issuers: two
     static constexpr int NH = D / 128, QT = TWO ? 2 : 1;
     static constexpr uint32_t BOX = TT * 128;        // 128 rows x 64 numbers
     static constexpr uint32_t SLOT = 2 * BOX;        // 128 rows x 128 numbers
@@ -360,7 +367,7 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 // which are loaded a block before they are wanted.
 template <int D, bool TWO>
 __device__ __forceinline__ void widen_role(const PfArgs &a, Bars *bs, unsigned char *smem, Walk w, bool has) {
-    using C = Cfg<D, TWO, true>;
+    using C = Cfg<D, TWO, kCodes>;
     const PrefillParams &p = a.p;
     const int tid = (int)threadIdx.x - 256, S = C::QT * a.T;
     const int chunk = tid & 7, row0 = (tid & ~31) + ((tid & 31) >> 3);   // rows row0 + 4 e
@@ -441,10 +448,101 @@ __device__ __forceinline__ void widen_role(const PfArgs &a, Bars *bs, unsigned c
     }
 }
 
+// ----------------------------------------------------------------- copying
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// One warp of the copying warpgroup: its 32 rows of every fill, zeros where there is
+// none, in the slots' 128-byte swizzle.  Two fills are on their way while a third
+// sets out; one that has come is fenced and announced.
+template <int D, bool TWO>
+__device__ __forceinline__ void copy_role(const PfArgs &a, Bars *bs, unsigned char *smem, Walk w, bool has) {
+    using C = Cfg<D, TWO, kCopies>;
+    const PrefillParams &p = a.p;
+    const int tid = (int)threadIdx.x - 256, lane = tid & 31, S = C::QT * a.T;
+    // in a round the warp copies two rows: 16 lanes take a row's 16 chunks
+    const int chunk = lane & 15, row0 = (tid & ~31) + (lane >> 4);       // rows row0 + 2 e
+    const uint32_t slots = ptx::smem_u32(smem) + C::OFF_SLOTS + (chunk >> 3) * C::BOX + row0 * 128;
+    const uint16_t *const bases[2] = {static_cast<const uint16_t *>(p.c.k), static_cast<const uint16_t *>(p.c.v)};
+    uint32_t fills = 0, told = 0, seen = 0;
+    bool ok = true;
+    const auto tell = [&]() {
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive(&bs->slot_full[told % C::NS]);
+        ++told;
+    };
+    const auto tell_all = [&]() {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        while (told < fills) tell();
+    };
+    for (bool more = has; more && ok; more = w.next(p, S)) {
+        const Piece x = piece_of<C::QT>(a, w);
+        const int n = x.j1 - x.j0;
+        if (n <= 0) continue;
+        const int32_t *table = p.c.block_table + (int64_t)w.b * p.c.max_pages;
+        // position tid of block i: its table entry, and where its row lies (elements)
+        const auto entry_of = [&](int i) {
+            const int pos = (x.j0 + i) * TT + tid;
+            return i < n && pos < w.s.L ? __ldg(table + (p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size)) : -1;
+        };
+        int entry = entry_of(0);
+        int64_t k_row = -1, v_row = -1, v_next = -1;
+        const auto look = [&](int i) {
+            const int pos = (x.j0 + i) * TT + tid;
+            const int row = p.c.page_shift >= 0 ? pos & (p.c.page_size - 1) : pos % p.c.page_size;
+            const bool there = entry >= 0 && entry < p.c.lead, hole = pos < w.s.L && !there;
+            if (hole) atomicOr(p.status, kDevBadIndex);
+            k_row = there ? entry * p.c.ks[0] + w.hk * p.c.ks[1] + row * p.c.ks[2] : -1;
+            v_row = v_next;
+            v_next = there ? entry * p.c.vs[0] + w.hk * p.c.vs[1] + row * p.c.vs[2] : -1;
+            entry = entry_of(i + 1);
+            const unsigned word = __ballot_sync(kAll, hole);
+            if (lane == 0) reinterpret_cast<uint32_t *>(smem + C::OFF_BAD)[((seen + i) & 7) * 8 + 1 + (tid >> 5)] = word;
+        };
+        // fills: K(0), K(1), V(0), K(2), V(1) .. V(n - 1), NH halves each; two tiles:
+        // K(0), V(0), K(1), V(1) ..
+        int i = 0;                                             // the next block of K
+#pragma unroll 1
+        for (int g = 0; g < 2 * n && ok; ++g) {
+            const bool k = TWO ? (g & 1) == 0 : g == 0 || ((g & 1) == 1 && g != 2 * n - 1);
+            if (k) look(i++);
+            // (V of the block before the last of K, or of the last where no K follows)
+            const int64_t mine = k ? k_row : TWO || g == 2 * n - 1 ? v_next : v_row;
+#pragma unroll 1
+            for (int h = 0; h < C::NH; ++h) {
+                const uint32_t slot = fills % C::NS, use = fills / C::NS;
+                if (!ptx::mbar_try_wait(&bs->slot_empty[slot], (use + 1) & 1)) {
+                    tell_all();      // what has been copied may be what is waited for
+                    ok = wait_on(bs, p, &bs->slot_empty[slot], use + 1, 2);
+                }
+                ok = __all_sync(kAll, ok);
+                if (!ok) break;
+                const uint32_t dst = slots + slot * C::SLOT;
+                const uint16_t *src = bases[k ? 0 : 1] + h * 128 + chunk * 8;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int64_t row = __shfl_sync(kAll, mine, 2 * e + (lane >> 4));
+                    copy16(dst + e * 256 + (((chunk & 7) ^ ((row0 + 2 * e) & 7)) * 16), src + (row < 0 ? 0 : row), row >= 0);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                ++fills;
+                if (fills - told > 2) {
+                    asm volatile("cp.async.wait_group 2;" ::: "memory");
+                    tell();
+                }
+            }
+        }
+        seen += n;
+    }
+    tell_all();
+}
+
 // ------------------------------------------------------------------ kernel
-template <int D, bool TWO, bool I8>
-__global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel(const __grid_constant__ PfArgs a) {
-    using C = Cfg<D, TWO, I8>;
+template <int D, bool TWO, int LOAD>
+__global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kernel(const __grid_constant__ PfArgs a) {
+    using C = Cfg<D, TWO, LOAD>;
+    constexpr bool I8 = C::I8;
     const PrefillParams &p = a.p;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t base = ptx::smem_u32(smem);
@@ -459,7 +557,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
         ptx::prefetch_tmap(&a.tk);
         ptx::prefetch_tmap(&a.tv);
         for (int i = 0; i < C::NS; ++i) {
-            ptx::mbar_init(&bs->slot_full[i], I8 ? 128 : 2);
+            ptx::mbar_init(&bs->slot_full[i], C::MORE ? 128 : 2);
             ptx::mbar_init(&bs->raw_full[i], 1);
             ptx::mbar_init(&bs->slot_empty[i], C::QT);   // two tiles: by both issuers
         }
@@ -494,9 +592,10 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
     ptx::tc_fence_after();
     const uint32_t tmem = bs->tmem_base;
 
-    if (I8 && warp >= 8 && warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(I8 ? C::WIDEN_REGS : 24));
-        if constexpr (I8) widen_role<D, TWO>(a, bs, smem, w, has);
+    if (C::MORE && warp >= 8 && warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::MORE ? C::MORE_REGS : 24));
+        if constexpr (LOAD == kCodes) widen_role<D, TWO>(a, bs, smem, w, has);
+        if constexpr (LOAD == kCopies) copy_role<D, TWO>(a, bs, smem, w, has);
     } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == C::PRODUCER || warp == C::PRODUCER2) {
@@ -528,6 +627,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 }
                 ok = __shfl_sync(kAll, ok, 0);
             }
+            if (LOAD == kCopies) continue;      // (Q only)
             const auto tiled = [&](int j) { return !paged || (a.prow > 0 && (int64_t)(j + 1) * TT <= w.s.L); };
             const auto look = [&](int j) {
                 Rows r{{-1, -1, -1, -1}};
@@ -952,7 +1052,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, I8>::THREADS, 1) prefill_tc_kernel
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const volatile uint32_t *bad = reinterpret_cast<const volatile uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
-                const bool holes = p.c.block_table && bad[0] != 0;
+                const bool holes = p.c.block_table && (LOAD == kCopies ? bad[1] | bad[2] | bad[3] | bad[4] : bad[0]) != 0;
                 const bool masked = j >= plain || holes;
                 if (masked) {
                     // in place first: blocks that a row does not see whole are few, and
@@ -1067,7 +1167,7 @@ constexpr int kJoinParts = 4, kJoinThreads = 256;
 
 template <int D, bool TWO>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__ PfArgs a, int grid) {
-    using C = Cfg<D, TWO, false>;
+    using C = Cfg<D, TWO, kTma>;
     const PrefillParams &p = a.p;
     const int c = blockIdx.x + 1;
     const int S = C::QT * a.T;
@@ -1154,12 +1254,12 @@ int box_rows(const KvCache &c) {
     return c.page_size >= 8 && c.page_size < TT && TT % c.page_size == 0 ? c.page_size : 0;
 }
 
-template <int D, bool TWO, bool I8>
+template <int D, bool TWO, int LOAD>
 int launch(const PfArgs &a, int grid, cudaStream_t st) {
-    using C = Cfg<D, TWO, I8>;
-    if (cudaFuncSetAttribute(prefill_tc_kernel<D, TWO, I8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
+    using C = Cfg<D, TWO, LOAD>;
+    if (cudaFuncSetAttribute(prefill_tc_kernel<D, TWO, LOAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
         return -5;
-    prefill_tc_kernel<D, TWO, I8><<<grid, C::THREADS, C::SMEM, st>>>(a);
+    prefill_tc_kernel<D, TWO, LOAD><<<grid, C::THREADS, C::SMEM, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return -5;
     if (grid > 1) prefill_join_kernel<D, TWO><<<dim3(grid - 1, kJoinParts), kJoinThreads, 0, st>>>(a, grid);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
@@ -1168,11 +1268,11 @@ int launch(const PfArgs &a, int grid, cudaStream_t st) {
 }  // namespace
 
 // Two tiles hold 256 rows' partial sums at head_dim 128, one 128 at 256.
-int64_t prefill_slot_floats(int d) { return d == 128 ? Cfg<128, true, false>::SLOT_FLOATS : Cfg<256, false, false>::SLOT_FLOATS; }
+int64_t prefill_slot_floats(int d) { return d == 128 ? Cfg<128, true, kTma>::SLOT_FLOATS : Cfg<256, false, kTma>::SLOT_FLOATS; }
 
 bool prefill_tc_supports(const PrefillParams &p) {
     int64_t rs, rows, g[3];
-    return p.scale_log2 > 0.f && (!p.c.block_table || pool_rows(p.c, &rs, &rows, g));
+    return p.scale_log2 > 0.f && (!p.c.block_table || (!p.c.int8 && box_rows(p.c) < 64) || pool_rows(p.c, &rs, &rows, g));
 }
 
 int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
@@ -1196,9 +1296,12 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
     }
     const int es = p.c.int8 ? 1 : 2;                 // bytes a number
     const cuuint64_t width = (cuuint64_t)p.c.d * es / 2;
+    // Boxes of fewer than 64 rows: 4 x 65,520 positions of 8 heads, 64 rows, pages of
+    // 8 / 16 / 24 / 32 / 64 by TMA: 328 / 259 / 420 / 218 / 207 us (flat: 184).
+    const bool copies = p.c.block_table && !p.c.int8 && a.prow < 64;
     const void *caches[2] = {p.c.k, p.c.v};
     const int64_t *strides_of[2] = {p.c.ks, p.c.vs};
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 && !copies; ++i) {
         const int64_t *s = strides_of[i];
         if (a.prow > 0) {
             const int64_t rows = p.c.block_table ? p.c.page_size : p.c.cap;
@@ -1216,12 +1319,20 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
             if (!encode(i ? &a.gv : &a.gk, 2, caches[i], dims, strides, box, p.c.int8)) return -2;
         }
     }
-    if (a.prow == 0) { a.tk = a.gk; a.tv = a.gv; }   // (unused)
-    const bool two = p.n > a.T, i8 = p.c.int8;   // two tiles where the longest chunk fills more than one
-    a.p.per = max(1, TT / (two && p.c.d == 128 ? 2 * a.T : a.T));
-    if (p.c.d == 256) return i8 ? launch<256, false, true>(a, grid, st) : launch<256, false, false>(a, grid, st);
-    if (two) return i8 ? launch<128, true, true>(a, grid, st) : launch<128, true, false>(a, grid, st);
-    return i8 ? launch<128, false, true>(a, grid, st) : launch<128, false, false>(a, grid, st);
+    if (copies) a.tk = a.tv = a.tq;                 // (unused)
+    else if (a.prow == 0) { a.tk = a.gk; a.tv = a.gv; }   // (unused)
+    const bool two = p.c.d == 128 && p.n > a.T;   // where the longest chunk fills more than one tile
+    a.p.per = TT / (two ? 2 * a.T : a.T);
+    if (a.p.per < 1) a.p.per = 1;
+    const auto go = [&](auto load) {
+        constexpr int LOAD = decltype(load)::value;
+        return p.c.d == 256 ? launch<256, false, LOAD>(a, grid, st)
+               : two        ? launch<128, true, LOAD>(a, grid, st)
+                            : launch<128, false, LOAD>(a, grid, st);
+    };
+    if (p.c.int8) return go(std::integral_constant<int, kCodes>());
+    if (copies) return go(std::integral_constant<int, kCopies>());
+    return go(std::integral_constant<int, kTma>());
 }
 
 }  // namespace fd
