@@ -27,8 +27,7 @@
 //            overwrites S in TMEM in bf16.  A row's reference is its running
 //            maximum, refreshed, and O rescaled, only where a score passes it
 //            by 2^8.
-// Small pages (boxes of fewer than 64 rows) take too many TMA copies: warps 8-11
-// copy K and V by cp.async instead.
+// K and V of most paged calls do not come by TMA: warps 8-11 copy them by cp.async.
 // int8 caches: codes are copied into the second half of their slot, and
 // warps 8-11 widen them in place to bf16 (exactly); the position's K scale
 // multiplies its scores, its V scale its weights.  In both the producer is warp 12,
@@ -629,16 +628,26 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             }
             if (LOAD == kCopies) continue;      // (Q only)
             const auto tiled = [&](int j) { return !paged || (a.prow > 0 && (int64_t)(j + 1) * TT <= w.s.L); };
+            // entries of the runs of the next blocks, one a lane: a load's latency in
+            // every block held the copies up (2,048 tokens at d 256 over pages of 128:
+            // 2,095 -> 1,975 us)
+            int window = 0, window_end = -1, entry = -1;
             const auto look = [&](int j) {
                 Rows r{{-1, -1, -1, -1}};
                 if (!paged || j >= x.j1) return r;
                 const int32_t *table = p.c.block_table + (int64_t)w.b * p.c.max_pages;
                 const bool box = tiled(j);
                 const int pos = j * TT + lane * (box ? a.prow : 4);
-                if (box && lane >= TT / a.prow) return r;
                 int i = p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size, row = pos - i * p.c.page_size;
                 if (box) {
-                    const int32_t page = __ldg(table + i);
+                    const int runs = TT / a.prow;
+                    if (j >= window_end) {
+                        window = j;
+                        window_end = j + 32 / runs;
+                        entry = pos < w.s.L ? __ldg(table + i) : -1;
+                    }
+                    const int page = __shfl_sync(kAll, entry, ((j - window) * runs + lane) & 31);
+                    if (lane >= runs) return r;
                     r.y[0] = page < p.c.lead ? page : -1;
                     r.y[1] = row;
                     return r;
@@ -1254,6 +1263,18 @@ int box_rows(const KvCache &c) {
     return c.page_size >= 8 && c.page_size < TT && TT % c.page_size == 0 ? c.page_size : 0;
 }
 
+// Two tiles of queries share the blocks where the longest chunk fills more than one.
+bool two_tiles(const PrefillParams &p) { return p.c.d == 128 && p.n > TT / p.g; }
+
+// Pages whose K and V are copied by cp.async and not by TMA.  us, by TMA / copied (32
+// heads of 8; rows of one head 2 KB apart, 4 KB at d 256):
+//   one tile, 4 x 16 tokens, 65,520 positions, pages of 8: 328 / 186, 16: 259 / 189,
+//     24: 420 / 188, 32: 218 / 188, 64: 201 / 184, 128: 197 / 183
+//   d 256, 2,048 tokens, 32,768 positions, pages of 64: 2,095 / 1,848, 128: 1,973 / 1,847
+//   two tiles, 2,048 tokens, 32,768 positions, pages of 16: 927 / 902, 64: 770 / 900,
+//     128: 768 / 903
+bool copied(const PrefillParams &p) { return p.c.block_table && !p.c.int8 && (!two_tiles(p) || box_rows(p.c) < 64); }
+
 template <int D, bool TWO, int LOAD>
 int launch(const PfArgs &a, int grid, cudaStream_t st) {
     using C = Cfg<D, TWO, LOAD>;
@@ -1272,7 +1293,7 @@ int64_t prefill_slot_floats(int d) { return d == 128 ? Cfg<128, true, kTma>::SLO
 
 bool prefill_tc_supports(const PrefillParams &p) {
     int64_t rs, rows, g[3];
-    return p.scale_log2 > 0.f && (!p.c.block_table || (!p.c.int8 && box_rows(p.c) < 64) || pool_rows(p.c, &rs, &rows, g));
+    return p.scale_log2 > 0.f && (!p.c.block_table || copied(p) || pool_rows(p.c, &rs, &rows, g));
 }
 
 int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
@@ -1296,9 +1317,7 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
     }
     const int es = p.c.int8 ? 1 : 2;                 // bytes a number
     const cuuint64_t width = (cuuint64_t)p.c.d * es / 2;
-    // Boxes of fewer than 64 rows: 4 x 65,520 positions of 8 heads, 64 rows, pages of
-    // 8 / 16 / 24 / 32 / 64 by TMA: 328 / 259 / 420 / 218 / 207 us (flat: 184).
-    const bool copies = p.c.block_table && !p.c.int8 && a.prow < 64;
+    const bool two = two_tiles(p), copies = copied(p);
     const void *caches[2] = {p.c.k, p.c.v};
     const int64_t *strides_of[2] = {p.c.ks, p.c.vs};
     for (int i = 0; i < 2 && !copies; ++i) {
@@ -1321,7 +1340,6 @@ int launch_prefill_tc(const PrefillParams &p, int grid, cudaStream_t st) {
     }
     if (copies) a.tk = a.tv = a.tq;                 // (unused)
     else if (a.prow == 0) { a.tk = a.gk; a.tv = a.gv; }   // (unused)
-    const bool two = p.c.d == 128 && p.n > a.T;   // where the longest chunk fills more than one tile
     a.p.per = TT / (two ? 2 * a.T : a.T);
     if (a.p.per < 1) a.p.per = 1;
     const auto go = [&](auto load) {
