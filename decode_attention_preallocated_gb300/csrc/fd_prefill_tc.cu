@@ -547,6 +547,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
     const uint32_t base = ptx::smem_u32(smem);
     Bars *bs = reinterpret_cast<Bars *>(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;");   // (the join waits for this kernel's end)
     if (base & 1023u) {   // the swizzled layouts want aligned buffers
         if (tid == 0) atomicOr(p.status, kDevTimeout);
         return;
@@ -1137,19 +1138,22 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             } else {
                 float *slot = a.slots + (2 * (int64_t)blockIdx.x + (x.j0 > 0 ? 0 : 1)) * C::SLOT_FLOATS;
                 const int r = t * TT + row;
-                if (TWO || group == 0) {
+                if (real && (TWO || group == 0)) {
                     slot[C::ROWS * D + r] = n > 0 && m != neg_inf() ? m * sc : neg_inf();
                     slot[C::ROWS * (D + 1) + r] = l;
                 }
                 if (n > 0) {
-                    float *dst = slot + (int64_t)r * D + c0;
+                    // eight columns of every row, then the next eight: a warp's stores
+                    // are one run
+                    float *dst = slot + c0 * C::ROWS + r * 8;
 #pragma unroll 1
                     for (int c = 0; c < C::OC; c += 32) {
                         float o[32];
                         ptx::tmem_ld32(o_at + c, o);
                         ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) store32(dst + c + e, reinterpret_cast<const uint32_t *>(o + e));
+                        for (int e = 0; e < 32; e += 8)
+                            if (real) store32(dst + (c + e) * C::ROWS, reinterpret_cast<const uint32_t *>(o + e));
                     }
                 }
             }
@@ -1172,7 +1176,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
 // blockIdx.x: a place between two blocks' shares.  If it cuts a segment's blocks
 // of positions, this place's part of the segment's rows (of kJoinParts) is
 // joined from the pieces, in order.
-constexpr int kJoinParts = 4, kJoinThreads = 256;
+constexpr int kJoinParts = 4, kJoinThreads = 256, kJoinAhead = 4;
 
 template <int D, bool TWO>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid_constant__ PfArgs a, int grid) {
@@ -1181,44 +1185,55 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
     const int c = blockIdx.x + 1;
     const int S = C::QT * a.T;
     const Total total = total_of(p, S, grid, false);
-    if (c >= total.G || total.units == 0) return;
-    const int u = total.start(c);
+    int first = 0, last = 0;
     Walk w;
-    w.seek(p, S, total, u, u);
-    const int all = w.blocks(p, S);
-    if (all == 0) return;
-    const int block0 = u - w.from;                          // unit of the first block
-    const int first = total.owner(block0), last = total.owner(block0 + all - 1);
+    if (c < total.G && total.units > 0) {
+        const int u = total.start(c);
+        w.seek(p, S, total, u, u);
+        const int all = w.blocks(p, S), block0 = u - w.from;   // unit of the first block
+        if (all > 0) {
+            first = total.owner(block0);
+            last = total.owner(block0 + all - 1);
+        }
+    }
+    // (every thread: the launch behind this one may count on the pieces' kernel)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c <= first || c > last) return;
     const int parts = (last - first) * kJoinParts, at = (c - first - 1) * kJoinParts + (int)blockIdx.y;
     const int r0 = C::ROWS * at / parts, r1 = C::ROWS * (at + 1) / parts;
     constexpr int PER = D / 8;
-    for (int e = r0 * PER + (int)threadIdx.x; e < r1 * PER; e += kJoinThreads) {
-        const int r = e / PER, d = (e % PER) * 8;
+    // a warp: eight rows of four runs of eight columns
+    for (int e = threadIdx.x; e < (r1 - r0 + 7) / 8 * 8 * PER; e += kJoinThreads) {
+        const int r = r0 + e / (8 * PER) * 8 + (e & 7), d = (e >> 3) % PER * 8;
         int token;
         int64_t off;
-        if (!row_at<C::QT>(a, w, r / TT, r % TT, token, off)) continue;
-        // the first piece is its block's second slot, the others their first
-        const float *s = a.slots + (2 * (int64_t)first + 1) * C::SLOT_FLOATS;
-        int64_t step = C::SLOT_FLOATS;
+        if (r >= r1 || !row_at<C::QT>(a, w, r / TT, r % TT, token, off)) continue;
         float top = neg_inf(), l = 0.f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 2
-        for (int k = first; k <= last; ++k) {
-            // (a piece that saw nothing for the row holds no O)
-            const float m = s[C::ROWS * D + r];
-            const float4 u = *reinterpret_cast<const float4 *>(s + (int64_t)r * D + d);
-            const float4 v = *reinterpret_cast<const float4 *>(s + (int64_t)r * D + d + 4);
-            const float more = s[C::ROWS * (D + 1) + r];
-            s += step;
-            step = 2 * C::SLOT_FLOATS;
-            const float now = fmaxf(top, m), f = now == neg_inf() ? 0.f : fast_exp2(top - now);
-            const bool any = m != neg_inf();
-            const float g = any ? fast_exp2(m - now) : 0.f;
-            const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-            top = now;
-            l = l * f + (any ? more * g : 0.f);
+        for (int k0 = first; k0 <= last; k0 += kJoinAhead) {
+            float m[kJoinAhead], more[kJoinAhead];
+            float4 y[kJoinAhead][2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = o[i] * f + (any ? y[i] * g : 0.f);
+            for (int i = 0; i < kJoinAhead; ++i) {
+                // the first piece is its block's second slot, the others their first
+                const int k = min(k0 + i, last);
+                const float *s = a.slots + (2 * (int64_t)k + (k == first)) * C::SLOT_FLOATS;
+                m[i] = s[C::ROWS * D + r];
+                more[i] = s[C::ROWS * (D + 1) + r];
+                y[i][0] = *reinterpret_cast<const float4 *>(s + d * C::ROWS + r * 8);
+                y[i][1] = *reinterpret_cast<const float4 *>(s + d * C::ROWS + r * 8 + 4);
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinAhead; ++i) {
+                // (a piece that saw nothing for the row holds no O)
+                const bool any = k0 + i <= last && m[i] != neg_inf();
+                const float now = any ? fmaxf(top, m[i]) : top, f = now == neg_inf() ? 0.f : fast_exp2(top - now);
+                const float g = any ? fast_exp2(m[i] - now) : 0.f;
+                const float x[8] = {y[i][0].x, y[i][0].y, y[i][0].z, y[i][0].w, y[i][1].x, y[i][1].y, y[i][1].z, y[i][1].w};
+                top = now;
+                l = l * f + (any ? more[i] * g : 0.f);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) o[z] = o[z] * f + (any ? x[z] * g : 0.f);
+            }
         }
         const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
         *reinterpret_cast<uint4 *>(p.out + off + d) =
@@ -1282,8 +1297,20 @@ int launch(const PfArgs &a, int grid, cudaStream_t st) {
         return -5;
     prefill_tc_kernel<D, TWO, LOAD><<<grid, C::THREADS, C::SMEM, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return -5;
-    if (grid > 1) prefill_join_kernel<D, TWO><<<dim3(grid - 1, kJoinParts), kJoinThreads, 0, st>>>(a, grid);
-    return cudaGetLastError() == cudaSuccess ? 0 : -5;
+    if (grid == 1) return 0;
+    // launched ahead: its blocks find their places while the last pieces are made
+    cudaLaunchAttribute ahead;
+    memset(&ahead, 0, sizeof ahead);
+    ahead.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    ahead.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(grid - 1, kJoinParts);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cfg.attrs = &ahead;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefill_join_kernel<D, TWO>, a, grid) == cudaSuccess ? 0 : -5;
 }
 
 }  // namespace
