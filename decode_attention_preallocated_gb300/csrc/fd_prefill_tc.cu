@@ -1210,12 +1210,13 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
         if (r >= r1 || !row_at<C::QT>(a, w, r / TT, r % TT, token, off)) continue;
         float top = neg_inf(), l = 0.f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int k0 = first; k0 <= last; k0 += kJoinAhead) {
-            float m[kJoinAhead], more[kJoinAhead];
-            float4 y[kJoinAhead][2];
+            float m[kJoinAhead] = {}, more[kJoinAhead] = {};
+            float4 y[kJoinAhead][2] = {};
 #pragma unroll
             for (int i = 0; i < kJoinAhead; ++i) {
                 // the first piece is its block's second slot, the others their first
-                const int k = min(k0 + i, last);
+                const int k = k0 + i;
+                if (k > last) continue;
                 const float *s = a.slots + (2 * (int64_t)k + (k == first)) * C::SLOT_FLOATS;
                 m[i] = s[C::ROWS * D + r];
                 more[i] = s[C::ROWS * (D + 1) + r];
