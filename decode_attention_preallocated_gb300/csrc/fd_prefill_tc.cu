@@ -954,26 +954,20 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
                         s[e + 3] = v.y;
                     }
                 };
-                // the row's maximum; columns 0 .. 63 stay in registers, 64 .. 127
-                // are read again below
+                // the row's maximum; columns 0 .. 63 stay in registers, 64 .. 127 are
+                // read again below (both loops stay loops: a block of 128 columns
+                // unrolled came from memory more often than from the instruction cache)
                 float s[64], h[32];
                 float top = neg_inf();
-#pragma unroll
-                for (int c = 64; c < C::NC; c += 32) {
-                    ptx::tmem_ld32(s_at + c, c == 64 ? s : s + 32);
-                    if (c == 96) {
-                        ptx::tmem_wait_ld();
-                        scale(s, 64);
-                        scale(s + 32, 96);
-                        top = most(s, most(s + 32, top));
-                    }
+#pragma unroll (I8 ? 1 : 2)
+                for (int c = C::NC - 64; c >= 0; c -= 64) {
+                    ptx::tmem_ld32(s_at + col0 + c, s);
+                    ptx::tmem_ld32(s_at + col0 + c + 32, s + 32);
+                    ptx::tmem_wait_ld();
+                    scale(s, c);
+                    scale(s + 32, c + 32);
+                    top = most(s, most(s + 32, top));
                 }
-                ptx::tmem_ld32(s_at + col0, s);
-                ptx::tmem_ld32(s_at + col0 + 32, s + 32);
-                ptx::tmem_wait_ld();
-                scale(s, 0);
-                scale(s + 32, 32);
-                top = most(s, most(s + 32, top));
                 if (!TWO) top = fmaxf(top, other(top));
                 if (!ok) return;
                 // a new reference where a score passes the old one by 2^8
@@ -1038,17 +1032,18 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
                     }
                     ptx::tmem_st16(s_at + (col0 + c) / 2, word);
                 };
-                weigh(s, 0);
-                if (C::NC == 128) ptx::tmem_ld32(s_at + 64, h);
-                weigh(s + 32, 32);
-                if (C::NC == 128) {
-                    ptx::tmem_wait_ld();
-                    ptx::tmem_ld32(s_at + 96, s);
-                    scale(h, 64);
-                    weigh(h, 64);
-                    ptx::tmem_wait_ld();
-                    scale(s, 96);
-                    weigh(s, 96);
+#pragma unroll (I8 ? 1 : 2)
+                for (int c = 0; c < C::NC; c += 64) {
+                    const bool more = c + 64 < C::NC;
+                    weigh(s, c);
+                    if (more) ptx::tmem_ld32(s_at + 64, s);
+                    weigh(s + 32, c + 32);
+                    if (more) {
+                        ptx::tmem_ld32(s_at + 96, s + 32);
+                        ptx::tmem_wait_ld();
+                        scale(s, 64);
+                        scale(s + 32, 96);
+                    }
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
