@@ -543,12 +543,18 @@ int fd_append(const fd_tensor *k_new, const fd_tensor *v_new, const int32_t *new
  * FD_DEV_BAD_LENGTH is set where a length or new length is out of range;
  * FD_DEV_BAD_INDEX where the entry of a page below L_b names none, whose
  * positions nobody sees.
- *   opts->kernel: FD_KERNEL_AUTO, FD_KERNEL_TC (the tcgen05 kernel: flat
- *     caches, and pools whose three outer strides are multiples of the
- *     smallest, itself at least d, and the same for K and V; else
- *     FD_ERR_UNSUPPORTED) or FD_KERNEL_SIMT (warp-level matrix instructions,
- *     every layout).  opts->num_ctas: 0, or the number of thread blocks that
- *     share the work of the tcgen05 kernel.
+ *   An int8 position whose K or V scale is NaN makes NaN of the rows that see it.
+ *   opts->kernel: FD_KERNEL_AUTO; FD_KERNEL_TC (the tcgen05 kernel; scale > 0,
+ *     q and a flat cache of strides that a tensor map can describe, and
+ *     B * Hkv * tiles * blocks below 2^31, where a tile is 128 / (Hq / Hkv) tokens of
+ *     n and a block 128 positions of cap + n.  Pools of int8, or of bf16 at d = 128
+ *     where n is more than one tile and page_size 64 or a multiple of 128, must also have the same
+ *     strides for K and V, the outer three multiples of the smallest, itself at
+ *     least d.  FD_ERR_UNSUPPORTED otherwise); or FD_KERNEL_SIMT (warp-level matrix
+ *     instructions, every call), which AUTO falls back to.
+ *   opts->num_ctas: 0, or the number of thread blocks that share the work of the
+ *     tcgen05 kernel.  opts->wait_limit_us bounds its waits; one that runs out sets
+ *     FD_DEV_INTERNAL, and the outputs are then undefined.
  * Long contexts of few rows are split over thread blocks, which takes
  * fd_prefill_scratch_bytes(num_ctas, d) bytes of the workspace's room for split
  * partials (num_ctas 0: of an automatic launch on the current device; see
