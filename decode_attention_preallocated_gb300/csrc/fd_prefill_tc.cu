@@ -9,8 +9,9 @@
 // Work.  Segments (sequence, kv head, tiles) follow one another in units of 128
 // positions: a charge for its start and end, then its blocks of positions (a
 // bound on them that sums in closed form).  The grid's blocks, one an SM, take
-// equal consecutive shares of the units.  A segment that is cut leaves partial sums in the workspace, which a
-// second launch joins in the order of the pieces.
+// equal consecutive shares of the units.  A segment that is cut leaves partial sums
+// in the workspace, which a second launch, set out ahead, joins in the order of the
+// pieces.
 //
 // Roles in a block:
 //   warps 8, 11  TMA producers: Q of a segment, then K and V tiles of 128 positions
@@ -28,10 +29,26 @@
 //            maximum, refreshed, and O rescaled, only where a score passes it
 //            by 2^8.
 // K and V of most paged calls do not come by TMA: warps 8-11 copy them by cp.async.
-// int8 caches: codes are copied into the second half of their slot, and
+// int8 caches: codes are copied by TMA into the second half of their slot, and
 // warps 8-11 widen them in place to bf16 (exactly); the position's K scale
 // multiplies its scores, its V scale its weights.  In both the producer is warp 12,
 // the issuers 13 and 14.
+//
+// Bounds and times (us; 32 heads of 8 at head_dim 128, rates of a 6,787 GB/s copy and a
+// 1,906 TFLOP/s product):
+//   2,048 tokens behind 30,720, pages of 64: 825, 1.3 PFLOP/s (floor 559).  Softmax and
+//     the matrix pipe take turns of a similar length; some of each shows.
+//   4 x 5 .. 16 tokens about 30,000 .. 65,536 positions: 149, 5.2 TB/s (floor 115): the
+//     memory; ends and the join take 15.
+//   8 prompts of 500 .. 4,096 tokens, 16 heads of 4, head_dim 256: 497, 0.7 PFLOP/s (floor
+//     182).  O fills half of TMEM, so one tile is held; its scores, softmax and products
+//     wait for one another, and two blocks in flight do not cover that (the matrix pipe is
+//     busy a third of the time).
+//   4 x 200 .. 512 tokens behind up to 8,000 int8 positions: 261, 0.42 PFLOP/s (floor 57):
+//     widening the codes and the scales of every score and weight.
+//   37 tokens behind 963, 8 heads of 2: 16.4: two launches of dependent steps.
+// Code is kept small: the roles' instructions together pass what the caches hold, and a
+// third less of them took prompts at d 256 from 640 to 503 us.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -86,6 +103,8 @@ struct Cfg {
                          OTHER_REGS = MORE ? 72 : 104;
     static_assert(256 * SOFTMAX_REGS + 128 * (MORE_REGS + OTHER_REGS) <= THREADS * LAUNCH_REGS, "registers of the launch");
     static constexpr int PRODUCER = MORE ? 12 : 8, PRODUCER2 = MORE ? -1 : 11, ISSUER = PRODUCER + 1;   // warps; issuers: two
+    // One tile by TMA is of a flat cache (copied()).
+    static constexpr bool PAGED = MORE || TWO;
     static constexpr int NH = D / 128, QT = TWO ? 2 : 1;
     static constexpr uint32_t BOX = TT * 128;        // 128 rows x 64 numbers
     static constexpr uint32_t SLOT = 2 * BOX;        // 128 rows x 128 numbers
@@ -608,7 +627,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
         struct Rows {
             int y[4];
         };
-        const bool paged = p.c.block_table != nullptr;
+        const bool paged = C::PAGED && p.c.block_table;
         for (bool more = has; more && ok; more = w.next(p, S)) {
             const Piece x = piece_of<C::QT>(a, w);
             if (x.j0 >= x.j1) continue;
@@ -1057,14 +1076,14 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const volatile uint32_t *bad = reinterpret_cast<const volatile uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
-                const bool holes = p.c.block_table && (LOAD == kCopies ? bad[1] | bad[2] | bad[3] | bad[4] : bad[0]) != 0;
+                const bool holes = C::PAGED && p.c.block_table && (LOAD == kCopies ? bad[1] | bad[2] | bad[3] | bad[4] : bad[0]) != 0;
                 const bool masked = j >= plain || holes;
                 if (masked) {
                     // in place first: blocks that a row does not see whole are few, and
                     // a second loop body would crowd the instruction caches
                     const uint32_t s_at = tmem + lanes + buf * 128 + col0;
                     const int pos0 = j * TT;
-                    const int at = p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
+                    const int at = C::PAGED && p.c.block_table ? pos0 : min(pos0, w.s.L - TT);   // position of column 0
 #pragma unroll 1
                     for (int c = 0; c < C::NC; c += 32) {
                         float s[32];
