@@ -129,8 +129,9 @@ struct Cfg {
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
 // ------------------------------------------------------------------ work
-// Blocks of positions that a segment's start and end are charged as.
-constexpr int kCharge = 2;
+// Blocks of positions that a segment's start and end are charged as (prompts at d 256
+// with 1, 2, 3, 4, 6: 520, 494, 478, 482, 496 us).
+constexpr int kCharge = 3;
 
 // What a launch's share of the work goes by: B sequences of L_b positions, fresh_b
 // of them new.
@@ -1124,8 +1125,16 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             const int c0 = TWO ? 0 : group * C::OC;
             if (x.whole()) {
                 const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-                const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.os[0] * 2) | (uintptr_t)(p.os[1] * 2) |
-                                    (uintptr_t)(p.os[2] * 2)) & 31) == 0;
+                // four neighbours trade their rows' runs of eight columns, so that they
+                // store 64 bytes of one row at a time (a row each, 32 bytes at a time:
+                // 7,000 cycles a segment at d 256, TRADED now)
+                uint16_t *at[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t where = reinterpret_cast<uint64_t>(real ? p.out + off + c0 : nullptr);
+                    const uint64_t theirs = __shfl_sync(kAll, where, (lane & ~3) + e);
+                    at[e] = theirs ? reinterpret_cast<uint16_t *>(theirs) + (lane & 3) * 8 : nullptr;
+                }
 #pragma unroll 1
                 for (int c = 0; c < C::OC; c += 32) {
                     float o[32];
@@ -1137,17 +1146,20 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         word[e] = n > 0 && inv != 0.f ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
-                    if (real) {
-                        uint16_t *dst = p.out + off + c0 + c;
-                        if (wide) {
-                            store32(dst, word);
-                            store32(dst + 16, word + 8);
-                        } else {
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4)
-                                *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(word[e], word[e + 1], word[e + 2], word[e + 3]);
+                    for (int by = 1; by < 4; by *= 2)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            if (e & (4 * by)) continue;
+                            uint32_t &lo = word[e], &hi = word[e + 4 * by];
+                            const uint32_t got = __shfl_xor_sync(kAll, lane & by ? lo : hi, by);
+                            (lane & by ? lo : hi) = got;
                         }
-                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (at[e])
+                            *reinterpret_cast<uint4 *>(at[e] + c) =
+                                make_uint4(word[4 * e], word[4 * e + 1], word[4 * e + 2], word[4 * e + 3]);
                 }
             } else {
                 float *slot = a.slots + (2 * (int64_t)blockIdx.x + (x.j0 > 0 ? 0 : 1)) * C::SLOT_FLOATS;
