@@ -14,6 +14,12 @@
 // do.  Those are ranked by counting how many are better than each.  The join
 // ranks what the slices left the same way, by scores in single precision widened
 // by what those may be off, and orders the few that remain by their exact scores.
+//
+// Times (us, floors by the copy rate): 4 beams of 32,000 fp32 words 12.3, of which the
+// read is 0.1: dependent steps of one slice (load, bound, read again, rank) and of the
+// join.  32 x 8 beams of 128,000 bf16 words, a fifth of them ended, 35 (floor 9.7): a block
+// streams for half its time, and spends the other half on its bound, the second look
+// and the ranking, with barriers between; four blocks an SM overlap the two only in part.
 #include <cuda_runtime.h>
 
 #include <math.h>

@@ -1126,8 +1126,8 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             if (x.whole()) {
                 const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
                 // four neighbours trade their rows' runs of eight columns, so that they
-                // store 64 bytes of one row at a time (a row each, 32 bytes at a time:
-                // 7,000 cycles a segment at d 256, TRADED now)
+                // store 64 bytes of one row at a time (a row each, 32 bytes at a time, made a
+                // segment's end 7,000 cycles at d 256; 6,300 so)
                 uint16_t *at[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

@@ -1,5 +1,19 @@
 // fd_rows.cu -- new rows into a bf16 or int8 cache, keys and queries rotated to
 // their positions on the way.
+//
+// A pair of values (a, b) at position p turns to (a cos - b sin, b cos + a sin) by the
+// table's row of p; an int8 row is codes rint(x / s) and s = max|x| / 127.  Every
+// number is read once and written once, so memory bounds long prompts and the launch
+// a single token.
+//
+// A thread block per token: its heads' loads are independent, eight (d 128) or sixteen
+// lanes take a head in runs of 16 bytes, and a row's maximum is one reduction over
+// them.  Loads of three heads set out together (8 prompts of 300 .. 2,048 tokens, 32
+// heads of 8, pages of 64: 54 us with three, 60 with two, 62 with four or six, which
+// hold more registers; 77 one after the other); loads that pass by L1 changed nothing.
+// That is 4.4 TB/s for 236 MB (floor 35 us): reads and writes of 256-byte rows of
+// many pages in turn.  4 prompts into an int8 cache at d 256: 22 us; one token of 64
+// sequences 4.1.
 #include <cuda_runtime.h>
 
 #include "fd_device.cuh"
