@@ -10,7 +10,8 @@
 // lanes take a head in runs of 16 bytes, and a row's maximum is one reduction over
 // them.  Loads of three heads set out together (8 prompts of 300 .. 2,048 tokens, 32
 // heads of 8, pages of 64: 54 us with three, 60 with two, 62 with four or six, which
-// hold more registers; 77 one after the other); loads that pass by L1 changed nothing.
+// hold more registers; 77 one after the other), and at most 80 registers let six blocks
+// share an SM (53; 50 with eight, whose spills cost a single token 1.5 of 4.1 us).
 // That is 4.4 TB/s for 236 MB (floor 35 us): reads and writes of 256-byte rows of
 // many pages in turn.  4 prompts into an int8 cache at d 256: 22 us; one token of 64
 // sequences 4.1.
@@ -25,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kBatch = 3;      // heads whose loads a thread has in flight
+constexpr int kBlocks = 6;     // blocks an SM holds at least
 
 __device__ __forceinline__ void write_length(const RowsParams &p, int b) {
     const int64_t raw = p.lengths[b], base = clamp_len(raw, p.c.cap);
@@ -85,7 +87,7 @@ __device__ __forceinline__ uint2 codes_of(const float *x, float s) {
 
 // One block per token: its heads of q, k and v, LANES threads a head.
 template <int LANES, bool INT8>
-__global__ void __launch_bounds__(kThreads) append_rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kThreads, kBlocks) append_rows_kernel(const __grid_constant__ RowsParams p) {
     constexpr int kSlots = kThreads / LANES;   // heads side by side
     const int b = (int)(blockIdx.x / (uint32_t)p.n), i = (int)(blockIdx.x % (uint32_t)p.n);
     const int64_t base = clamp_len(__ldg(p.lengths + b), p.c.cap);
