@@ -17,9 +17,11 @@
 //
 // Times (us, floors by the copy rate): 4 beams of 32,000 fp32 words 12.3, of which the
 // read is 0.1: dependent steps of one slice (load, bound, read again, rank) and of the
-// join.  32 x 8 beams of 128,000 bf16 words, a fifth of them ended, 35 (floor 9.7): a block
-// streams for half its time, and spends the other half on its bound, the second look
-// and the ranking, with barriers between; four blocks an SM overlap the two only in part.
+// join.  32 x 8 beams of 128,000 bf16 words, a fifth of them ended, 30.6 (floor 9.7): a block
+// streams for a third of that, and spends as long on its bound, the second look and the
+// ranking, with barriers between, and the last one on the join (7 us).  Four steps'
+// loads in flight and three blocks an SM: 30.6; two and four, three and four 31.3; six
+// and three 31.3; six or eight and two 36.
 #include <cuda_runtime.h>
 
 #include <math.h>
@@ -44,8 +46,8 @@ constexpr int kAgain = 64;         // threads' steps read again at a time
 constexpr int kKeep = 512;         // a longer list is cut before more comes
 constexpr int kList = kKeep + kAgain * kPer<uint16_t>;
 constexpr int kFinals = 512;       // the join's list
-constexpr int kAhead = 2;          // steps whose loads are in flight
-constexpr int kBlocks = 4;         // blocks an SM holds
+constexpr int kAhead = 4;          // steps whose loads are in flight
+constexpr int kBlocks = 3;         // blocks an SM holds
 constexpr unsigned kAll = 0xffffffffu;
 
 // Unsigned numbers in the order of the floats, both zeros alike; 0 for what is
@@ -538,12 +540,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_co
     if (tid == 0) p.tickets[b] = 0;
 }
 
-// Steps a slice: as many blocks as 152 SMs hold, rounded down where that gives each
-// row eight slices, else up (32 x 8 rows of 128,000 bf16 words, a fifth of them
-// ended: 35.1 us; 39.9, 37.3 and 37.3 in rounds of twice, three and four times as many).
+// Steps a slice: all rows in one round of the blocks that 152 SMs hold where there are
+// not more rows than blocks (32 x 8 rows of 128,000 bf16 words, a fifth of them ended:
+// 30.6 us; with more blocks than that 35 to 40), else a row a block; kSteps at most.
 int steps_of(int64_t rows, int64_t V, int step) {
     const int64_t steps = ceil_div(V, step), room = 152 * kBlocks;
-    const int64_t slices = rows * 8 <= room ? room / rows : ceil_div(room, rows);
+    const int64_t slices = rows <= room ? room / rows : 1;
     const int64_t each = ceil_div(steps, slices < steps ? slices : steps);
     return (int)(each < kSteps ? each : kSteps);
 }

@@ -13,7 +13,7 @@
 // hold more registers; 77 one after the other), and at most 80 registers let six blocks
 // share an SM (53; 50 with eight, whose spills cost a single token 1.5 of 4.1 us).
 // That is 4.4 TB/s for 236 MB (floor 35 us): reads and writes of 256-byte rows of
-// many pages in turn.  4 prompts into an int8 cache at d 256: 22 us; one token of 64
+// many pages in turn.  4 prompts into an int8 cache at d 256: 20 us; one token of 64
 // sequences 4.1.
 #include <cuda_runtime.h>
 

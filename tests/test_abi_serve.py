@@ -198,3 +198,11 @@ def test_the_binding_refuses_what_is_on_no_gpu():
     for call in (lambda: fd.append(None, x, c, c, lens), lambda: fd.prefill(3, c, c, lens), lambda: fd.beam_select(None, None, 3)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_prefill_scratch():
+    need = fd.lib().fd_prefill_scratch_bytes
+    for bad in ((-1, 128), (65536, 128), (1, 64), (1, 0)):
+        assert need(*bad) == 0
+    # two slots of 256 rows (128 at d 256) and their two numbers a block
+    assert need(3, 128) == 3 * 2 * 256 * 130 * 4 and need(3, 256) == 3 * 2 * 128 * 258 * 4
