@@ -15,13 +15,15 @@
 // ranks what the slices left the same way, by scores in single precision widened
 // by what those may be off, and orders the few that remain by their exact scores.
 //
-// Times (us, floors by the copy rate): 4 beams of 32,000 fp32 words 12.3, of which the
+// Times (us, floors by the copy rate): 4 beams of 32,000 fp32 words 13, of which the
 // read is 0.1: dependent steps of one slice (load, bound, read again, rank) and of the
-// join.  32 x 8 beams of 128,000 bf16 words, a fifth of them ended, 30.6 (floor 9.7): a block
+// join.  32 x 8 beams of 128,000 bf16 words, a fifth of them ended, 26 (floor 9.7): a block
 // streams for a third of that, and spends as long on its bound, the second look and the
-// ranking, with barriers between, and the last one on the join (7 us).  Four steps'
-// loads in flight and three blocks an SM: 30.6; two and four, three and four 31.3; six
-// and three 31.3; six or eight and two 36.
+// ranking, with barriers between, and the last one on the join.  Four steps' loads in
+// flight and three blocks an SM: 30.6, before the join took its candidates in another
+// order; two and four, three and four 31.3; six and three 31.3; six or eight and two 36.
+// More than kFinals candidates as good as the bound (all words alike) are picked one
+// by one: 4 x 8 beams of 50,000 words, 32 best, 620 us.
 #include <cuda_runtime.h>
 
 #include <math.h>
@@ -236,13 +238,16 @@ __device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm) {
     const int room = 2 * n, total = K * S * room;
     // the first of this thread's candidates set out before the sums are joined
     constexpr int kHeld = 8;
+    // (every warp takes some of every beam: the worst warp's largest bound them all, and
+    // beams lie far apart.  32 x 16 beams, 32 best, a warp by beams: 51 to 320 us, 25 to 37 so)
+    const int mine = (tid & 31) * kWarps + (tid >> 5);
     uint64_t held[kHeld];
     const auto key_at = [&](int e) {
         const int slice = e / room;
         return __ldcg(keys_of(head_of(p.scratch, first + slice, n)) + (e - slice * room));
     };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = tid + i * kThreads < total ? key_at(tid + i * kThreads) : 0;
+    for (int i = 0; i < kHeld; ++i) held[i] = mine + i * kThreads < total ? key_at(mine + i * kThreads) : 0;
     for (int k = tid >> 5; k < K; k += kWarps) {
         const int lane = tid & 31;
         float top = neg_inf(), sum = 0.f;
@@ -289,8 +294,8 @@ __device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm) {
     const auto visit = [&](auto f) {
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            if (tid + i * kThreads < total) one(tid + i * kThreads, held[i], f);
-        for (int e = tid + kHeld * kThreads; e < total; e += kThreads) one(e, key_at(e), f);
+            if (mine + i * kThreads < total) one(mine + i * kThreads, held[i], f);
+        for (int e = mine + kHeld * kThreads; e < total; e += kThreads) one(e, key_at(e), f);
     };
     float low = neg_inf();
     visit([&](int, uint64_t, float score, float off) { low = fmaxf(low, score - off); });
@@ -341,11 +346,21 @@ __device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm) {
                     ba = at;
                 }
             });
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const uint64_t s = __shfl_xor_sync(kAll, bs, o), at = __shfl_xor_sync(kAll, ba, o);
+                if (better(s, at, bs, ba)) {
+                    bs = s;
+                    ba = at;
+                }
+            }
             __syncthreads();
-            sm.finals.score[tid] = bs;
-            sm.finals.at[tid] = ba;
+            if ((tid & 31) == 0) {
+                sm.finals.score[tid >> 5] = bs;
+                sm.finals.at[tid >> 5] = ba;
+            }
             __syncthreads();
-            for (int j = 0; j < kThreads; ++j)
+            for (int j = 0; j < kWarps; ++j)
                 if (better(sm.finals.score[j], sm.finals.at[j], bs, ba)) {
                     bs = sm.finals.score[j];
                     ba = sm.finals.at[j];
@@ -542,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_co
 
 // Steps a slice: all rows in one round of the blocks that 152 SMs hold where there are
 // not more rows than blocks (32 x 8 rows of 128,000 bf16 words, a fifth of them ended:
-// 30.6 us; with more blocks than that 35 to 40), else a row a block; kSteps at most.
+// 30.6 us when tried; with more blocks than that 35 to 40), else a row a block;
+// kSteps at most.
 int steps_of(int64_t rows, int64_t V, int step) {
     const int64_t steps = ceil_div(V, step), room = 152 * kBlocks;
     const int64_t slices = rows <= room ? room / rows : 1;

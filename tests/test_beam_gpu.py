@@ -149,3 +149,15 @@ def test_captured_replayed_and_repeated():
             graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_beams_far_apart_and_many_alike(dtype):
+    # more candidates near the best than the join's list holds, in some beams only
+    rng = np.random.default_rng(11)
+    logits = torch.from_numpy(rng.standard_normal((3, 16, 10623))).float().cuda().to(dtype) * 2
+    scores = torch.from_numpy(rng.standard_normal((3, 16)) * 3).float().cuda()
+    check(logits, scores, 32)
+    check(torch.zeros(2, 8, 50000, device="cuda", dtype=dtype), torch.zeros(2, 8, device="cuda"), 32)
+    logits[1] = 0.5
+    check(logits, torch.where(scores > 0, 1.0, scores), 64)
