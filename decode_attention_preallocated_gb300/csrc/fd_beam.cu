@@ -43,6 +43,7 @@ template <typename T>
 constexpr int kPer = 32 / (int)sizeof(T);
 template <typename T>
 constexpr int kStep = kPer<T> * kThreads;
+constexpr int kLead = 7;           // words before a row in its first 16 bytes, at most
 constexpr int kSteps = 16;         // steps of a slice at most
 constexpr int kAgain = 64;         // threads' steps read again at a time
 constexpr int kKeep = 512;         // a longer list is cut before more comes
@@ -379,39 +380,27 @@ __device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm) {
     }
 }
 
-// This thread's words of one step: neighbours by wide loads, or every 256th.
-template <typename T, bool VEC>
+// This thread's words of one step, neighbours, of words begin .. end - 1 behind src
+// (16-byte aligned: begin is where in its first 16 bytes the row starts).
+template <typename T>
 struct Words {
-    static constexpr int PER = kPer<T>, N = VEC ? PER * (int)sizeof(T) / 16 : 1;
+    static constexpr int PER = kPer<T>, N = PER * (int)sizeof(T) / 16;
     uint4 w[N];
-    float x[VEC ? 1 : PER];
-    __device__ __forceinline__ void load(const T *src, int first, int end, int who) {
-        if (VEC) {
-            const int v = first + who * PER;
+    __device__ __forceinline__ static bool whole(int v, int begin, int end) { return v >= begin && v + PER <= end; }
+    __device__ __forceinline__ void load(const T *src, int first, int begin, int end, int who) {
+        const int v = first + who * PER;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (v + PER <= end) w[i] = ldg_stream(reinterpret_cast<const uint4 *>(src + v) + i);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                const int v = first + e * kThreads + who;
-                x[e] = v < end ? number(src + v) : neg_inf();
-            }
+        for (int i = 0; i < N; ++i) {
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (whole(v, begin, end)) w[i] = ldg_stream(reinterpret_cast<const uint4 *>(src + v) + i);
         }
     }
     __device__ __forceinline__ static float number(const T *at) {
         if constexpr (sizeof(T) == 4) return __ldg(at);
         else return __uint_as_float((uint32_t)__ldg(at) << 16);
     }
-    // As numbers; the row's last few one by one.
-    __device__ __forceinline__ void get(const T *src, int first, int end, int who, float *to) const {
-        if (!VEC) {
-#pragma unroll
-            for (int e = 0; e < PER; ++e) to[e] = x[e];
-            return;
-        }
+    // As numbers; the row's first and last few one by one.
+    __device__ __forceinline__ void get(const T *src, int first, int begin, int end, int who, float *to) const {
         const int v = first + who * PER;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -426,19 +415,15 @@ struct Words {
                 }
             }
         }
-        if (v + PER > end) {
+        if (!whole(v, begin, end)) {
 #pragma unroll
-            for (int e = 0; e < PER; ++e) to[e] = v + e < end ? number(src + v + e) : neg_inf();
+            for (int e = 0; e < PER; ++e) to[e] = v + e >= begin && v + e < end ? number(src + v + e) : neg_inf();
         }
-    }
-    __device__ __forceinline__ static uint32_t word(int first, int who, int e) {
-        return VEC ? first + who * PER + e : first + e * kThreads + who;
     }
 };
 
-// blockIdx.x: slice of a row (beam of a request).  VEC: rows are read 16 bytes at a
-// time.
-template <typename T, bool VEC>
+// blockIdx.x: slice of a row (beam of a request).
+template <typename T>
 __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_constant__ BeamArgs a) {
     constexpr int PER = kPer<T>, STEP = kStep<T>;
     __shared__ Room sm;
@@ -455,13 +440,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_co
             keys[i] = slice == 0 && i == 0 ? (uint64_t)order_of(0.f) << 32 | (uint32_t)~p.end_token : 0ull;
     } else {
         const T *src = static_cast<const T *>(p.logits) + b * p.ls[0] + k * p.ls[1];
+        // words are counted from the 16-byte boundary at or before the row
+        const int begin = (int)(reinterpret_cast<uintptr_t>(src) % 16 / sizeof(T)), end = begin + p.V;
+        src -= begin;
         const int first = slice * a.steps * STEP;
-        const int steps = min(a.steps, (p.V - first + STEP - 1) / STEP);
+        const int steps = min(a.steps, (end - first + STEP - 1) / STEP);   // (0 or less: it has no words)
         if (tid == 0) sm.count = sm.n_again = 0;
-        Words<T, VEC> next[kAhead];
+        Words<T> next[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
-            if (i < steps) next[i].load(src, first + i * STEP, p.V, tid);
+            if (i < steps) next[i].load(src, first + i * STEP, begin, end, tid);
         // of this thread's words so far: maximum, and sum of exp(x - top) (two halves)
         float top = neg_inf();
         uint64_t sum = 0;
@@ -471,8 +459,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_co
                 const int i = i0 + q, at = first + i * STEP;
                 if (i >= steps) break;
                 float x[PER];
-                next[q].get(src, at, p.V, tid, x);
-                if (i + kAhead < steps) next[q].load(src, at + kAhead * STEP, p.V, tid);
+                next[q].get(src, at, begin, end, tid, x);
+                if (i + kAhead < steps) next[q].load(src, at + kAhead * STEP, begin, end, tid);
                 float most = x[0];
 #pragma unroll
                 for (int e = 1; e < PER; ++e) most = fmaxf(most, x[e]);
@@ -521,14 +509,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_co
             if (tid < kAgain && i0 + tid < sm.n_again) {
                 const int e0 = sm.again[i0 + tid], at = first + e0 / kThreads * STEP, who = e0 % kThreads;
                 float x[PER];
-                next[0].load(src, at, p.V, who);
-                next[0].get(src, at, p.V, who, x);
+                next[0].load(src, at, begin, end, who);
+                next[0].get(src, at, begin, end, who, x);
 #pragma unroll
                 for (int e = 0; e < PER; ++e)
                     if (x[e] >= edge) {
                         const int to = atomicAdd(&sm.count, 1);
                         over |= to >= kKeep;
-                        sm.list[to] = (uint64_t)order_of(x[e]) << 32 | (uint32_t)~Words<T, VEC>::word(at, who, e);
+                        sm.list[to] = (uint64_t)order_of(x[e]) << 32 | ~(uint32_t)(at + who * PER + e - begin);
                     }
             }
             if (__syncthreads_or(over)) cut_long(sm, sm.count, n);
@@ -566,34 +554,30 @@ int steps_of(int64_t rows, int64_t V, int step) {
     return (int)(each < kSteps ? each : kSteps);
 }
 
-template <typename T>
-void launch(const BeamArgs &a, bool vec, unsigned blocks, cudaStream_t st) {
-    if (vec) beam_kernel<T, true><<<blocks, kThreads, 0, st>>>(a);
-    else beam_kernel<T, false><<<blocks, kThreads, 0, st>>>(a);
-}
-
 }  // namespace
 
 int64_t beam_scratch_bytes(int64_t B, int K, int64_t V, int n_out) {
-    // (the more slices of the two types')
+    // (the most slices of the two types', of rows that start anywhere)
     int64_t slices = 0;
-    for (const int step : {kStep<float>, kStep<uint16_t>}) {
-        const int64_t n = ceil_div(V, (int64_t)steps_of(B * K, V, step) * step);
-        slices = n > slices ? n : slices;
-    }
+    for (const int step : {kStep<float>, kStep<uint16_t>})
+        for (const int64_t words : {V, V + kLead}) {
+            const int64_t n = ceil_div(words, (int64_t)steps_of(B * K, words, step) * step);
+            slices = n > slices ? n : slices;
+        }
     return B * K * slices * (int64_t)(8 + 16 * n_out);
 }
 
 int launch_beam_select(const BeamParams &p, cudaStream_t st) {
     const int64_t rows = (int64_t)p.B * p.K;
-    const int step = p.bf16 ? kStep<uint16_t> : kStep<float>, steps = steps_of(rows, p.V, step);
-    BeamArgs a{p, (int32_t)ceil_div(p.V, (int64_t)steps * step), steps};
+    const int es = p.bf16 ? 2 : 4, step = p.bf16 ? kStep<uint16_t> : kStep<float>;
+    const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.ls[0] * es % 16 == 0 && p.ls[1] * es % 16 == 0;
+    const int64_t words = aligned ? p.V : (int64_t)p.V + kLead;
+    const int steps = steps_of(rows, words, step);
+    const BeamArgs a{p, (int32_t)ceil_div(words, (int64_t)steps * step), steps};
     const int64_t blocks = rows * a.slices;
     if (blocks >= (int64_t)1 << 31) return -2;
-    const int es = p.bf16 ? 2 : 4;
-    const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.ls[0] * es % 16 == 0 && p.ls[1] * es % 16 == 0;
-    if (p.bf16) launch<uint16_t>(a, vec, (unsigned)blocks, st);
-    else launch<float>(a, vec, (unsigned)blocks, st);
+    if (p.bf16) beam_kernel<uint16_t><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    else beam_kernel<float><<<(unsigned)blocks, kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
