@@ -48,6 +48,7 @@ constexpr int kSteps = 16;         // steps of a slice at most
 constexpr int kAgain = 64;         // threads' steps read again at a time
 constexpr int kKeep = 512;         // a longer list is cut before more comes
 constexpr int kList = kKeep + kAgain * kPer<uint16_t>;
+constexpr int kHeld = 8;           // of the join's candidates, those that a thread holds
 constexpr int kFinals = 512;       // the join's list
 constexpr int kAhead = 4;          // steps whose loads are in flight
 constexpr int kBlocks = 3;         // blocks an SM holds
@@ -238,7 +239,6 @@ __device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm) {
     const int64_t first = (int64_t)b * K * S;
     const int room = 2 * n, total = K * S * room;
     // the first of this thread's candidates set out before the sums are joined
-    constexpr int kHeld = 8;
     // (every warp takes some of every beam: the worst warp's largest bound them all, and
     // beams lie far apart.  32 x 16 beams, 32 best, a warp by beams: 51 to 320 us, 25 to 37 so)
     const int mine = (tid & 31) * kWarps + (tid >> 5);
@@ -546,10 +546,14 @@ __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_co
 // Steps a slice: all rows in one round of the blocks that 152 SMs hold where there are
 // not more rows than blocks (32 x 8 rows of 128,000 bf16 words, a fifth of them ended:
 // 30.6 us when tried; with more blocks than that 35 to 40), else a row a block;
-// kSteps at most.
-int steps_of(int64_t rows, int64_t V, int step) {
+// kSteps at most.  And no more slices than leave the join what its threads hold (each
+// slice leaves up to `per` keys of a request): 8 beams of 128,000 words, 16 best, 20.5
+// us against 41 in single steps; 128 beams of 32,000, 64 best, 92 against 192; half of
+// that changed nothing.
+int steps_of(int64_t rows, int64_t V, int step, int per) {
     const int64_t steps = ceil_div(V, step), room = 152 * kBlocks;
-    const int64_t slices = rows <= room ? room / rows : 1;
+    const int64_t most = kHeld * kThreads / per < 1 ? 1 : kHeld * kThreads / per;
+    const int64_t full = rows <= room ? room / rows : 1, slices = full < most ? full : most;
     const int64_t each = ceil_div(steps, slices < steps ? slices : steps);
     return (int)(each < kSteps ? each : kSteps);
 }
@@ -561,7 +565,7 @@ int64_t beam_scratch_bytes(int64_t B, int K, int64_t V, int n_out) {
     int64_t slices = 0;
     for (const int step : {kStep<float>, kStep<uint16_t>})
         for (const int64_t words : {V, V + kLead}) {
-            const int64_t n = ceil_div(words, (int64_t)steps_of(B * K, words, step) * step);
+            const int64_t n = ceil_div(words, (int64_t)steps_of(B * K, words, step, K * 2 * n_out) * step);
             slices = n > slices ? n : slices;
         }
     return B * K * slices * (int64_t)(8 + 16 * n_out);
@@ -572,7 +576,7 @@ int launch_beam_select(const BeamParams &p, cudaStream_t st) {
     const int es = p.bf16 ? 2 : 4, step = p.bf16 ? kStep<uint16_t> : kStep<float>;
     const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.ls[0] * es % 16 == 0 && p.ls[1] * es % 16 == 0;
     const int64_t words = aligned ? p.V : (int64_t)p.V + kLead;
-    const int steps = steps_of(rows, words, step);
+    const int steps = steps_of(rows, words, step, p.K * 2 * p.n_out);
     const BeamArgs a{p, (int32_t)ceil_div(words, (int64_t)steps * step), steps};
     const int64_t blocks = rows * a.slices;
     if (blocks >= (int64_t)1 << 31) return -2;
