@@ -537,7 +537,7 @@ int fd_append(const fd_tensor *k_new, const fd_tensor *v_new, const int32_t *new
  *     stride 1; overlaps nothing else.
  *   n >= 1, Hq / Hkv up to 128; any number of rows.
  *   Scores and sums are fp32; a softmax weight (for int8 times its position's v
- *     scale) is rounded to bf16, i.e. by up to 2^-9 of itself.  Positions below
+ *     scale) is rounded to bf16, i.e. by up to 2^-8 of itself.  Positions below
  *     L_b must hold finite values where some row does not see them; those at
  *     or past L_b and pages past it are never read.
  * FD_DEV_BAD_LENGTH is set where a length or new length is out of range;
@@ -547,11 +547,12 @@ int fd_append(const fd_tensor *k_new, const fd_tensor *v_new, const int32_t *new
  *   opts->kernel: FD_KERNEL_AUTO; FD_KERNEL_TC (the tcgen05 kernel; scale > 0,
  *     q and a flat cache of strides that a tensor map can describe, and
  *     B * Hkv * tiles * blocks below 2^31, where a tile is 128 / (Hq / Hkv) tokens of
- *     n and a block 128 positions of cap + n.  Pools of int8, or of bf16 at d = 128
- *     where n is more than one tile and page_size 64 or a multiple of 128, must also have the same
- *     strides for K and V, the outer three multiples of the smallest, itself at
- *     least d.  FD_ERR_UNSUPPORTED otherwise); or FD_KERNEL_SIMT (warp-level matrix
- *     instructions, every call), which AUTO falls back to.
+ *     n and a block 128 positions of cap + n.  K and V of int8 pools must also have
+ *     the same strides, the outer three multiples of the smallest, itself at least
+ *     d, and so must those of bf16 pools at d = 128 with n more than one tile and a
+ *     page_size of 64 or a multiple of 128; FD_ERR_UNSUPPORTED otherwise), or
+ *     FD_KERNEL_SIMT (warp-level matrix instructions, every call), which AUTO falls
+ *     back to.
  *   opts->num_ctas: 0, or the number of thread blocks that share the work of the
  *     tcgen05 kernel.  opts->wait_limit_us bounds its waits; one that runs out sets
  *     FD_DEV_INTERNAL, and the outputs are then undefined.
