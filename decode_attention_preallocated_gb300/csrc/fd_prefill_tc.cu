@@ -1251,8 +1251,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
             }
 #pragma unroll
             for (int i = 0; i < kJoinAhead; ++i) {
-                // (a piece that saw nothing for the row holds no O)
-                const bool any = k0 + i <= last && m[i] != neg_inf();
+                // (a piece that saw nothing for the row holds no O; one whose scores
+                // were all NaN has a sum that is, and no maximum)
+                const bool any = k0 + i <= last && (m[i] != neg_inf() || more[i] != more[i]);
                 const float now = any ? fmaxf(top, m[i]) : top, f = now == neg_inf() ? 0.f : fast_exp2(top - now);
                 const float g = any ? fast_exp2(m[i] - now) : 0.f;
                 const float x[8] = {y[i][0].x, y[i][0].y, y[i][0].z, y[i][0].w, y[i][1].x, y[i][1].y, y[i][1].z, y[i][1].w};
