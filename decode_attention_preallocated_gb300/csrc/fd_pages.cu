@@ -704,8 +704,9 @@ int launch_pages_reorder(const Books &k, const int32_t *src, int32_t *ticket, cu
     int shift = kReorderShift;
     while (shift > 0 && ((int64_t)k.B << shift) > kReorderRows) --shift;
     const int bytes = (k.B << shift) * 4;
-    if (bytes > 48 * 1024 && cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  kReorderRows * 4) != cudaSuccess)
+    // (48 KB need no leave, the kernel's own few bytes among them)
+    if (bytes + 128 > 48 * 1024 && cudaFuncSetAttribute(reorder_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                        kReorderRows * 4) != cudaSuccess)
         return -5;
     const unsigned blocks = (unsigned)ceil_div(k.max_pages, 1 << shift);
     reorder_kernel<<<blocks, kReorderThreads, bytes, st>>>(k, src, shift, ticket);
