@@ -308,6 +308,12 @@ __device__ __forceinline__ bool wait_on(Bars *bs, const PrefillParams &p, uint64
     return true;
 }
 
+// The same for a whole warp, which goes on or gives up as one: what follows (votes,
+// loads from TMEM) wants all of its lanes.
+__device__ __forceinline__ bool warp_wait_on(Bars *bs, const PrefillParams &p, uint64_t *bar, uint32_t parity, int site) {
+    return __all_sync(kAll, wait_on(bs, p, bar, parity, site));
+}
+
 // Waits for a block's own copies or MMAs, which must end even when another role
 // gave up.
 __device__ __forceinline__ void drain_on(uint64_t *bar, uint32_t parity) {
@@ -435,8 +441,7 @@ __device__ __forceinline__ void widen_role(const PfArgs &a, Bars *bs, unsigned c
             }
             for (int h = 0; h < C::NH; ++h) {
                 const uint32_t slot = fills % C::NS, use = fills / C::NS;
-                ok = wait_on(bs, p, &bs->raw_full[slot], use, 11);
-                ok = __all_sync(kAll, ok);
+                ok = warp_wait_on(bs, p, &bs->raw_full[slot], use, 11);
                 if (!ok) break;
                 ++fills;
                 unsigned char *const box = smem + C::OFF_SLOTS + slot * C::SLOT;
@@ -922,7 +927,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             room[group * 128 + row] = mine;
             ptx::tc_fence_before();
             ptx::mbar_arrive(&bs->cross);
-            ok = ok && wait_on(bs, p, &bs->cross, crossed, 6);
+            ok = ok && warp_wait_on(bs, p, &bs->cross, crossed, 6);
             ptx::tc_fence_after();
             ++crossed;
             return room[(group ^ 1) * 128 + row];
@@ -1006,7 +1011,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
                         // two tiles: the last PV into O was issued before these
                         // scores, whose end was waited for; one tile: after
                         if (!TWO) {
-                            ok = wait_on(bs, p, &bs->pv_done[ctr & 1], (ctr - 2) >> 1, 9);
+                            ok = warp_wait_on(bs, p, &bs->pv_done[ctr & 1], (ctr - 2) >> 1, 9);
                             if (!ok) return;
                             ptx::tc_fence_after();
                         }
@@ -1073,7 +1078,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             for (int j = x.j0; j < x.hi[t] && ok; ++j) {
                 const uint32_t buf = TWO ? t : ctr & 1, use = TWO ? ctr : ctr >> 1;
                 ++ctr;
-                ok = wait_on(bs, p, &bs->s_full[buf], use, 7);
+                ok = warp_wait_on(bs, p, &bs->s_full[buf], use, 7);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const volatile uint32_t *bad = reinterpret_cast<const volatile uint32_t *>(smem + C::OFF_BAD) + ((seen + j - x.j0) & 7) * 8;
@@ -1118,7 +1123,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             if (!TWO) l += other(l);
             if (!ok) break;
             if (n > 0) {
-                ok = wait_on(bs, p, &bs->o_full[t], pieces++, 8);
+                ok = warp_wait_on(bs, p, &bs->o_full[t], pieces++, 8);
                 if (!ok) break;
                 ptx::tc_fence_after();
             }
