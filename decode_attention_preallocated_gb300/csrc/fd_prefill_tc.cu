@@ -87,6 +87,7 @@ struct Bars {
     uint32_t tmem_base;
     int abort_flag;          // the site of the first wait that ran out, else 0
     int turn;                // held by the issuer whose tile's MMAs go out
+    uint32_t armed[2];       // two producers: slots that each has set out, at its end
 };
 
 // How K and V come: whole slots by TMA; int8 codes by TMA, widened; by cp.async.
@@ -315,9 +316,8 @@ __device__ __forceinline__ bool warp_wait_on(Bars *bs, const PrefillParams &p, u
 }
 
 // Waits for a block's own copies or MMAs, which must end even when another role
-// gave up.
-__device__ __forceinline__ void drain_on(uint64_t *bar, uint32_t parity) {
-    const uint64_t t0 = ptx::globaltimer_ns();
+// gave up; until kDrainNs after t0.
+__device__ __forceinline__ void drain_on(uint64_t *bar, uint32_t parity, uint64_t t0) {
     for (uint32_t n = 1; !ptx::mbar_try_wait(bar, parity); ++n)
         if ((n & 63) == 0 && ptx::globaltimer_ns() - t0 > kDrainNs) return;
 }
@@ -778,13 +778,24 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             }
             seen += x.j1 - x.j0;
         }
-        // every copy that was issued lands before the block exits
-        if (lane == 0)
+        // every copy that was issued lands before the block exits.  Two producers: one
+        // that gave up may be up to a ring behind; it arrives, without bytes, for the
+        // slots that the other has set out, whose phases would not end otherwise
+        if (C::PRODUCER2 >= 0) {
+            if (lane == 0) bs->armed[part] = fills;
+            __syncwarp();
+            asm volatile("barrier.sync 1, 64;" ::: "memory");
+            const uint32_t most = max(fills, bs->armed[part ^ 1]);
+            for (; fills < most; ++fills)
+                if (lane == 0) ptx::mbar_arrive(&bs->slot_full[fills % C::NS]);
+        }
+        if (lane == 0) {
+            const uint64_t t0 = ptx::globaltimer_ns();
             for (uint32_t i = fills > C::NS ? fills - C::NS : 0; i < fills; ++i)
-                drain_on(I8 ? &bs->raw_full[i % C::NS] : &bs->slot_full[i % C::NS], (i / C::NS) & 1);
-        if (lane == 0)
+                drain_on(I8 ? &bs->raw_full[i % C::NS] : &bs->slot_full[i % C::NS], (i / C::NS) & 1, t0);
             for (int t = 0; t < C::QT; ++t)
-                if (loads[t] > 0) drain_on(&bs->q_full[t], (loads[t] - 1) & 1);
+                if (loads[t] > 0) drain_on(&bs->q_full[t], (loads[t] - 1) & 1, t0);
+        }
     } else if (warp == C::ISSUER || warp == C::ISSUER + 1) {
         // --------------------------------------------------------- issuers
         if (lane == 0) {
@@ -907,7 +918,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             }
             // every MMA that was issued ends before the block exits
             ptx::mma_commit(&bs->drain[me]);
-            drain_on(&bs->drain[me], 0);
+            drain_on(&bs->drain[me], 0, ptx::globaltimer_ns());
         }
     }
     } else {
