@@ -22,6 +22,10 @@
 // ranking, with barriers between, and the last one on the join.  Four steps' loads in
 // flight and three blocks an SM: 30.6, before the join took its candidates in another
 // order; two and four, three and four 31.3; six and three 31.3; six or eight and two 36.
+// Rows that start off a 16-byte boundary bring 16 bytes more a thread and shift their words
+// out of them: 32 x 16 beams of 10,623 bf16 words 26.8 us (fp32 29.7; two steps ahead, 27.1
+// and 29.5 with three, 28.0 and 28.9 with four).  Words counted from the boundary took 26.0
+// and 27.7, but rows of the same logits then had other sums, and did not tie.
 // More than kFinals candidates as good as the bound (all words alike) are picked one
 // by one: 4 x 8 beams of 50,000 words, 32 best, 620 us.
 #include <cuda_runtime.h>
@@ -43,14 +47,13 @@ template <typename T>
 constexpr int kPer = 32 / (int)sizeof(T);
 template <typename T>
 constexpr int kStep = kPer<T> * kThreads;
-constexpr int kLead = 7;           // words before a row in its first 16 bytes, at most
 constexpr int kSteps = 16;         // steps of a slice at most
 constexpr int kAgain = 64;         // threads' steps read again at a time
 constexpr int kKeep = 512;         // a longer list is cut before more comes
 constexpr int kList = kKeep + kAgain * kPer<uint16_t>;
 constexpr int kHeld = 8;           // of the join's candidates, those that a thread holds
 constexpr int kFinals = 512;       // the join's list
-constexpr int kAhead = 4;          // steps whose loads are in flight
+constexpr int kAhead = 4, kAheadOdd = 2;   // steps whose loads are in flight (rows on 16-byte boundaries, others)
 constexpr int kBlocks = 3;         // blocks an SM holds
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -380,50 +383,75 @@ __device__ __noinline__ void join(const BeamArgs &a, int b, Room &sm) {
     }
 }
 
-// This thread's words of one step, neighbours, of words begin .. end - 1 behind src
-// (16-byte aligned: begin is where in its first 16 bytes the row starts).
-template <typename T>
+// This thread's words of one step: neighbours, the same of every row wherever it starts
+// (rows of the same numbers then have the same sums, and tie).  ODD: base is the 16-byte
+// boundary at or before the row, `off` words before it, and one load more brings what the
+// words are shifted out of.
+template <typename T, bool ODD>
 struct Words {
-    static constexpr int PER = kPer<T>, N = PER * (int)sizeof(T) / 16;
-    uint4 w[N];
-    __device__ __forceinline__ static bool whole(int v, int begin, int end) { return v >= begin && v + PER <= end; }
-    __device__ __forceinline__ void load(const T *src, int first, int begin, int end, int who) {
-        const int v = first + who * PER;
+    static constexpr int PER = kPer<T>, N = PER * (int)sizeof(T) / 16, EACH = 16 / (int)sizeof(T);
+    uint4 w[N + ODD];
+    // Every load lies in the row.
+    __device__ __forceinline__ static bool whole(int v, int off, int end) {
+        return ODD ? v >= off && v + PER + EACH - off <= end : v + PER <= end;
+    }
+    __device__ __forceinline__ void load(const T *base, int off, int end, int v) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N + ODD; ++i) {
             w[i] = make_uint4(0, 0, 0, 0);
-            if (whole(v, begin, end)) w[i] = ldg_stream(reinterpret_cast<const uint4 *>(src + v) + i);
+            if (whole(v, off, end)) w[i] = ldg_stream(reinterpret_cast<const uint4 *>(base + v) + i);
         }
     }
     __device__ __forceinline__ static float number(const T *at) {
         if constexpr (sizeof(T) == 4) return __ldg(at);
         else return __uint_as_float((uint32_t)__ldg(at) << 16);
     }
-    // As numbers; the row's first and last few one by one.
-    __device__ __forceinline__ void get(const T *src, int first, int begin, int end, int who, float *to) const {
-        const int v = first + who * PER;
+    // Words v .. v + PER - 1 as numbers; the row's first and last few one by one.
+    __device__ __forceinline__ void get(const T *base, int off, int end, int v, float *to) const {
+        constexpr int U = 4 * N;
+        uint32_t u[4 * (N + ODD)];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+        for (int i = 0; i < N + ODD; ++i) {
+            u[4 * i] = w[i].x;
+            u[4 * i + 1] = w[i].y;
+            u[4 * i + 2] = w[i].z;
+            u[4 * i + 3] = w[i].w;
+        }
+        if constexpr (ODD) {
+            // by two, by one and by half a 32-bit word
+            const int half = sizeof(T) == 4 ? 2 * off : off;
+            if (half & 4) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (sizeof(T) == 4) {
-                    to[i * 4 + e] = __uint_as_float(u[e]);
-                } else {
-                    to[i * 8 + 2 * e] = bf16lo(u[e]);
-                    to[i * 8 + 2 * e + 1] = bf16hi(u[e]);
-                }
+                for (int e = 0; e < U + 2; ++e) u[e] = u[e + 2];
+            }
+            if (half & 2) {
+#pragma unroll
+                for (int e = 0; e < U + 1; ++e) u[e] = u[e + 1];
+            }
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int e = 0; e < U; ++e) u[e] = __funnelshift_r(u[e], u[e + 1], (half & 1) * 16);
             }
         }
-        if (!whole(v, begin, end)) {
 #pragma unroll
-            for (int e = 0; e < PER; ++e) to[e] = v + e >= begin && v + e < end ? number(src + v + e) : neg_inf();
+        for (int e = 0; e < U; ++e) {
+            if (sizeof(T) == 4) {
+                to[e] = __uint_as_float(u[e]);
+            } else {
+                to[2 * e] = bf16lo(u[e]);
+                to[2 * e + 1] = bf16hi(u[e]);
+            }
+        }
+        if (!whole(v, off, end)) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) to[e] = v + e < end ? number(base + off + v + e) : neg_inf();
         }
     }
 };
 
-// blockIdx.x: slice of a row (beam of a request).
-template <typename T>
+// blockIdx.x: slice of a row (beam of a request).  ODD: some row starts off a 16-byte
+// boundary.
+template <typename T, bool ODD>
 __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_constant__ BeamArgs a) {
     constexpr int PER = kPer<T>, STEP = kStep<T>;
     __shared__ Room sm;
@@ -439,28 +467,28 @@ __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_co
         for (int i = tid; i < 2 * n; i += kThreads)
             keys[i] = slice == 0 && i == 0 ? (uint64_t)order_of(0.f) << 32 | (uint32_t)~p.end_token : 0ull;
     } else {
-        const T *src = static_cast<const T *>(p.logits) + b * p.ls[0] + k * p.ls[1];
-        // words are counted from the 16-byte boundary at or before the row
-        const int begin = (int)(reinterpret_cast<uintptr_t>(src) % 16 / sizeof(T)), end = begin + p.V;
-        src -= begin;
+        constexpr int AHEAD = ODD ? kAheadOdd : kAhead;
+        const T *base = static_cast<const T *>(p.logits) + b * p.ls[0] + k * p.ls[1];
+        const int off = ODD ? (int)(reinterpret_cast<uintptr_t>(base) % 16 / sizeof(T)) : 0, end = p.V;
+        base -= off;
         const int first = slice * a.steps * STEP;
         const int steps = min(a.steps, (end - first + STEP - 1) / STEP);   // (0 or less: it has no words)
         if (tid == 0) sm.count = sm.n_again = 0;
-        Words<T> next[kAhead];
+        Words<T, ODD> next[AHEAD];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (i < steps) next[i].load(src, first + i * STEP, begin, end, tid);
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < steps) next[i].load(base, off, end, first + i * STEP + tid * PER);
         // of this thread's words so far: maximum, and sum of exp(x - top) (two halves)
         float top = neg_inf();
         uint64_t sum = 0;
-        for (int i0 = 0; i0 < steps; i0 += kAhead) {
+        for (int i0 = 0; i0 < steps; i0 += AHEAD) {
 #pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                const int i = i0 + q, at = first + i * STEP;
+            for (int q = 0; q < AHEAD; ++q) {
+                const int i = i0 + q, at = first + i * STEP + tid * PER;
                 if (i >= steps) break;
                 float x[PER];
-                next[q].get(src, at, begin, end, tid, x);
-                if (i + kAhead < steps) next[q].load(src, at + kAhead * STEP, begin, end, tid);
+                next[q].get(base, off, end, at, x);
+                if (i + AHEAD < steps) next[q].load(base, off, end, at + AHEAD * STEP);
                 float most = x[0];
 #pragma unroll
                 for (int e = 1; e < PER; ++e) most = fmaxf(most, x[e]);
@@ -507,16 +535,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) beam_kernel(const __grid_co
         for (int i0 = 0; i0 < sm.n_again; i0 += kAgain) {
             bool over = false;
             if (tid < kAgain && i0 + tid < sm.n_again) {
-                const int e0 = sm.again[i0 + tid], at = first + e0 / kThreads * STEP, who = e0 % kThreads;
+                const int e0 = sm.again[i0 + tid], at = first + e0 / kThreads * STEP + e0 % kThreads * PER;
                 float x[PER];
-                next[0].load(src, at, begin, end, who);
-                next[0].get(src, at, begin, end, who, x);
+                next[0].load(base, off, end, at);
+                next[0].get(base, off, end, at, x);
 #pragma unroll
                 for (int e = 0; e < PER; ++e)
                     if (x[e] >= edge) {
                         const int to = atomicAdd(&sm.count, 1);
                         over |= to >= kKeep;
-                        sm.list[to] = (uint64_t)order_of(x[e]) << 32 | ~(uint32_t)(at + who * PER + e - begin);
+                        sm.list[to] = (uint64_t)order_of(x[e]) << 32 | ~(uint32_t)(at + e);
                     }
             }
             if (__syncthreads_or(over)) cut_long(sm, sm.count, n);
@@ -561,27 +589,26 @@ int steps_of(int64_t rows, int64_t V, int step, int per) {
 }  // namespace
 
 int64_t beam_scratch_bytes(int64_t B, int K, int64_t V, int n_out) {
-    // (the most slices of the two types', of rows that start anywhere)
+    // (the more slices of the two types')
     int64_t slices = 0;
-    for (const int step : {kStep<float>, kStep<uint16_t>})
-        for (const int64_t words : {V, V + kLead}) {
-            const int64_t n = ceil_div(words, (int64_t)steps_of(B * K, words, step, K * 2 * n_out) * step);
-            slices = n > slices ? n : slices;
-        }
+    for (const int step : {kStep<float>, kStep<uint16_t>}) {
+        const int64_t n = ceil_div(V, (int64_t)steps_of(B * K, V, step, K * 2 * n_out) * step);
+        slices = n > slices ? n : slices;
+    }
     return B * K * slices * (int64_t)(8 + 16 * n_out);
 }
 
 int launch_beam_select(const BeamParams &p, cudaStream_t st) {
     const int64_t rows = (int64_t)p.B * p.K;
     const int es = p.bf16 ? 2 : 4, step = p.bf16 ? kStep<uint16_t> : kStep<float>;
-    const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && p.ls[0] * es % 16 == 0 && p.ls[1] * es % 16 == 0;
-    const int64_t words = aligned ? p.V : (int64_t)p.V + kLead;
-    const int steps = steps_of(rows, words, step, p.K * 2 * p.n_out);
-    const BeamArgs a{p, (int32_t)ceil_div(words, (int64_t)steps * step), steps};
+    const int steps = steps_of(rows, p.V, step, p.K * 2 * p.n_out);
+    const BeamArgs a{p, (int32_t)ceil_div(p.V, (int64_t)steps * step), steps};
     const int64_t blocks = rows * a.slices;
     if (blocks >= (int64_t)1 << 31) return -2;
-    if (p.bf16) beam_kernel<uint16_t><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-    else beam_kernel<float><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    const bool odd = reinterpret_cast<uintptr_t>(p.logits) % 16 || (p.B > 1 && p.ls[0] * es % 16) || (p.K > 1 && p.ls[1] * es % 16);
+    const auto kernel = p.bf16 ? (odd ? beam_kernel<uint16_t, true> : beam_kernel<uint16_t, false>)
+                               : (odd ? beam_kernel<float, true> : beam_kernel<float, false>);
+    kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
