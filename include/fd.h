@@ -571,7 +571,9 @@ int fd_prefill(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_
  * One step of a beam search: the n_out best of a request's K beams times V
  * words.  logits [B, K, V] (bf16 or fp32, innermost stride 1), scores fp32
  * [B, K] (contiguous; the beams' sums of log-probabilities so far; -inf: no
- * beam).  With lse = log sum exp of a beam's logits, rounded to fp32, word v of
+ * beam).  With lse = log sum exp of a beam's logits as an fp32 number (off by at
+ * most half a step of its own and 2^-15, by less than 2^-20 beside the half step on
+ * logits of every spread measured; the same for beams of the same logits), word v of
  * beam k scores scores[b,k] + (logit - lse), compared exactly; higher scores
  * win, equal ones go to the lower beam, then the lower word.
  *   finished: NULL, or device int32 [B, K]: a beam whose entry is not 0 has
