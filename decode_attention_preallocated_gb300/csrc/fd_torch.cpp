@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
+#include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -40,7 +41,7 @@ struct {
 } fd;
 PyObject *workspaces;   // {(device, stream): Workspace}
 PyObject *opts_for;     // (workspace, device, stream, segments, rows, ctas, num_ctas) -> fd_opts as bytes
-PyObject *empty_on;     // (shape, dtype, device, stream) -> tensor
+PyObject *empty_on;     // (shape, dtype, device, stream, zero) -> tensor
 PyObject *error;        // FdError(code, name)
 
 struct Raised {};       // a Python exception is set
@@ -140,10 +141,14 @@ bool truth(PyObject *o) {
     return x != 0;
 }
 
-// The output a call makes: on the current stream, or by fd.py on a given one.
-at::Tensor make(at::IntArrayRef shape, at::ScalarType type, PyObject *dtype, const Device &dev, PyObject *stream) {
-    if (stream == Py_None)
-        return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev.index)));
+// The output a call makes: on the current stream, or by fd.py on a given one; zeros where
+// the call may leave some of it as it was.
+at::Tensor make(at::IntArrayRef shape, at::ScalarType type, PyObject *dtype, const Device &dev, PyObject *stream,
+                bool zero = false) {
+    if (stream == Py_None) {
+        const auto kind = at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev.index));
+        return zero ? at::zeros(shape, kind) : at::empty(shape, kind);
+    }
     Ref size(PyTuple_New((Py_ssize_t)shape.size()));
     for (size_t i = 0; i < shape.size(); ++i) {
         PyObject *const x = PyLong_FromLongLong(shape[i]);
@@ -151,7 +156,7 @@ at::Tensor make(at::IntArrayRef shape, at::ScalarType type, PyObject *dtype, con
         PyTuple_SET_ITEM(size.p, (Py_ssize_t)i, x);
     }
     Ref index(PyLong_FromLong(dev.index));
-    Ref t(PyObject_CallFunctionObjArgs(empty_on, size.p, dtype, index.p, stream, nullptr));
+    Ref t(PyObject_CallFunctionObjArgs(empty_on, size.p, dtype, index.p, stream, zero ? Py_True : Py_False, nullptr));
     return tensor(t.p, "out");
 }
 
@@ -471,7 +476,8 @@ PyObject *append_rows(PyObject *const *a) {
     Ref to(a[7] == Py_None || a[8] != Py_None
                ? Py_NewRef(a[8])
                : THPVariable_Wrap(make(THPVariable_Unpack(a[7]).sizes(), at::kBFloat16,
-                                       reinterpret_cast<PyObject *>(torch::getTHPDtype(at::kBFloat16)), dev, a[14])));
+                                       reinterpret_cast<PyObject *>(torch::getTHPDtype(at::kBFloat16)), dev, a[14],
+                                       fresh != nullptr)));
     const Maybe q_out(to.p, "q_out", dev), rope(a[9], "rope", dev);
     const bool interleaved = truth(a[10]);
     const Maybe ks(a[11], "k_scale", dev), vs(a[12], "v_scale", dev);
@@ -499,7 +505,8 @@ PyObject *prefill(PyObject *const *a) {
     const Table t(a[9], B, dev);
     const int32_t num_ctas = whole(a[11]), kernel = whole(a[12]);
     const at::Tensor made = a[10] == Py_None
-                                ? make(tq.sizes(), at::kBFloat16, reinterpret_cast<PyObject *>(torch::getTHPDtype(at::kBFloat16)), dev, a[13])
+                                ? make(tq.sizes(), at::kBFloat16, reinterpret_cast<PyObject *>(torch::getTHPDtype(at::kBFloat16)), dev, a[13],
+                                       fresh != nullptr)
                                 : tensor(a[10], "out");
     const fd_tensor out = describe(made, dev);
     const int64_t room = [&] {

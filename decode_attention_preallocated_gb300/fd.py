@@ -658,10 +658,10 @@ def _pack(t: torch.Tensor) -> bytes:
     return _TENSOR.pack(t.data_ptr(), kind, n, *shape, *pad, *t.stride(), *pad)
 
 
-def _empty(shape, dtype, index, stream):
-    """New memory that belongs to the given stream."""
+def _empty(shape, dtype, index, stream, zero=False):
+    """New memory that belongs to the given stream, or zeros made on it."""
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+        return (torch.zeros if zero else torch.empty)(shape, dtype=dtype, device=torch.device("cuda", index))
 
 
 def _opts_for(workspace, index, stream, segments, rows, ctas, num_ctas) -> bytes:
@@ -752,8 +752,9 @@ def append(k_new, v_new, k_cache, v_cache, kv_lengths, new_lengths=None, lengths
     sines of each position's angles) turns the first r values of the keys, and of
     q [B, n, Hq, d] where given, to their positions: pairs (j, j + r/2), or
     interleaved (2j, 2j + 1).  lengths_out (int32 [B], may be kv_lengths) receives
-    the lengths with the new rows.  Returns q_out (made when not given, may be q
-    itself; padding rows are left as they were), or None without q."""
+    the lengths with the new rows.  Returns q_out (may be q itself; padding rows
+    are left as they were, and are zeros where the call makes it), or None without
+    q."""
     return _native.append(k_new, v_new, k_cache, v_cache, kv_lengths, new_lengths, lengths_out, q, q_out,
                           rope, interleaved, k_scale, v_scale, block_table, stream, workspace)
 
@@ -766,7 +767,7 @@ def prefill(q, k_cache, v_cache, kv_lengths, new_lengths=None, causal=True, scal
     (int32 [B]; None: n) of sequence b's kv_lengths[b] positions are its rows.
     Row i sees positions 0 .. kv_lengths[b] - new_lengths[b] + i when causal, else
     all of them.  Returns out [B, n, Hq, d] (bf16); rows past new_lengths[b] keep
-    what out held."""
+    what out held, and are zeros where the call makes it."""
     return _native.prefill(q, k_cache, v_cache, kv_lengths, new_lengths, causal, scale, k_scale, v_scale,
                            block_table, out, num_ctas, kernel, stream, workspace)
 
