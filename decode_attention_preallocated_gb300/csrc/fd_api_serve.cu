@@ -30,6 +30,11 @@ int check_opts(const fd_opts *o, bool any_kernel) {
     return o->ws ? FD_OK : FD_ERR_WORKSPACE;
 }
 
+bool overlap(const void *a, size_t bytes_a, const void *b, size_t bytes_b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + bytes_b && y < x + bytes_a;
+}
+
 int status_of(int rc) { return rc == 0 ? FD_OK : (rc == -2 ? FD_ERR_UNSUPPORTED : FD_ERR_CUDA); }
 
 int check_cache(const fd_tensor *k, const fd_tensor *v, const fd_tensor *ks, const fd_tensor *vs,
@@ -221,6 +226,13 @@ int fd_beam_select(const fd_tensor *logits, const float *scores, const int32_t *
     if (B > (1 << 24) || K > 128 || V >= (1 << 24) || n_out > 64) return FD_ERR_UNSUPPORTED;
     if (finished && (end_token < 0 || end_token >= V)) return FD_ERR_ARG;
     if ((rc = check_opts(opts, false))) return rc;
+    // a request's winners are written while its scores are read
+    const void *const outs[3] = {scores_out, beams_out, tokens_out};
+    const size_t out_bytes = (size_t)(B * n_out) * 4, in_bytes = (size_t)(B * K) * 4;
+    for (int i = 0; i < 3; ++i)
+        if (overlap(outs[i], out_bytes, scores, in_bytes) || overlap(outs[i], out_bytes, finished, in_bytes) ||
+            overlap(outs[i], out_bytes, outs[(i + 1) % 3], out_bytes))
+            return FD_ERR_ARG;
     fd_workspace *ws = opts->ws;
     if ((size_t)fd::beam_scratch_bytes(B, (int)K, V, n_out) > ws->partial_floats * 4 || B > ws->max_segments)
         return FD_ERR_WORKSPACE;

@@ -778,9 +778,9 @@ def beam_select(logits, scores, n_out, finished=None, end_token=None, out=None, 
     [B, K, V] (bf16 or fp32) of its K beams, whose log-probabilities so far are
     scores (fp32 [B, K]; -inf: no beam).  A beam whose entry in finished (int32
     [B, K]) is not 0 goes on by end_token alone, at no cost.  Returns (or fills
-    out =) scores fp32, rows b*K + k of the winners' beams (for
-    ``pages_reorder``) and tokens, int32, [B, n_out] each, best first; -inf, -1,
-    -1 where too few are left."""
+    out =, three tensors apart from the inputs) scores fp32, rows b*K + k of the
+    winners' beams (for ``pages_reorder``) and tokens, int32, [B, n_out] each, best
+    first; -inf, -1, -1 where too few are left."""
     return _native.beam_select(logits, scores, n_out, finished, end_token, out, stream, workspace)
 
 

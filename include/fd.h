@@ -583,7 +583,8 @@ int fd_prefill(const fd_tensor *q, const fd_tensor *k_cache, const fd_tensor *v_
  *     winners by falling score; beams_out holds the row b*K + k of the winner's
  *     beam, as fd_pages_reorder's src takes it.  Candidates of -inf or NaN
  *     score are none; where too few are left, the rest are -inf, -1 and -1.
- *     They overlap none of the inputs.
+ *     They overlap none of the inputs and not one another (FD_ERR_ARG where they do
+ *     scores, finished or one another).
  *   K <= 128, n_out <= 64, V < 2^24 (FD_ERR_UNSUPPORTED beyond).
  * opts supplies the stream and the workspace, whose room for split partials
  * holds fd_beam_scratch_bytes(B, K, V, n_out) bytes; opts->kernel must be
