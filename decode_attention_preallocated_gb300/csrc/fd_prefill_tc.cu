@@ -141,6 +141,9 @@ static_assert(sizeof(Bars) <= 512, "barrier block");
 // with 1, 2, 3, 4, 6: 520, 494, 478, 482, 496 us).
 constexpr int kCharge = 3;
 
+// Blocks that hold x positions (lengths go up to 2^31 - 1: sums with them are unsigned).
+__device__ __forceinline__ int blocks_of(int x) { return (int)(((unsigned)x + TT - 1) / TT); }
+
 // What a launch's share of the work goes by: B sequences of L_b positions, fresh_b
 // of them new.
 struct Seq {
@@ -159,13 +162,13 @@ __device__ __forceinline__ Seq seq_of(const PrefillParams &p, int b, int S, bool
 // positions before the chunk and (q + 1) S new ones, in at most ceil((q + 1) /
 // per) blocks, per = 128 / S whole segments a block (S = 256: 2 (q + 1) blocks).
 __device__ __forceinline__ int cost_of(const PrefillParams &p, const Seq &s, int S, int q) {
-    if (!p.causal) return kCharge + (s.L + TT - 1) / TT;
+    if (!p.causal) return kCharge + blocks_of(s.L);
     const int per = p.per;
-    return kCharge + (max(s.base(), 0) + TT - 1) / TT + (S > TT ? 2 * (q + 1) : (q + per) / per);
+    return kCharge + blocks_of(max(s.base(), 0)) + (S > TT ? 2 * (q + 1) : (q + per) / per);
 }
 __device__ __forceinline__ int units_of(const PrefillParams &p, const Seq &s, int S, int q) {
-    if (!p.causal) return q * (kCharge + (s.L + TT - 1) / TT);
-    const int before = q * (kCharge + (max(s.base(), 0) + TT - 1) / TT);
+    if (!p.causal) return q * (kCharge + blocks_of(s.L));
+    const int before = q * (kCharge + blocks_of(max(s.base(), 0)));
     if (S > TT) return before + q * (q + 1);
     const int per = p.per, m = q / per;
     return before + per * (m * (m + 1) / 2) + (q - m * per) * (m + 1);
@@ -274,7 +277,7 @@ struct Walk {
         if (!p.causal) return s.L;
         return max(0, min(s.L, s.base() + min(s.fresh, q * S + tokens)));
     }
-    __device__ __forceinline__ int blocks(const PrefillParams &p, int S) const { return (seen(p, S, S) + TT - 1) / TT; }
+    __device__ __forceinline__ int blocks(const PrefillParams &p, int S) const { return blocks_of(seen(p, S, S)); }
 };
 
 // The blocks of positions of the current segment that are this share's, and of
@@ -297,7 +300,7 @@ __device__ __forceinline__ Piece piece_of(const PfArgs &a, const Walk &w) {
     for (int t = 0; t < 2; ++t) {
         x.hi[t] = x.j0;
         if (t < QT && w.q * S + t * a.T < w.s.fresh)
-            x.hi[t] = max(x.j0, min(x.j1, (w.seen(p, S, (t + 1) * a.T) + TT - 1) / TT));
+            x.hi[t] = max(x.j0, min(x.j1, blocks_of(w.seen(p, S, (t + 1) * a.T))));
     }
     return x;
 }
@@ -415,8 +418,9 @@ __device__ __forceinline__ void widen_role(const PfArgs &a, Bars *bs, unsigned c
             return (p.c.block_table ? pos0 : min(pos0, w.s.L - TT)) + tid;
         };
         const auto lead_of = [&](int i) {
+            if (i >= n) return -1;
             const int pos = position(i);
-            if (i >= n || pos < 0 || pos >= w.s.L) return -1;
+            if (pos < 0 || pos >= w.s.L) return -1;
             if (!p.c.block_table) return w.b;
             const int e = __ldg(p.c.block_table + (int64_t)w.b * p.c.max_pages +
                                 (p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size));
@@ -514,8 +518,9 @@ __device__ __forceinline__ void copy_role(const PfArgs &a, Bars *bs, unsigned ch
         const int32_t *table = p.c.block_table + (int64_t)w.b * p.c.max_pages;
         // position tid of block i: its table entry, and where its row lies (elements)
         const auto entry_of = [&](int i) {
+            if (i >= n) return -1;
             const int pos = (x.j0 + i) * TT + tid;
-            return i < n && pos < w.s.L ? __ldg(table + (p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size)) : -1;
+            return pos < w.s.L ? __ldg(table + (p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size)) : -1;
         };
         int entry = entry_of(0);
         int64_t k_row = -1, v_row = -1, v_next = -1;
@@ -670,14 +675,15 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
                 if (!paged || j >= x.j1) return r;
                 const int32_t *table = p.c.block_table + (int64_t)w.b * p.c.max_pages;
                 const bool box = tiled(j);
-                const int pos = j * TT + lane * (box ? a.prow : 4);
-                int i = p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / p.c.page_size, row = pos - i * p.c.page_size;
+                // (the window's last runs may lie past 2^31)
+                const unsigned pos = (unsigned)(j * TT) + lane * (box ? a.prow : 4), page_size = p.c.page_size;
+                int i = (int)(p.c.page_shift >= 0 ? pos >> p.c.page_shift : pos / page_size), row = (int)(pos - i * page_size);
                 if (box) {
                     const int runs = TT / a.prow;
                     if (j >= window_end) {
                         window = j;
                         window_end = j + 32 / runs;
-                        entry = pos < w.s.L ? __ldg(table + i) : -1;
+                        entry = pos < (unsigned)w.s.L ? __ldg(table + i) : -1;
                     }
                     const int page = __shfl_sync(kAll, entry, ((j - window) * runs + lane) & 31);
                     if (lane >= runs) return r;
@@ -690,7 +696,7 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     at[e] = row;
-                    page[e] = pos + e < w.s.L ? __ldg(table + i) : -1;
+                    page[e] = pos + e < (unsigned)w.s.L ? __ldg(table + i) : -1;
                     if (++row == p.c.page_size) {
                         row = 0;
                         ++i;
@@ -966,8 +972,8 @@ __global__ void __launch_bounds__(Cfg<D, TWO, LOAD>::THREADS, 1) prefill_tc_kern
             if (x.j0 >= x.j1) continue;
             const int n = x.hi[t] - x.j0;
             const int first = w.q * S + t * a.T;            // the tile's first token
-            const int last = p.causal ? min(w.s.base() + token, w.s.L - 1) : w.s.L - 1;
-            const int all_see = p.causal ? min(w.s.base() + first, w.s.L - 1) : w.s.L - 1;
+            const int last = p.causal ? min(w.s.base() + min(token, w.s.fresh), w.s.L - 1) : w.s.L - 1;
+            const int all_see = p.causal ? min(w.s.base() + min(first, w.s.fresh), w.s.L - 1) : w.s.L - 1;
             float m = neg_inf(), l = 0.f;
             uint64_t sum0 = 0, sum1 = 0;
             // one block of positions, whose hidden scores are -inf already where some row
