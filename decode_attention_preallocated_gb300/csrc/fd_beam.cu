@@ -35,6 +35,7 @@
 #include <initializer_list>
 
 #include "fd_device.cuh"
+#include "fd_packed.cuh"
 #include "fd_serve.h"
 
 namespace fd {
@@ -72,27 +73,7 @@ __device__ __forceinline__ float float_of(uint32_t k) {
 constexpr uint32_t kLowest = 0x00800000u;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Two fp32 numbers in one 64-bit register, and operations on both.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
+// Both numbers of a pair times f.
 __device__ __forceinline__ uint64_t scaled(uint64_t a, float f) { return mul2(a, pair(f, f)); }
 
 // What a slice leaves behind: then room for 2 n_out keys (order of the logit,

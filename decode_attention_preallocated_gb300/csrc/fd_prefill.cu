@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "fd_device.cuh"
+#include "fd_packed.cuh"
 #include "fd_ptx.cuh"
 #include "fd_prefill.h"
 
@@ -38,12 +39,6 @@ __device__ __forceinline__ void ldsm_t(uint32_t *r, uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-// Four int8 codes -> four bf16 numbers.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
-    const float a = (float)(int8_t)(w & 0xff), b = (float)(int8_t)((w >> 8) & 0xff);
-    const float c = (float)(int8_t)((w >> 16) & 0xff), d = (float)(int8_t)(w >> 24);
-    return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
-}
 
 template <int D>
 struct Smem {

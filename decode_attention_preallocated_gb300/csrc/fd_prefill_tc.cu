@@ -63,6 +63,7 @@
 
 #include "fd_api.h"
 #include "fd_device.cuh"
+#include "fd_packed.cuh"
 #include "fd_prefill.h"
 #include "fd_ptx.cuh"
 #include "fd_tensor_map.h"
@@ -344,31 +345,6 @@ __device__ __forceinline__ bool take_turn(Bars *bs, const PrefillParams &p) {
 }
 __device__ __forceinline__ void give_turn(Bars *bs) { atomicExch(&bs->turn, 0); }
 
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t x) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ void store32(void *dst, const uint32_t *w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]),
                  "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -385,16 +361,6 @@ __device__ __forceinline__ bool row_at(const PfArgs &a, const Walk &w, int t, in
 }
 
 // ---------------------------------------------------------------- widening
-// Four int8 codes (the bytes of w) -> four bf16 numbers, exactly: with c's low
-// seven bits as the mantissa of 128 + (c & 127), less 128, or 256 where c's sign
-// bit is set.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
-    const uint32_t lo = __byte_perm(w, 0x43434343u, 0x4140), hi = __byte_perm(w, 0x43434343u, 0x4342);
-    uint2 r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(lo & 0xff7fff7fu), "r"(lo & 0xff80ff80u));
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(hi & 0xff7fff7fu), "r"(hi & 0xff80ff80u));
-    return r;
-}
 
 // One warp of the widening warpgroup: its 32 rows of every fill, in place.  A thread
 // takes 16 of a row's 128 codes, of every fourth row, all of them into registers
