@@ -3,9 +3,9 @@
 //
 // A word of beam k scores s_k + (x - lse_k), lse_k = m + log sum exp(x - m).  Within
 // a beam the order is that of the logits, so the logits are read once: a block
-// takes a slice of one beam's row into registers, leaves its maximum, its sum
-// of exponentials and its n_out best words (logit, lowest word first), and the
-// last block of a request joins the slices of all its beams.
+// takes a slice of one beam's row, leaves its maximum, its sum of exponentials and its
+// n_out best words (logit, lowest word first), and the last block of a request joins the
+// slices of all its beams.
 //
 // The best n of many: at least n of the threads' largest lie at or above a bound
 // that warp maxima give (bound_of), and few more numbers do.  A block streams its
@@ -14,10 +14,12 @@
 // do.  Those are ranked by counting how many are better than each.  The join
 // ranks what the slices left the same way, by scores in single precision widened
 // by what those may be off, and orders the few that remain by their exact scores.
+// lse is an fp32 number off by some 2^-20 (exponentials by the special function unit, sums
+// in fp32); its terms are added in an order that is the same for every row of a call.
 //
-// Times (us, floors by the copy rate): 4 beams of 32,000 fp32 words 13, of which the
+// Times (us, floors by the copy rate): 4 beams of 32,000 fp32 words 13.6, of which the
 // read is 0.1: dependent steps of one slice (load, bound, read again, rank) and of the
-// join.  32 x 8 beams of 128,000 bf16 words, a fifth of them ended, 26 (floor 9.7): a block
+// join.  32 x 8 beams of 128,000 bf16 words, a fifth of them ended, 26.7 (floor 7.8): a block
 // streams for a third of that, and spends as long on its bound, the second look and the
 // ranking, with barriers between, and the last one on the join.  Four steps' loads in
 // flight and three blocks an SM: 30.6, before the join took its candidates in another
@@ -27,7 +29,7 @@
 // and 29.5 with three, 28.0 and 28.9 with four).  Words counted from the boundary took 26.0
 // and 27.7, but rows of the same logits then had other sums, and did not tie.
 // More than kFinals candidates as good as the bound (all words alike) are picked one
-// by one: 4 x 8 beams of 50,000 words, 32 best, 620 us.
+// by one: 4 x 8 beams of 50,000 words, 32 best, 395 us.
 #include <cuda_runtime.h>
 
 #include <math.h>

@@ -8,9 +8,9 @@
 // keeps a running maximum and sum a row.
 //
 // It takes the calls that the tcgen05 kernel does not (a factor of 0 or below, strides
-// that no tensor map has): 4 x 5 .. 16 tokens about 30,000 .. 65,536 positions 7,675 us
-// (146 there), 2,048 tokens behind 30,720 9,653 us (818): its rows are not split over
-// positions, and K and V wait for the products of the tile before.
+// that no tensor map has): 4 x 5 .. 16 tokens about 30,000 .. 65,536 positions 7,675 us,
+// 2,048 tokens behind 30,720 9,653 us, 50 and 12 times what that one takes: its rows are not
+// split over positions, and K and V wait for the products of the tile before.
 #include <cuda_runtime.h>
 
 #include "fd_device.cuh"

@@ -43,17 +43,17 @@
 //
 // Bounds and times (us; 32 heads of 8 at head_dim 128, rates of a 6,787 GB/s copy and a
 // 1,906 TFLOP/s product):
-//   2,048 tokens behind 30,720, pages of 64: 813, 1.3 PFLOP/s (floor 559).  Softmax and
+//   2,048 tokens behind 30,720, pages of 64: 780, 1.4 PFLOP/s (floor 559).  Softmax and
 //     the matrix pipe take turns of a similar length; some of each shows.
-//   4 x 5 .. 16 tokens about 30,000 .. 65,536 positions: 143, 5.4 TB/s (floor 115): the
+//   4 x 5 .. 16 tokens about 30,000 .. 65,536 positions: 148, 5.9 TB/s (floor 129): the
 //     memory; ends and the join take 15.
-//   8 prompts of 500 .. 4,096 tokens, 16 heads of 4, head_dim 256: 467, 0.74 PFLOP/s (floor
-//     182).  O fills half of TMEM, so one tile is held; its scores, softmax and products
+//   8 prompts of 500 .. 4,096 tokens, 16 heads of 4, head_dim 256: 430, 1.1 PFLOP/s (floor
+//     254).  O fills half of TMEM, so one tile is held; its scores, softmax and products
 //     wait for one another, and two blocks in flight do not cover that (the matrix pipe is
 //     busy half of the time, and its operands fill what shared memory passes).
-//   4 x 200 .. 512 tokens behind up to 8,000 int8 positions: 248, 0.44 PFLOP/s (floor 57):
+//   4 x 200 .. 512 tokens behind up to 8,000 int8 positions: 239, 0.58 PFLOP/s (floor 73):
 //     widening the codes and the scales of every score and weight.
-//   37 tokens behind 963, 8 heads of 2: 16.4: two launches of dependent steps.
+//   37 tokens behind 963, 8 heads of 2: 16.5: two launches of dependent steps.
 // Code is kept small: the roles' instructions together pass what the caches hold, and a
 // third less of them took prompts at d 256 from 640 to 503 us.
 #include <cuda_runtime.h>

@@ -12,9 +12,9 @@
 // heads of 8, pages of 64: 54 us with three, 60 with two, 62 with four or six, which
 // hold more registers; 77 one after the other), and at most 80 registers let six blocks
 // share an SM (53; 50 with eight, whose spills cost a single token 1.5 of 4.1 us).
-// That is 4.4 TB/s for 236 MB (floor 35 us): reads and writes of 256-byte rows of
-// many pages in turn.  4 prompts into an int8 cache at d 256: 20 us; one token of 64
-// sequences 4.1.
+// That is 5.0 TB/s for 262 MB (52 us, floor 38.6): reads and writes of 256-byte rows of
+// many pages in turn.  4 prompts into an int8 cache at d 256: 20 us (floor 9.9); one token of
+// 64 sequences 4.3.
 #include <cuda_runtime.h>
 
 #include "fd_device.cuh"
