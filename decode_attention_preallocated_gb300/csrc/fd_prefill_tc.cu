@@ -1269,11 +1269,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const __grid
 // bf16 numbers, or pairs of int8 codes.
 bool encode(CUtensorMap *m, cuuint32_t rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
             const cuuint32_t *box, bool codes = false) {
-    const EncodeTiledFn fn = encode_fn();
     const cuuint32_t one[4] = {1, 1, 1, 1};
-    return fn && fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_tiled(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base),
+                        dims, strides, box, one, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
 }
 
 // The pool's rows as one strided 2-D array: the smallest stride, rows, and the

@@ -24,7 +24,36 @@ struct MapKey {
     cuuint32_t box[4];
 };
 
-inline EncodeTiledFn encode_fn();
+inline EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                                         cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<EncodeTiledFn>(ptr) : nullptr;
+    }();
+    return fn;
+}
+
+// The driver's call wants a context that is current to the host thread.  The runtime makes
+// the device's one so only with a thread's first call that needs it, which this may precede.
+inline CUresult encode_tiled(CUtensorMap *m, CUtensorMapDataType dtype, cuuint32_t rank, void *base,
+                             const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                             const cuuint32_t *estr, CUtensorMapSwizzle swizzle) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return CUDA_ERROR_NOT_SUPPORTED;
+    const auto call = [&] {
+        return fn(m, dtype, rank, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    CUresult r = call();
+    if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+        int device;
+        if (cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess) r = call();
+    }
+    return r;
+}
 
 inline CUresult encode_cached(CUtensorMap *m, CUtensorMapDataType dtype, cuuint32_t rank, void *base,
                        const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
@@ -53,11 +82,7 @@ inline CUresult encode_cached(CUtensorMap *m, CUtensorMapDataType dtype, cuuint3
                 return CUDA_SUCCESS;
             }
     }
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return CUDA_ERROR_NOT_SUPPORTED;
-    const CUresult r = fn(m, dtype, rank, base, dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = encode_tiled(m, dtype, rank, base, dims, strides, box, estr, swizzle);
     if (r == CUDA_SUCCESS) {
         std::lock_guard<std::mutex> lk(mu);
         keys[next] = k;
@@ -66,18 +91,6 @@ inline CUresult encode_cached(CUtensorMap *m, CUtensorMapDataType dtype, cuuint3
         if (used < kEntries) ++used;
     }
     return r;
-}
-
-inline EncodeTiledFn encode_fn() {
-    static const EncodeTiledFn fn = [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                                         cudaEnableDefault, &q) == cudaSuccess &&
-                        q == cudaDriverEntryPointSuccess;
-        return ok ? reinterpret_cast<EncodeTiledFn>(ptr) : nullptr;
-    }();
-    return fn;
 }
 
 }  // namespace fd
