@@ -246,6 +246,7 @@ int fd_beam_select(const fd_tensor *logits, const float *scores, const int32_t *
     p.scores_out = scores_out; p.beams_out = beams_out; p.tokens_out = tokens_out;
     p.scratch = reinterpret_cast<char *>(ws->partials);
     p.tickets = ws->counters;
+    const std::lock_guard<std::mutex> turn(ws->turn);
     return status_of(fd::launch_beam_select(p, static_cast<cudaStream_t>(opts->stream)));
 }
 
