@@ -766,7 +766,8 @@ def prefill(q, k_cache, v_cache, kv_lengths, new_lengths=None, causal=True, scal
     cache (as in ``append``) that holds them already: the newest new_lengths[b]
     (int32 [B]; None: n) of sequence b's kv_lengths[b] positions are its rows.
     Row i sees positions 0 .. kv_lengths[b] - new_lengths[b] + i when causal, else
-    all of them.  Returns out [B, n, Hq, d] (bf16); rows past new_lengths[b] keep
+    all of them; those below kv_lengths[b] that it does not see must hold finite
+    values.  Returns out [B, n, Hq, d] (bf16); rows past new_lengths[b] keep
     what out held, and are zeros where the call makes it."""
     return _native.prefill(q, k_cache, v_cache, kv_lengths, new_lengths, causal, scale, k_scale, v_scale,
                            block_table, out, num_ctas, kernel, stream, workspace)
