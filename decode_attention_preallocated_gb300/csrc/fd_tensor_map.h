@@ -36,8 +36,9 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// The driver's call wants a context that is current to the host thread.  The runtime makes
-// the device's one so only with a thread's first call that needs it, which this may precede.
+// cuTensorMapEncodeTiled wants a context that is current to the host thread.  The runtime
+// makes the device's one so only with a thread's first call that needs it, which this may
+// precede.
 inline CUresult encode_tiled(CUtensorMap *m, CUtensorMapDataType dtype, cuuint32_t rank, void *base,
                              const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
                              const cuuint32_t *estr, CUtensorMapSwizzle swizzle) {
